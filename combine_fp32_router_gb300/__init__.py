@@ -28,6 +28,9 @@ MOE_FWD_FUSED_COMBINE = 2
 MOE_FWD_GATHER_ROWS = 4
 MOE_WS_BACKWARD = 1
 MOE_WS_HOST_IO = 2
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F16 = 1
+MOE_DTYPE_F32 = 2
 MOE_FWD_NUM_EVENTS = 5
 MOE_BWD_NUM_EVENTS = 7
 
@@ -38,6 +41,9 @@ EXPORTS = ("moe_route_workspace_bytes", "moe_workspace_bytes", "moe_route_dispat
            "moe_forward_graph_destroy", "moe_forward_host", "moe_forward_host_pipelined",
            "moe_backward",
            "moe_route_dispatch_noalloc", "moe_route_dispatch_noalloc_get_error",
+           "moe_fp4_row_bytes", "moe_fp4_scale_bytes", "moe_quantize_rows_fp4",
+           "moe_dequantize_rows_fp4", "moe_quantize_weights_fp4", "moe_gemm_fp4",
+           "moe_gemm_fp4_get_error", "moe_few_workspace_bytes", "moe_forward_few_fp4",
            "moe_ep_first_expert", "moe_ep_plan", "moe_ep_return_plan", "moe_ep_copy_rows",
            "moe_expert_workspace_bytes", "moe_expert_forward", "moe_combine",
            "moe_probe_dram_read", "moe_get_error", "moe_set_wait_timeout_ns",
@@ -87,6 +93,24 @@ def _load():
     lib.moe_get_error.restype = i
     lib.moe_route_dispatch_noalloc_get_error.argtypes = [p]
     lib.moe_route_dispatch_noalloc_get_error.restype = i
+    lib.moe_fp4_row_bytes.argtypes = [i]
+    lib.moe_fp4_row_bytes.restype = i64
+    lib.moe_fp4_scale_bytes.argtypes = [i64, i]
+    lib.moe_fp4_scale_bytes.restype = sz
+    lib.moe_quantize_rows_fp4.argtypes = [p, i, i64, i, i64, p, p, p]
+    lib.moe_quantize_rows_fp4.restype = i
+    lib.moe_dequantize_rows_fp4.argtypes = [p, p, i, i64, i, i, p, p]
+    lib.moe_dequantize_rows_fp4.restype = i
+    lib.moe_quantize_weights_fp4.argtypes = [p, i, i, i, p, p, p]
+    lib.moe_quantize_weights_fp4.restype = i
+    lib.moe_gemm_fp4.argtypes = [p, p, i64, p, p, p, i, i, i, p, i, p]
+    lib.moe_gemm_fp4.restype = i
+    lib.moe_gemm_fp4_get_error.argtypes = [p]
+    lib.moe_gemm_fp4_get_error.restype = i
+    lib.moe_few_workspace_bytes.argtypes = [i64, i, i, i, i]
+    lib.moe_few_workspace_bytes.restype = sz
+    lib.moe_forward_few_fp4.argtypes = [p] * 9 + [i64, i, i, i, i, p, p, sz, p]
+    lib.moe_forward_few_fp4.restype = i
     lib.moe_ep_first_expert.argtypes = [i, i, i]
     lib.moe_ep_first_expert.restype = i
     lib.moe_ep_plan.argtypes = [p, i, i, i, i, i, p, p, p, p, p]
@@ -206,6 +230,123 @@ def moe_forward_fp8(x, logits, W1q, W3q, w1_scale, w3_scale, W2, k, out, ws, sta
                                 _ptr(w3_scale), _ptr(W2), T, d, E, k, d_ff, _ptr(out), _ptr(ws),
                                 _nbytes(ws), _events(stage_events), _stream(stream)),
            "moe_forward_fp8")
+
+
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
+           torch.float32: MOE_DTYPE_F32}
+
+
+def _dtype(dt):
+    if dt not in _DTYPES:
+        raise ValueError("dtype must be bfloat16, float16 or float32: got %s" % dt)
+    return _DTYPES[dt]
+
+
+def moe_fp4_row_bytes(cols):
+    """Bytes of the codes of one MXFP4 row of ``cols`` values."""
+    return int(_lib.moe_fp4_row_bytes(int(cols)))
+
+
+def moe_fp4_scale_bytes(rows, cols):
+    """Bytes of the scales of a rows x cols MXFP4 matrix."""
+    return int(_lib.moe_fp4_scale_bytes(int(rows), int(cols)))
+
+
+def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
+    """MXFP4 form of x [rows, cols] (bf16, fp16 or fp32; rows may have a stride): returns
+    (q [rows, moe_fp4_row_bytes(cols)] uint8, scales [moe_fp4_scale_bytes(rows, cols)] uint8),
+    written into ``q`` and ``scales`` where they are given (see include/moe.h)."""
+    rows, cols = x.shape
+    if cols > 1 and x.stride(1) != 1:
+        raise ValueError("the values of a row must be contiguous")
+    if q is None:
+        q = torch.empty(rows, moe_fp4_row_bytes(cols), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty(moe_fp4_scale_bytes(rows, cols), dtype=torch.uint8, device=x.device)
+    if _nbytes(q) < rows * moe_fp4_row_bytes(cols) or \
+            _nbytes(scales) < moe_fp4_scale_bytes(rows, cols):
+        raise ValueError("q or scales too small for %d x %d values" % (rows, cols))
+    _check(_lib.moe_quantize_rows_fp4(ctypes.c_void_p(x.data_ptr()), _dtype(x.dtype), rows, cols,
+                                      x.stride(0), _ptr(q), _ptr(scales), _stream(stream)),
+           "moe_quantize_rows_fp4")
+    return q, scales
+
+
+def moe_dequantize_rows_fp4(q, scales, cols, dtype=torch.bfloat16, stream=None):
+    """The values of one MXFP4 matrix (q [rows, bytes]) or of a group of them
+    (q [E, rows, bytes], scales [E, ...]) as a new tensor [..., rows, cols] of ``dtype``."""
+    groups = q.shape[0] if q.dim() == 3 else 1
+    rows = q.shape[-2]
+    if q.shape[-1] != moe_fp4_row_bytes(cols) or \
+            _nbytes(scales) < groups * moe_fp4_scale_bytes(rows, cols):
+        raise ValueError("q or scales do not hold rows of %d values" % cols)
+    out = torch.empty(*q.shape[:-1], cols, dtype=dtype, device=q.device)
+    _check(_lib.moe_dequantize_rows_fp4(_ptr(q), _ptr(scales), groups, rows, cols, _dtype(dtype),
+                                        _ptr(out), _stream(stream)), "moe_dequantize_rows_fp4")
+    return out
+
+
+def moe_quantize_weights_fp4(W, stream=None):
+    """MXFP4 form of expert weights W [E, K, N] bf16, quantised along K: returns
+    (Wq [E, N, moe_fp4_row_bytes(K)] uint8, scales [E, moe_fp4_scale_bytes(N, K)] uint8)."""
+    E, K, N = W.shape
+    if W.dtype != torch.bfloat16:
+        raise ValueError("W must be bfloat16: got %s" % W.dtype)
+    Wq = torch.empty(E, N, moe_fp4_row_bytes(K), dtype=torch.uint8, device=W.device)
+    sc = torch.empty(E, moe_fp4_scale_bytes(N, K), dtype=torch.uint8, device=W.device)
+    _check(_lib.moe_quantize_weights_fp4(_ptr(W), E, K, N, _ptr(Wq), _ptr(sc), _stream(stream)),
+           "moe_quantize_weights_fp4")
+    return Wq, sc
+
+
+def moe_gemm_fp4(aq, a_scales, bq, b_scales, out, K, counts=None, stream=None):
+    """out [rows, N] (bf16 or fp32) = the product over K of MXFP4 rows aq and weights
+    bq [E, N, bytes] (or [N, bytes]).  ``counts`` (int32 device tensor [E]): expert e's rows
+    start on a 128-row boundary after expert e - 1's; without it E is 1 (see include/moe.h)."""
+    rows, N = out.shape
+    E = bq.shape[0] if bq.dim() == 3 else 1
+    kb = moe_fp4_row_bytes(K)
+    if aq.shape[-1] != kb or bq.shape[-1] != kb or aq.shape[0] < rows or bq.shape[-2] != N:
+        raise ValueError("aq, bq and out do not fit one product over %d values" % K)
+    if _nbytes(a_scales) < moe_fp4_scale_bytes(rows, K) or \
+            _nbytes(b_scales) < E * moe_fp4_scale_bytes(N, K):
+        raise ValueError("a_scales or b_scales too small")
+    if counts is not None and (counts.dtype != torch.int32 or counts.numel() != E):
+        raise ValueError("counts must hold one int32 per expert")
+    _check(_lib.moe_gemm_fp4(_ptr(aq), _ptr(a_scales), rows, _ptr(counts), _ptr(bq),
+                             _ptr(b_scales), E, N, K, _ptr(out), _dtype(out.dtype),
+                             _stream(stream)), "moe_gemm_fp4")
+
+
+def moe_gemm_fp4_get_error(stream=None):
+    """Synchronise the stream; the first device-side problem that moe_gemm_fp4 recorded on the
+    current device since the last call (cleared by it)."""
+    return int(_lib.moe_gemm_fp4_get_error(_stream(stream)))
+
+
+def moe_few_workspace_bytes(T, d, E, k, d_ff):
+    return int(_lib.moe_few_workspace_bytes(T, d, E, k, d_ff))
+
+
+def moe_forward_few_fp4(x, logits, router, W1q, W3q, W2q, w1_scales, w3_scales, w2_scales, k, out,
+                        ws, stream=None):
+    """The whole layer for T <= 32 tokens on MXFP4 experts (moe_quantize_weights_fp4 of W1, W3
+    and W2) into ``out`` [T, d] bf16.  ``router`` [E, d] fp32: the logits [T, E] fp32 are
+    computed and written; None: they are read."""
+    T, d = x.shape
+    E, d_ff, kb = W1q.shape
+    if kb != d // 2 or W3q.shape != W1q.shape or tuple(W2q.shape) != (E, d, d_ff // 2) or \
+            tuple(logits.shape) != (T, E) or out.shape != x.shape or \
+            (router is not None and tuple(router.shape) != (E, d)):
+        raise ValueError("the arguments' shapes do not fit one layer")
+    if x.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or \
+            logits.dtype != torch.float32 or \
+            (router is not None and router.dtype != torch.float32):
+        raise ValueError("x and out are bfloat16, logits and router float32")
+    _check(_lib.moe_forward_few_fp4(_ptr(x), _ptr(logits), _ptr(router), _ptr(W1q), _ptr(W3q),
+                                    _ptr(W2q), _ptr(w1_scales), _ptr(w3_scales),
+                                    _ptr(w2_scales), T, d, E, k, d_ff, _ptr(out), _ptr(ws),
+                                    _nbytes(ws), _stream(stream)), "moe_forward_few_fp4")
 
 
 class ForwardGraph:

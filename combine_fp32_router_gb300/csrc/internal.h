@@ -14,6 +14,8 @@ constexpr int kTileRows = 128;             // rows of one expert GEMM tile; padd
 constexpr int kPairOddMinTiles = 7;        // CTA pairs for an odd tile count from this many
 constexpr int kMaxK = 16;
 constexpr int kMaxE = 1024;
+constexpr int kFewMaxTokens = 32;          // tokens of moe_forward_few_fp4 (one bit each)
+constexpr int kMaxFp4Cols = 1 << 20;       // values per row of a 4-bit matrix
 
 struct DevErr;
 
@@ -29,6 +31,11 @@ struct WsLayout {
          dXp = 0, seg = 0, xscale = 0;
   size_t route_total = 0, fwd_total = 0, bwd_total = 0;
 };
+
+// SM count of the current device (152 if it cannot be read), and the limit of device-side
+// waits that moe_set_wait_timeout_ns set.
+int num_sms_of_current_device();
+uint64_t wait_limit_ns();
 
 WsLayout make_layout(int64_t T, int d, int E, int k, int dff);
 

@@ -158,6 +158,8 @@ moe_status_t check_dims(int64_t T, int d, int E, int k, int dff, bool need_gemm)
   return MOE_OK;
 }
 
+}  // namespace
+
 int num_sms_of_current_device() {
   static std::atomic<int> cache[64] = {};
   int dev = 0;
@@ -172,6 +174,10 @@ int num_sms_of_current_device() {
   if (dev >= 0 && dev < 64) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
+
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+
+namespace {
 
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 

@@ -288,6 +288,96 @@ moe_status_t moe_route_dispatch_noalloc(const moe_bf16_t* x, const float* logits
 moe_status_t moe_route_dispatch_noalloc_get_error(cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * 4-bit experts: microscaled quantisation (MXFP4), the product of quantised rows and weights,
+ * and the whole layer for a few tokens on quantised experts.  The pages train experts in
+ * 4 bits (DeepSeek-V4 report, Thai translation, itsolotime.com: FP4 quantisation-aware
+ * training) and give no format; the reading is the OCP Microscaling Formats 1.0 MXFP4, the
+ * format of the tensor cores' 4-bit path.
+ *
+ * Format of a matrix of R rows and C columns: Kp = C rounded up to a multiple of 128.
+ *   codes  [R, Kp / 2] bytes: two E2M1 values per byte, the earlier one in the low nibble;
+ *          columns past C are zero codes.
+ *   scales moe_fp4_scale_bytes(R, C) bytes: one E8M0 byte s (factor 2^(s - 127), 255 = NaN) per
+ *          row and 32 columns, R rounded up to 128 rows; row r and block b at
+ *          ((r / 128) * (Kp / 128) + b / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4.
+ * A block's scale is floor(log2(max |x|)) - 2 + 127 (at least 0; 0 for a block of zeros), its
+ * codes are the E2M1 values nearest to x / 2^(s - 127), ties to the even mantissa, saturating
+ * at 6.  A block that holds an infinity or a NaN has s = 255: all its values are NaN.
+ * Both arrays are 16-byte aligned.  Groups of matrices (experts) lie one after another.
+ * ------------------------------------------------------------------------------------- */
+
+/* Element types of the entry points below. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F16 1
+#define MOE_DTYPE_F32 2
+
+/* Bytes of one row's codes, and of a rows x cols matrix's scales. */
+int64_t moe_fp4_row_bytes(int cols);
+size_t moe_fp4_scale_bytes(int64_t rows, int cols);
+
+/* x [rows, cols] (device, MOE_DTYPE_*, row r at x + r * row_stride elements, aligned to its
+ * element) -> q, scales.  Reads each value once.  cols <= 2^20 and rows * ceil(cols / 1024)
+ * < 2^31, else MOE_ERR_UNSUPPORTED.  rows = 0 writes nothing.  Asynchronous on `stream`, as
+ * every entry point here. */
+moe_status_t moe_quantize_rows_fp4(const void* x, int dtype, int64_t rows, int cols,
+                                   int64_t row_stride, uint8_t* q, uint8_t* scales,
+                                   cudaStream_t stream);
+
+/* The values that `groups` matrices of rows x cols stand for, to out [groups, rows, cols]
+ * (contiguous, 16-byte aligned), rounded once to `dtype` (exact in bf16 and fp32 down to their
+ * smallest subnormal). */
+moe_status_t moe_dequantize_rows_fp4(const uint8_t* q, const uint8_t* scales, int groups,
+                                     int64_t rows, int cols, int dtype, void* out,
+                                     cudaStream_t stream);
+
+/* Expert weights W [E, K, N] bf16 -> Wq [E, N, Kp / 2] and scales [E][moe_fp4_scale_bytes(N, K)]:
+ * each output column a row of codes, quantised along K.  E <= 1024, K and N <= 2^20. */
+moe_status_t moe_quantize_weights_fp4(const moe_bf16_t* W, int E, int K, int N, uint8_t* Wq,
+                                      uint8_t* scales, cudaStream_t stream);
+
+/*
+ * out[r, n] = sum_k A[r, k] B[e(r)][n, k], accumulated in fp32 in a K order that depends on K
+ * alone, rounded once to out_dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
+ *   a, a_scales : rows x K; b, b_scales: E matrices of N x K (moe_quantize_weights_fp4's
+ *                 layout); out [rows, N] contiguous.
+ *   counts      : NULL (E = 1: every row), or a DEVICE array [E]: expert e's counts[e] rows
+ *                 start at row sum_{j<e} round_up(counts[j], 128) (the layout of
+ *                 moe_expert_forward); rows between the segments are left as they were.
+ * Any rows, N, K >= 1 (rows = 0 writes nothing); E <= 1024, E * N < 2^31, K <= 2^20.  Counts
+ * that are negative or do not fit `rows` record MOE_ERR_DEVICE_BOUNDS and nothing is written;
+ * device-side problems are read with moe_gemm_fp4_get_error, which synchronises `stream`,
+ * returns the first one recorded on the current device since the last call, and clears it.
+ */
+moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t rows,
+                          const int32_t* counts, const uint8_t* b, const uint8_t* b_scales, int E,
+                          int N, int K, void* out, int out_dtype, cudaStream_t stream);
+moe_status_t moe_gemm_fp4_get_error(cudaStream_t stream);
+
+/*
+ * The whole layer for a few tokens (T <= 32) on 4-bit experts, in two launches, reading each
+ * chosen expert's weights once:
+ *   logits = x router^T (fp32 products and sums), or given; top-k and gate as moe_forward;
+ *   out_t = bf16( sum_j gate[t,j] * (h_tj W2[e_j]) ),  h_tj = silu(x_t W1[e_j]) * (x_t W3[e_j])
+ * The weights enter as the values that their codes stand for; x and h are not quantised: they
+ * enter the products as fp16 with a power of two per token (x) or per 16 values (h), i.e. with
+ * 11 significant bits wherever they are above 2^-28 of that group's largest; every sum is fp32,
+ * and the expert outputs are combined in fp32 in slot order and rounded once.
+ *   x [T,d] bf16; router [E,d] fp32, or NULL; logits [T,E] fp32: written when router is given,
+ *   read when it is NULL; W1q, W3q: E matrices of d_ff x d, W2q: of d x d_ff, with their scales
+ *   (moe_quantize_weights_fp4 of the bf16 weights of moe_forward); out [T,d] bf16.
+ *   ws: moe_few_workspace_bytes(T, d, E, k, d_ff) bytes (0 for unsupported sizes), 256-byte
+ *   aligned, ordered between calls as for moe_forward; its error word is read with moe_get_error.
+ * Sizes as moe_forward, with T <= 32, E * d < 2^31 and E * d_ff < 2^31.  T = 0 writes nothing.
+ * Bitwise reproducible, and each token's results are bitwise independent of the others and of T.
+ */
+size_t moe_few_workspace_bytes(int64_t T, int d, int E, int k, int d_ff);
+moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float* router,
+                                 const uint8_t* W1q, const uint8_t* W3q, const uint8_t* W2q,
+                                 const uint8_t* w1_scales, const uint8_t* w3_scales,
+                                 const uint8_t* w2_scales, int64_t T, int d, int E, int k, int d_ff,
+                                 moe_bf16_t* out, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * Fine-grained expert parallelism across R GPUs: the exchange plan and the pull-based row
  * copies (DeepSeek-V4 report, Thai translation, itsolotime.com, section 1.2 and Figure 5:
  * each GPU's experts run in waves, wave i+1's rows are fetched and wave i-1's outputs
