@@ -28,9 +28,6 @@
 
 namespace moe {
 
-CUtensorMap make_map_u8(const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
-                        cudaError_t* st);
-
 namespace {
 
 constexpr int kMaxT = kFewMaxTokens;
@@ -44,8 +41,11 @@ constexpr uint32_t kScBytes = 32 * 8 * 4;        // 32 rows x 8 words of 4 scale
 constexpr uint32_t kActRow = kStageK * 2 + 64;   // + 64: rows on different banks
 constexpr uint32_t kHsRow = kStageK / 16 * 4 + 16;
 constexpr int kMaxStages = 8;
-constexpr int kCons = 8;  // consumer warps
-constexpr int kThreads = 32 * (1 + kCons);
+constexpr int kCons = 16;  // consumer warps: 8 words of scales (128 values) x 2 halves of 16 rows
+constexpr int kParts = 8;  // partial sums of an output: one per word
+constexpr int kEpi = 4;    // epilogue warps: unit i of a CTA is finished by warp i % kEpi
+// warp 0 loads weights, warps 1..16 multiply, 17..20 finish units, 21 loads scales and activations
+constexpr int kThreads = 32 * (1 + kCons + kEpi + 1);
 
 struct FewLayout {
   size_t err, ticket, done1, done2, xs, x16, hs, h16, y, total;
@@ -215,8 +215,10 @@ struct ExpertParams {
   int32_t *ticket, *done1, *done2;
   DevErr* err;
   uint64_t wait_ns;
-  CUtensorMap map1, map3;  // codes [E dff / 8][8][Kp / 2], boxes 4 x 4 x 128 bytes
-  CUtensorMap map2;        // codes [E d][Kp / 2], boxes 32 x 128 bytes
+  // W1 and W3: boxes of 16 rows (8 j + i, i < 4) of 128 bytes, W2: of 32 rows; where a row is a
+  // whole number of 128-byte pieces (wide), a box holds four of them side by side
+  CUtensorMap map1, map3, map2;
+  int wide1, wide2;
 };
 
 // A unit's token group: expert, tokens (bits), first row of its h and y rows.
@@ -238,18 +240,19 @@ struct Shared {
   float gate[kMaxT][kMaxK];
   uint16_t slot_e[kMaxT][kMaxK];
   StageMeta meta[kMaxStages];
-  uint64_t bars[2 * kMaxStages + 1];
+  uint64_t bars[3 * kMaxStages + 2 * kEpi];
+  StageMeta unit[kEpi];  // the unit whose partial sums a buffer holds
   int32_t groups;
   int32_t abort_flag;
-  alignas(16) float red[2][kCons][2][32][4];
 };
+// behind Shared: kEpi buffers of partial sums [word][token][32 rows]
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint32_t bar, int x,
+                                            int y, int z, int w) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int x,
@@ -265,7 +268,7 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -294,61 +297,58 @@ __device__ __forceinline__ float scale_of(uint32_t w, int i) {
   return __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
 }
 
-// One stage of one warp: word w of the scales, i.e. 4 blocks of 32 values, for both 16-row
-// halves.  KIND 2: the activations' own factors (16 values each) are applied to the two
-// halves of a block.
+// One stage of one warp: word w of the scales, i.e. 4 blocks of 32 values, for one 16-row half
+// (`rows`: its 16 x 128-byte box, `sc`: its words).  KIND 2: the activations' own factors (16
+// values each) are applied to the two halves of a block.
 template <int KIND>
-__device__ __forceinline__ void multiply(uint32_t st, uint32_t sc, uint32_t act, uint32_t hs,
-                                         int w, int lane, int tok, float (&acc)[2][4],
-                                         uint32_t (&bad)[2][2]) {
+__device__ __forceinline__ void multiply(uint32_t rows, uint32_t sc, uint32_t act, uint32_t hs,
+                                         int w, int lane, int tok, float (&acc)[4],
+                                         uint32_t (&bad)[2]) {
   const int g = lane >> 2, t = lane & 3;
-  const uint32_t box = st + (w >> 1) * 4096 + g * 128 + 4 * t;
+  const uint32_t r0 = rows + g * 128 + 4 * t;
   const uint32_t b0 = act + min(g, tok - 1) * kActRow + (w * 128 + 8 * t) * 2;
-  uint32_t s[2][2];
-#pragma unroll
-  for (int m = 0; m < 2; ++m)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      s[m][r] = lds32(sc + (w * 32 + m * 16 + r * 8 + g) * 4);
-      bad[m][r] |= __vcmpeq4(s[m][r], 0xFFFFFFFFu);
-    }
   const uint32_t h0 = hs + min(2 * t, tok - 1) * kHsRow + w * 32;
   const uint32_t h1 = hs + min(2 * t + 1, tok - 1) * kHsRow + w * 32;
+  // every shared-memory read of the stage first: a warp has little else to hide their latency
+  uint32_t wv[4][2];
+  uint4 x[4];
+  float2 f0[4], f1[4];
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
     const uint32_t chunk = (((w & 1) * 4 + b) ^ g) << 4;
-    const uint4 x = lds128(b0 + b * 64);
-    float2 f0, f1;
+    wv[b][0] = lds32(r0 + chunk);
+    wv[b][1] = lds32(r0 + 1024 + chunk);
+    x[b] = lds128(b0 + b * 64);
     if constexpr (KIND == 2) {
-      f0 = lds_f2(h0 + b * 8);
-      f1 = lds_f2(h1 + b * 8);
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      // a 16-row half is 16 rows of the 32-row box, or its own 16-row box: 2 KB either way
-      const uint32_t w0 = lds32(box + m * 2048 + chunk), w1 = lds32(box + m * 2048 + 1024 + chunk);
-      uint32_t a[4], c[4];
-      e2m1x8_to_half(w0, a);
-      e2m1x8_to_half(w1, c);
-      float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const float slo = scale_of(s[m][0], b), shi = scale_of(s[m][1], b);
-      mma_f16(p, a[0], c[0], a[1], c[1], x.x, x.y);
-      if constexpr (KIND == 2) {
-        float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        mma_f16(q, a[2], c[2], a[3], c[3], x.z, x.w);
-        p[0] = fmaf(q[0], f0.y, p[0] * f0.x);
-        p[1] = fmaf(q[1], f1.y, p[1] * f1.x);
-        p[2] = fmaf(q[2], f0.y, p[2] * f0.x);
-        p[3] = fmaf(q[3], f1.y, p[3] * f1.x);
-      } else {
-        mma_f16(p, a[2], c[2], a[3], c[3], x.z, x.w);
-      }
-      acc[m][0] = fmaf(p[0], slo, acc[m][0]);
-      acc[m][1] = fmaf(p[1], slo, acc[m][1]);
-      acc[m][2] = fmaf(p[2], shi, acc[m][2]);
-      acc[m][3] = fmaf(p[3], shi, acc[m][3]);
+      f0[b] = lds_f2(h0 + b * 8);
+      f1[b] = lds_f2(h1 + b * 8);
     }
   }
+  const uint32_t slo = lds32(sc + g * 4), shi = lds32(sc + (8 + g) * 4);
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    uint32_t a[4], c[4];
+    e2m1x8_to_half(wv[b][0], a);
+    e2m1x8_to_half(wv[b][1], c);
+    float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    mma_f16(p, a[0], c[0], a[1], c[1], x[b].x, x[b].y);
+    if constexpr (KIND == 2) {
+      float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      mma_f16(q, a[2], c[2], a[3], c[3], x[b].z, x[b].w);
+      p[0] = fmaf(q[0], f0[b].y, p[0] * f0[b].x);
+      p[1] = fmaf(q[1], f1[b].y, p[1] * f1[b].x);
+      p[2] = fmaf(q[2], f0[b].y, p[2] * f0[b].x);
+      p[3] = fmaf(q[3], f1[b].y, p[3] * f1[b].x);
+    } else {
+      mma_f16(p, a[2], c[2], a[3], c[3], x[b].z, x[b].w);
+    }
+    acc[0] = fmaf(p[0], scale_of(slo, b), acc[0]);
+    acc[1] = fmaf(p[1], scale_of(slo, b), acc[1]);
+    acc[2] = fmaf(p[2], scale_of(shi, b), acc[2]);
+    acc[3] = fmaf(p[3], scale_of(shi, b), acc[3]);
+  }
+  bad[0] |= __vcmpeq4(slo, 0xFFFFFFFFu);
+  bad[1] |= __vcmpeq4(shi, 0xFFFFFFFFu);
 }
 
 template <int EPL>
@@ -384,15 +384,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int S = p.stages;
   const auto full = [&](int s) { return smem_u32(&sh.bars[s]); };
   const auto empty = [&](int s) { return smem_u32(&sh.bars[kMaxStages + s]); };
-  const uint32_t ubar = smem_u32(&sh.bars[2 * kMaxStages]);
+  const auto told = [&](int s) { return smem_u32(&sh.bars[2 * kMaxStages + s]); };
+  const auto rfull = [&](int i) { return smem_u32(&sh.bars[3 * kMaxStages + i]); };
+  const auto rfree = [&](int i) { return smem_u32(&sh.bars[3 * kMaxStages + kEpi + i]); };
+  float* red = reinterpret_cast<float*>(&sh + 1);
+  const int red_floats = kParts * p.tok * 32;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&sh.abort_flag);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 33);  // the producer's lane 0 with the bytes, 32 lanes' scale copies
+      mbar_init(full(s), 33);  // the weights' producer with the bytes, 32 lanes' own copies
       mbar_init(empty(s), kCons);
+      mbar_init(told(s), 1);   // the stage's meta is written
     }
-    mbar_init(ubar, kCons);
+    for (int i = 0; i < kEpi; ++i) {
+      mbar_init(rfull(i), kCons);
+      mbar_init(rfree(i), 1);
+    }
     fence_mbar_init();
     sh.abort_flag = 0;
     tma_prefetch_desc(&p.map1);
@@ -402,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int e = threadIdx.x; e < p.E; e += kThreads) sh.mask[e] = 0u;
   __syncthreads();
   griddep_wait();
-  for (int t = warp; t < p.T; t += kCons + 1) {
+  for (int t = warp; t < p.T; t += kThreads / 32) {
     if (p.E <= 256) route_token<8>(p, sh, t, lane);
     else route_token<32>(p, sh, t, lane);
   }
@@ -450,183 +458,253 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int kt1 = p.d / 128, kt2 = p.dff / 128;  // scale words per row
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- producer
-    uint32_t it = 0;
-    int next = 0;
-    if (lane == 0) next = atomicAdd(p.ticket, 1);
-    bool ok = true;
-    while (ok) {
-      const int u = __shfl_sync(0xFFFFFFFFu, next, 0);
-      if (u >= n_units) break;
-      if (lane == 0) next = atomicAdd(p.ticket, 1);  // used after this unit's loads
-      const bool first = u < n1;
-      const int gi = first ? u / hu : (u - n1) / yu, tile = first ? u % hu : (u - n1) % yu;
-      const Group gr = sh.group[gi];
-      const int kt = first ? kt1 : kt2;
-      const int nks = (kt + 7) / 8;
-      // this lane's weight row: where its scale words start
-      const uint8_t* sp;
-      {
-        const int r = first ? 32 * (tile >> 1) + 8 * ((lane & 15) >> 2) + 4 * (tile & 1) + (lane & 3)
-                            : kUnitY * tile + lane;
-        const int64_t at = static_cast<int64_t>(r >> 7) * kt * kMxTileBytes + (r & 31) * 16 +
-                           ((r >> 5) & 3) * 4;
-        sp = (first ? (lane < 16 ? p.s1 : p.s3) + gr.e * p.s1_bytes : p.s2 + gr.e * p.s2_bytes) + at;
-      }
-      bool ready = first;  // a y unit's activations are there once all h units of its group are
-      for (int ks = 0; ks < nks; ++ks, ++it) {
-        const int s = it % S;
-        ok = it < static_cast<uint32_t>(S) ||
-             mbar_wait(empty(s), (it / S - 1) & 1, abort_flag, p.err, 70, p.wait_ns);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        const uint32_t st = base + s * p.stage_bytes;
-        const uint32_t sc = st + kWBytes, act = sc + kScBytes, hsm = act + p.tok * kActRow;
-        const int words = min(8, kt - 8 * ks);
-        for (int j = 0; j < words; ++j)
-          cp_async_4(sc + (j * 32 + lane) * 4, sp + static_cast<int64_t>(8 * ks + j) * kMxTileBytes);
-        cp_async_arrive_noinc(full(s));
-        if (lane == 0) {
-          sh.meta[s] = StageMeta{first ? 1 : 2, gi, tile, ks};
-          const int boxes = (words + 1) / 2;
-          const uint32_t abytes = words * 256;  // 128 values of 2 bytes per word
-          mbar_arrive_expect_tx(full(s), boxes * 4096 + gr.n * (abytes + (first ? 0 : words * 32)));
-          for (int c = 0; c < boxes; ++c) {
-            const int x = ks * (kStageK / 2) + 128 * c;
+    // ---------------------------------------------------------------- weights
+    if (lane == 0) {
+      uint32_t it = 0, s = 0, phase = 1;  // phase: parity of the empty barrier's last use
+      bool ok = true;
+      int next = atomicAdd(p.ticket, 1);
+      while (true) {
+        const int u = next;
+        const bool work = u < n_units;
+        if (work) next = atomicAdd(p.ticket, 1);  // used after this unit's loads
+        const bool first = u < n1;
+        const int v = first ? u : u - n1, per = first ? hu : yu;
+        const int gi = v / per, tile = v % per;
+        const int kt = work ? (first ? kt1 : kt2) : 1;
+        const int e = work ? sh.group[gi].e : 0;
+        const CUtensorMap* ma = first ? &p.map1 : &p.map2;
+        const bool wide = first ? p.wide1 : p.wide2;
+        const int y = first ? 4 * (tile & 1) : e * p.d + kUnitY * tile;
+        const int z = e * (p.dff / 8) + 4 * (tile >> 1);
+        for (int ks = 0; 8 * ks < kt; ++ks) {
+          if (it >= static_cast<uint32_t>(S))
+            ok = mbar_wait(empty(s), phase, abort_flag, p.err, 70, p.wait_ns);
+          if (!ok) break;
+          sh.meta[s] = StageMeta{work ? (first ? 1 : 2) : 0, gi, tile, ks};
+          mbar_arrive(told(s));
+          const uint32_t st = base + s * p.stage_bytes;
+          const int boxes = work ? (min(8, kt - 8 * ks) + 1) / 2 : 0;
+          if (!work) {
+            mbar_arrive(full(s));
+          } else if (wide) {
+            mbar_arrive_expect_tx(full(s), kWBytes);  // pieces past the row's end are zeros
             if (first) {
-              const int z = gr.e * (p.dff / 8) + 4 * (tile >> 1), yy = 4 * (tile & 1);
-              tma_load_3d(st + 4096 * c, &p.map1, full(s), x, yy, z);
-              tma_load_3d(st + 4096 * c + 2048, &p.map3, full(s), x, yy, z);
+              tma_load_4d(st, ma, full(s), 0, y, z, 4 * ks);
+              tma_load_4d(st + kWBytes / 2, &p.map3, full(s), 0, y, z, 4 * ks);
             } else {
-              tma_load_2d(st + 4096 * c, &p.map2, full(s), x, gr.e * p.d + kUnitY * tile);
+              tma_load_3d(st, ma, full(s), 0, y, 4 * ks);
+            }
+          } else {
+            mbar_arrive_expect_tx(full(s), boxes * 4096);
+            for (int c = 0; c < boxes; ++c) {
+              const int x = ks * (kStageK / 2) + 128 * c;
+              if (first) {
+                tma_load_3d(st + 2048 * c, ma, full(s), x, y, z);
+                tma_load_3d(st + kWBytes / 2 + 2048 * c, &p.map3, full(s), x, y, z);
+              } else {
+                tma_load_2d(st + 4096 * c, ma, full(s), x, y);
+              }
             }
           }
-          if (!ready) {
-            // two tokens per arriving warp
-            ready = wait_count(p.done1 + gi, hu * ((gr.n + 1) / 2), abort_flag, p.err, 71, p.wait_ns);
-            fence_proxy_async_global();
-          }
-          uint32_t left = gr.tokens;
-          for (int i = 0; i < gr.n; ++i, left &= left - 1u) {
-            const uint16_t* src = first
-                                      ? p.x16 + static_cast<int64_t>(__ffs(left) - 1) * p.d
-                                      : p.h16 + static_cast<int64_t>(gr.row0 + i) * p.dff;
-            bulk_load(act + i * kActRow, src + ks * kStageK, abytes, full(s));
-            if (!first)
-              bulk_load(hsm + i * kHsRow,
-                        p.hs + static_cast<int64_t>(gr.row0 + i) * (p.dff / 16) + ks * (kStageK / 16),
-                        words * 32, full(s));
+          ++it;
+          if (++s == static_cast<uint32_t>(S)) {
+            s = 0;
+            phase ^= 1;
           }
         }
-        __syncwarp();
+        if (!ok || !work) break;
       }
+      // copies still in flight land before the CTA ends
+      if (*abort_flag)
+        for (uint32_t i = it > static_cast<uint32_t>(S) ? it - S : 0; i < it; ++i)
+          mbar_wait(full(i % S), (i / S) & 1, nullptr, p.err, 72, p.wait_ns);
     }
-    if (ok) {  // a last stage without work
-      const int s = it % S;
-      ok = it < static_cast<uint32_t>(S) ||
-           mbar_wait(empty(s), (it / S - 1) & 1, abort_flag, p.err, 70, p.wait_ns);
-      if (__all_sync(0xFFFFFFFFu, ok)) {
-        if (lane == 0) {
-          sh.meta[s] = StageMeta{0, 0, 0, 0};
-          mbar_arrive(full(s));
-        }
+  } else if (warp == kThreads / 32 - 1) {
+    // ---------------------------------------------------------------- scales, activations
+    uint32_t s = 0, phase = 0;
+    while (true) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(told(s), phase, abort_flag, p.err, 76, p.wait_ns)))
+        break;
+      const StageMeta m = sh.meta[s];
+      if (m.kind == 0) {
         mbar_arrive(full(s));
-        ++it;
+        break;
+      }
+      const bool first = m.kind == 1;
+      const Group gr = sh.group[m.group];
+      const int kt = first ? kt1 : kt2;
+      const int words = min(8, kt - 8 * m.ks);
+      const uint32_t sc = base + s * p.stage_bytes + kWBytes;
+      const uint32_t act = sc + kScBytes, hsm = act + p.tok * kActRow;
+      {
+        // this lane's weight row
+        const int r = first ? 32 * (m.tile >> 1) + 8 * ((lane & 15) >> 2) + 4 * (m.tile & 1) + (lane & 3)
+                            : kUnitY * m.tile + lane;
+        const uint8_t* sp =
+            (first ? (lane < 16 ? p.s1 : p.s3) + gr.e * p.s1_bytes : p.s2 + gr.e * p.s2_bytes) +
+            (static_cast<int64_t>(r >> 7) * kt + 8 * m.ks) * kMxTileBytes + (r & 31) * 16 +
+            ((r >> 5) & 3) * 4;
+        const uint32_t dst = sc + lane * 4;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j < words) cp_async_4(dst + j * 128, sp + j * kMxTileBytes);
+      }
+      // a y unit's activations are there once all h units of its group are
+      if (!first && m.ks == 0 &&
+          !__all_sync(0xFFFFFFFFu, wait_count(p.done1 + m.group, hu, abort_flag, p.err, 71, p.wait_ns)))
+        break;
+      uint32_t left = gr.tokens;
+      for (int i = 0; i < gr.n; ++i, left &= left - 1u) {
+        const uint16_t* src =
+            (first ? p.x16 + static_cast<int64_t>(__ffs(left) - 1) * p.d
+                   : p.h16 + static_cast<int64_t>(gr.row0 + i) * p.dff) + m.ks * kStageK + lane * 8;
+        const uint32_t dst = act + i * kActRow + lane * 16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // a word of scales stands for 16 pieces of 16 bytes
+          if (j * 32 + lane < words * 16) cp_async_16(dst + j * 512, src + j * 256);
+      }
+      if (!first) {
+        // the factors of 16 values each: 32 bytes per word, two pieces of 16 bytes
+        for (int i = lane; i < gr.n * 16; i += 32)
+          if ((i & 15) < words * 2)
+            cp_async_16(hsm + (i >> 4) * kHsRow + (i & 15) * 16,
+                        p.hs + static_cast<int64_t>(gr.row0 + (i >> 4)) * (p.dff / 16) +
+                            m.ks * (kStageK / 16) + (i & 15) * 4);
+      }
+      cp_async_arrive_noinc(full(s));
+      if (++s == static_cast<uint32_t>(S)) {
+        s = 0;
+        phase ^= 1;
       }
     }
-    // copies still in flight land before the CTA ends
-    if (*abort_flag)
-      for (uint32_t i = it > static_cast<uint32_t>(S) ? it - S : 0; i < it; ++i)
-        mbar_wait(full(i % S), (i / S) & 1, nullptr, p.err, 72, p.wait_ns);
-  } else {
+    cp_async_wait_all();
+  } else if (warp <= kCons) {
     // ---------------------------------------------------------------- consumers
-    const int w = warp - 1;
-    float acc[2][4] = {};
-    uint32_t bad[2][2] = {};
-    uint32_t units = 0;
-    for (uint32_t it = 0;; ++it) {
-      const int s = it % S;
-      if (!mbar_wait(full(s), (it / S) & 1, abort_flag, p.err, 73, p.wait_ns)) break;
+    const int w = (warp - 1) & 7, half = (warp - 1) >> 3, g = lane >> 2, tc = 2 * (lane & 3);
+    float acc[4] = {};
+    uint32_t bad[2] = {};
+    uint32_t units = 0, s = 0, phase = 0;
+    while (true) {
+      if (!mbar_wait(full(s), phase, abort_flag, p.err, 73, p.wait_ns)) break;
       const StageMeta m = sh.meta[s];
       if (m.kind == 0) break;
       const uint32_t st = base + s * p.stage_bytes;
       const uint32_t sc = st + kWBytes, act = sc + kScBytes, hsm = act + p.tok * kActRow;
       const int kt = m.kind == 1 ? kt1 : kt2;
       if (8 * m.ks + w < kt) {
-        if (m.kind == 1) multiply<1>(st, sc, act, hsm, w, lane, p.tok, acc, bad);
-        else multiply<2>(st, sc, act, hsm, w, lane, p.tok, acc, bad);
+        const uint32_t scw = sc + (w * 32 + half * 16) * 4;
+        // h: [W1 | W3] of four 16-row boxes each; y: four 32-row boxes
+        if (m.kind == 1)
+          multiply<1>(st + half * (kWBytes / 2) + (w >> 1) * 2048, scw, act, hsm, w, lane, p.tok, acc, bad);
+        else
+          multiply<2>(st + (w >> 1) * 4096 + half * 2048, scw, act, hsm, w, lane, p.tok, acc, bad);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(empty(s));
+      if (++s == static_cast<uint32_t>(S)) {
+        s = 0;
+        phase ^= 1;
+      }
       if (8 * (m.ks + 1) < kt) continue;
 
-      // ------------------------------------------------ end of a unit: add the eight warps
-      const uint32_t par = units & 1;
+      // end of a unit: the partial sums go to the epilogue warp whose turn it is
+      const int buf = units % kEpi;
+      if (units >= kEpi &&
+          !mbar_wait(rfree(buf), (units / kEpi - 1) & 1, abort_flag, p.err, 74, p.wait_ns))
+        break;
+      float* r = red + buf * red_floats + w * p.tok * 32;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (bad[h][i >> 1]) acc[h][i] = __uint_as_float(0x7FC00000u);  // a NaN scale in the row
-          sh.red[par][w][h][lane][i] = acc[h][i];
-          acc[h][i] = 0.0f;
-        }
-        bad[h][0] = bad[h][1] = 0u;
+      for (int i = 0; i < 4; ++i) {
+        if (bad[i >> 1]) acc[i] = __uint_as_float(0x7FC00000u);  // a NaN scale in the row
+        const int n = tc + (i & 1);
+        if (n < p.tok) r[n * 32 + 16 * half + 8 * (i >> 1) + g] = acc[i];
+        acc[i] = 0.0f;
       }
+      bad[0] = bad[1] = 0u;
+      if (warp == 1 && lane == 0) sh.unit[buf] = m;
       __syncwarp();
-      if (lane == 0) mbar_arrive(ubar);
-      if (!mbar_wait(ubar, units & 1, abort_flag, p.err, 74, p.wait_ns)) break;
+      if (lane == 0) mbar_arrive(rfull(buf));
       ++units;
+    }
+    // no more units: each epilogue warp gets an empty one
+    if (!*abort_flag && warp <= kEpi) {
+      const uint32_t last = units + warp - 1;
+      const int buf = last % kEpi;
+      // all warps have written every unit that this one follows
+      bool ok = true;
+      if (last >= kEpi)
+        ok = mbar_wait(rfree(buf), (last / kEpi - 1) & 1, abort_flag, p.err, 74, p.wait_ns);
+      if (ok && lane == 0) {
+        sh.unit[buf].kind = 0;
+        for (int i = 0; i < kCons; ++i) mbar_arrive(rfull(buf));
+      }
+    }
+  } else {
+    // ---------------------------------------------------------------- epilogue
+    const int ew = warp - 1 - kCons;
+    const float* r = red + ew * red_floats;
+    for (uint32_t i = 0;; ++i) {
+      if (!mbar_wait(rfull(ew), i & 1, abort_flag, p.err, 75, p.wait_ns)) break;
+      const StageMeta m = sh.unit[ew];
+      if (m.kind == 0) break;
       const Group& gr = sh.group[m.group];
       if (m.kind == 1) {
-        // warp w: tokens 2 w and 2 w + 1, 16 columns of h each
-        if (2 * w >= gr.n) continue;
-        const int n = 2 * w + (lane >> 4), r = lane & 15;
-        const int src = (r & 7) * 4 + (n >> 1), idx = (r >> 3) * 2 + (n & 1);
-        float a = 0.0f, b = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kCons; ++i) {
-          a += sh.red[par][i][0][src][idx];
-          b += sh.red[par][i][1][src][idx];
-        }
-        float h = 0.0f;
+        // two tokens at a time, 16 columns of h each: rows 0..15 are W1's sums, 16..31 W3's
+        const int c = lane & 15;
         uint32_t tokens = gr.tokens;
-        for (int i = 0; i < n; ++i) tokens &= tokens - 1u;
-        if (n < gr.n) {
-          const float xs = __ldg(p.xs + __ffs(tokens) - 1);
-          a *= xs;
-          b *= xs;
-          h = a / (1.0f + expf(-a)) * b;
-        }
-        uint32_t amax = __float_as_uint(h) & 0x7FFFFFFFu;
+        for (int n0 = 0; n0 < gr.n; n0 += 2) {
+          const int n = n0 + (lane >> 4);
+          float h = 0.0f;
+          if (n < gr.n) {
+            const float* rn = r + n * 32 + c;
+            float a = 0.0f, b = 0.0f;
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        float mul, inv;
-        f16_scale(amax, &mul, &inv);
-        if (n < gr.n) {
-          const int64_t row = gr.row0 + n;
-          p.h16[row * p.dff + 32 * (m.tile >> 1) + 8 * (r >> 2) + 4 * (m.tile & 1) + (r & 3)] =
-              __half_as_ushort(__float2half_rn(h * mul));
-          if (r == 0) p.hs[row * (p.dff / 16) + m.tile] = inv;
+            for (int v = 0; v < kParts; ++v) {
+              a += rn[v * p.tok * 32];
+              b += rn[v * p.tok * 32 + 16];
+            }
+            const uint32_t tk = (lane >> 4) ? tokens & (tokens - 1u) : tokens;
+            const float xs = __ldg(p.xs + __ffs(tk) - 1);
+            a *= xs;
+            b *= xs;
+            h = a / (1.0f + expf(-a)) * b;
+          }
+          tokens &= tokens - 1u;
+          tokens &= tokens - 1u;
+          uint32_t amax = __float_as_uint(h) & 0x7FFFFFFFu;
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          float mul, inv;
+          f16_scale(amax, &mul, &inv);
+          if (n < gr.n) {
+            const int64_t row = gr.row0 + n;
+            p.h16[row * p.dff + 32 * (m.tile >> 1) + 8 * (c >> 2) + 4 * (m.tile & 1) + (c & 3)] =
+                __half_as_ushort(__float2half_rn(h * mul));
+            if (c == 0) p.hs[row * (p.dff / 16) + m.tile] = inv;
+          }
         }
-        fence_proxy_async_global();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rfree(ew));
         __threadfence();
         __syncwarp();
         if (lane == 0) red_release_add(p.done1 + m.group, 1);
       } else {
-        // warp w: token w, 32 columns of y
-        if (w >= gr.n) continue;
-        const int src = (lane & 7) * 4 + (w >> 1), idx = ((lane >> 3) & 1) * 2 + (w & 1);
-        float v = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kCons; ++i) v += sh.red[par][i][lane >> 4][src][idx];
         const int col = kUnitY * m.tile + lane;
-        __stcg(p.y + static_cast<int64_t>(gr.row0 + w) * p.d + col, v);
+        for (int n = 0; n < gr.n; ++n) {
+          const float* rn = r + n * 32 + lane;
+          float v = 0.0f;
+#pragma unroll
+          for (int i2 = 0; i2 < kParts; ++i2) v += rn[i2 * p.tok * 32];
+          __stcg(p.y + static_cast<int64_t>(gr.row0 + n) * p.d + col, v);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(rfree(ew));
         __threadfence();
         __syncwarp();
         int last = 0;
-        if (lane == 0) last = atomicAdd(p.done2 + m.tile, 1) == p.T * p.k - 1;
+        if (lane == 0) last = atomicAdd(p.done2 + m.tile, gr.n) + gr.n == p.T * p.k;
         if (__shfl_sync(0xFFFFFFFFu, last, 0)) {
-          // the last row of these 32 columns: combine them, in slot order
+          // the last rows of these 32 columns: combine them, in slot order
           __threadfence();
           for (int t = 0; t < p.T; ++t) {
             float o = 0.0f;
@@ -652,20 +730,38 @@ moe_status_t check_few(int64_t T, int d, int E, int k, int dff) {
   return MOE_OK;
 }
 
-// Weights [E dff rows][dff-row group of 8][Kp / 2 bytes] as 3-D boxes of 4 groups x 4 rows x 128
-// bytes: 16 rows 8 j + i (i < 4), the half of a 32-row block that shares a factor of h.
-CUtensorMap make_map_h(const void* base, uint64_t inner, uint64_t rows, cudaError_t* st) {
+// Map of weight rows for units of h (16 rows 8 j + i, i < 4: the half of a 32-row block that
+// shares a factor of h) or of y (32 rows), 128-byte swizzle.  `pieces` (a row is a whole number
+// of 128-byte pieces): the pieces are an outer dimension, and a box holds four of them, so a
+// stage is one copy per matrix; issuing eight 2 KB boxes per stage instead took the producer
+// 1700 cycles, over twice the stage's share of the memory time.  Otherwise a box is one piece,
+// zeros past the row's end.
+CUtensorMap make_weight_map(const void* base, uint64_t inner, uint64_t rows, bool h, bool pieces,
+                            cudaError_t* st) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   CUtensorMap m = {};
   auto enc = reinterpret_cast<Encode>(tensor_map_encoder());
-  const cuuint64_t dims[3] = {inner, 8, rows / 8};
-  const cuuint64_t strides[2] = {inner, 8 * inner};
-  const cuuint32_t box[3] = {128, 4, 4};
-  const cuuint32_t ones[3] = {1, 1, 1};
-  if (!enc || enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t box[4];
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  cuuint32_t n = 0;
+  const auto dim = [&](uint64_t size, uint64_t stride, uint32_t b) {
+    dims[n] = size;
+    if (n) strides[n - 1] = stride;
+    box[n++] = b;
+  };
+  dim(pieces ? 128 : inner, 1, 128);
+  if (h) {
+    dim(8, inner, 4);
+    dim(rows / 8, 8 * inner, 4);
+  } else {
+    dim(rows, inner, 32);
+  }
+  if (pieces) dim(inner / 128, 128, 4);
+  if (!enc || enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, n, const_cast<void*>(base), dims, strides, box,
                   ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
@@ -731,7 +827,8 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   p.dff = d_ff;
   p.tok = static_cast<int>(T < kTok ? T : kTok);
   p.stage_bytes = static_cast<uint32_t>((kWBytes + kScBytes + p.tok * (kActRow + kHsRow) + 1023) / 1024 * 1024);
-  const size_t room = 232448 - 1024 - sizeof(Shared);
+  const size_t red_bytes = static_cast<size_t>(kEpi) * kParts * p.tok * 32 * sizeof(float);
+  const size_t room = 232448 - 1024 - sizeof(Shared) - red_bytes;
   p.stages = static_cast<int>(room / p.stage_bytes < kMaxStages ? room / p.stage_bytes : kMaxStages);
   p.s1 = w1_scales;
   p.s3 = w3_scales;
@@ -749,9 +846,11 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   p.done2 = reinterpret_cast<int32_t*>(w + L.done2);
   p.err = r.err;
   p.wait_ns = wait_limit_ns();
-  p.map1 = make_map_h(W1q, d / 2, static_cast<uint64_t>(E) * d_ff, &st);
-  p.map3 = make_map_h(W3q, d / 2, static_cast<uint64_t>(E) * d_ff, &st);
-  p.map2 = make_map_u8(W2q, d_ff / 2, static_cast<uint64_t>(E) * d, 32, &st);
+  p.wide1 = d % 256 == 0;
+  p.wide2 = d_ff % 256 == 0;
+  p.map1 = make_weight_map(W1q, d / 2, static_cast<uint64_t>(E) * d_ff, true, p.wide1, &st);
+  p.map3 = make_weight_map(W3q, d / 2, static_cast<uint64_t>(E) * d_ff, true, p.wide1, &st);
+  p.map2 = make_weight_map(W2q, d_ff / 2, static_cast<uint64_t>(E) * d, false, p.wide2, &st);
   if (st != cudaSuccess) return MOE_ERR_CUDA;
 
   int rgrid = router ? (E + kRouterExperts - 1) / kRouterExperts : 1;
@@ -772,7 +871,7 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
       return MOE_ERR_CUDA;
     attr_set_mask.fetch_or(bit, std::memory_order_release);
   }
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + sizeof(Shared);
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + sizeof(Shared) + red_bytes;
   const int64_t units = T * k * (d_ff / kUnitH + d / kUnitY);
   const int sms = num_sms_of_current_device();
   st = launch_pdl(few_experts_kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)),
