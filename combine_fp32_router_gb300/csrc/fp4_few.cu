@@ -1,24 +1,23 @@
 // The whole MoE layer for a few tokens (T <= 32) on MXFP4 experts, in two launches:
-//   few_router_kernel  logits = x R^T in fp32 (unless the caller has them), x as fp16 with a
-//                      power of two per token, counters cleared
+//   few_router_kernel  logits = x R^T in fp32 (unless the caller has them), x in MXFP4 terms,
+//                      counters cleared
 //   few_experts_kernel top-k and gates, both expert products with SwiGLU between, the combine
 //
-// Bound by reading the chosen experts' weights once, 17/32 byte a value, so the kernel is a
-// stream of weight tiles: a producer warp keeps a ring of 16 KB stages full (TMA codes, and
-// the scale words and activations beside them), eight warps multiply.  Weights are the M
-// operand of mma.sync m16n8k16 (E2M1 to fp16 is one exact conversion per pair), up to eight
-// tokens of the expert the N operand: with one token in eight columns the tensor work is
-// still far below the stream's time, and the fp16 activations cost nothing in accuracy (fp16
-// has bf16's bits and three more; each token's power of two keeps its largest value at 2^14,
-// so only values below 2^-28 of it lose bits).  A block's scale is applied to the fp32 partial
-// sums of its 32 products.
+// Bound by reading the chosen experts' weights once, 17/32 byte a value.  The block-scaled
+// tensor cores (tcgen05 kind::mxf4) take the weights as they lie in memory; the activations
+// have to be 4-bit operands too, so each is written as a sum of kTerms = 6 MXFP4 numbers, the
+// residual of each being quantised again: a term leaves at most 1/5 of its block's largest
+// value, six at most 2^-13.9 of it (2^-19 is usual), which is below what rounding to bf16
+// would cost.  A token's terms are six columns of the N operand, the partial products are
+// added in fp32.  (Converting the weights to fp16 for mma.sync instead kept the integer pipe
+// busy for longer than the memory: 502 us for 16 tokens over 64 experts of d = 7168,
+// d_ff = 2048, where the stream alone takes 225 us.)
 //
-// Work units are (8 tokens of an expert) x 16 columns of h (both projections), then x 32
-// columns of y; CTAs take them from a counter in that order, so whoever waits for an h waits
-// only for units that running CTAs hold.  Every sum's order is fixed by the sizes: results do
-// not depend on the batch or on which CTA did what.
+// Units of work are 128 weight rows x a range of K for up to 8 tokens of an expert, first of
+// W1 and W3, then of W2.  CTAs take them from a counter in that order, so whoever waits for an h
+// waits only for units that running CTAs hold.  Every sum's order is fixed by the sizes:
+// results do not depend on the batch or on which CTA did what.
 #include <cuda.h>
-#include <cuda_fp16.h>
 
 #include <atomic>
 
@@ -32,25 +31,29 @@ namespace {
 
 constexpr int kMaxT = kFewMaxTokens;
 constexpr int kMaxRows = kMaxT * kMaxK;  // (token, slot) pairs
-constexpr int kUnitH = 16;               // columns of h per unit
-constexpr int kUnitY = 32;               // columns of y per unit
-constexpr int kTok = 8;                  // tokens per unit
-constexpr int kStageK = 1024;            // values of K per stage: 32 weight rows x 512 bytes
-constexpr uint32_t kWBytes = 32 * kStageK / 2;
-constexpr uint32_t kScBytes = 32 * 8 * 4;        // 32 rows x 8 words of 4 scales
-constexpr uint32_t kActRow = kStageK * 2 + 64;   // + 64: rows on different banks
-constexpr uint32_t kHsRow = kStageK / 16 * 4 + 16;
-constexpr int kMaxStages = 8;
-constexpr int kCons = 16;  // consumer warps: 8 words of scales (128 values) x 2 halves of 16 rows
-constexpr int kParts = 8;  // partial sums of an output: one per word
-constexpr int kEpi = 4;    // epilogue warps: unit i of a CTA is finished by warp i % kEpi
-// warp 0 loads weights, warps 1..16 multiply, 17..20 finish units, 21 loads scales and activations
-constexpr int kThreads = 32 * (1 + kCons + kEpi + 1);
+constexpr int kTok = 8;                  // token columns of a unit
+constexpr int kTerms = 6;
+constexpr int kMaxN = kTok * kTerms;
+constexpr int kStageKt = 4;              // 128-value K tiles per stage
+constexpr int kPartStages = 4;           // stages of a K range of W1 and W3 (at most)
+constexpr uint32_t kABytes = 128 * kStageKt * 64;
+constexpr uint32_t kSfBytes = kStageKt * kMxTileBytes;
+constexpr int kMaxStages = 5;
+constexpr uint32_t kAccCols = 64;        // TMEM: two accumulators, then the stages' scales
+constexpr uint32_t kSfCol0 = 2 * kAccCols;
+constexpr uint32_t kSfCols = 8 * kStageKt;
+static_assert(kSfCol0 + kMaxStages * kSfCols <= 512 && kMaxN <= static_cast<int>(kAccCols), "TMEM columns");
+// warp 0 loads, 1 issues MMAs, 2 owns TMEM, 4..7 finish units
+constexpr int kThreads = 256;
 
 struct FewLayout {
-  size_t err, ticket, done1, done2, xs, x16, hs, h16, y, total;
+  size_t err, ticket, cnt1, done1, done2, xdone, clear_end, xq, xs, gq, gs, hq, hs, part, y, total;
+  int cols, parts;
+  int64_t groups;
 };
-FewLayout few_layout(int64_t T, int d, int k, int dff) {
+// Tokens up to 8 are columns by themselves, the same for every expert; more are gathered into
+// groups of up to 8 per expert.
+FewLayout few_layout(int64_t T, int d, int E, int k, int dff) {
   FewLayout L;
   size_t at = 0;
   const auto take = [&](size_t n) {
@@ -58,28 +61,41 @@ FewLayout few_layout(int64_t T, int d, int k, int dff) {
     at = (at + n + 255) / 256 * 256;
     return r;
   };
-  const size_t P = static_cast<size_t>(T) * k;
+  const size_t P = static_cast<size_t>(T) * k, G = T <= kTok && static_cast<size_t>(E) < P ? E : P;
+  const int stages = (d / 128 + kStageKt - 1) / kStageKt;
+  L.groups = static_cast<int64_t>(G);
+  L.cols = static_cast<int>(T < kTok ? T : kTok);
+  L.parts = (stages + kPartStages - 1) / kPartStages;
+  const size_t rows = static_cast<size_t>(L.cols) * kTerms;
   L.err = take(sizeof(DevErr));
   L.ticket = take(4);
-  L.done1 = take(kMaxRows * 4);
-  L.done2 = take(static_cast<size_t>(d / kUnitY) * 4);
-  L.xs = take(T * 4);
-  L.x16 = take(T * d * 2);
-  L.hs = take(P * (dff / 16) * 4);
-  L.h16 = take(P * dff * 2);
+  L.cnt1 = take(G * (dff / 32) * 4);
+  L.done1 = take(G * 4);
+  L.done2 = take(static_cast<size_t>(d / 32) * 4);
+  L.xdone = take(G * 4);
+  L.clear_end = at;
+  L.xq = take(T * kTerms * (d / 2));
+  // scale tiles [d / 128][512] of up to 8 tokens, or words [d / 128][T kTerms] of more
+  L.xs = take(T <= kTok ? static_cast<size_t>(d / 128) * kMxTileBytes : static_cast<size_t>(d / 128) * T * kTerms * 4);
+  L.gq = take(T <= kTok ? 0 : G * rows * (d / 2));
+  L.gs = take(T <= kTok ? 0 : G * (d / 128) * kMxTileBytes);
+  L.hq = take(G * rows * (dff / 2));
+  L.hs = take(G * (dff / 128) * kMxTileBytes);
+  L.part = take(P * (dff / 128) * 2 * L.parts * 128 * 4);
   L.y = take(P * d * 4);
   L.total = at;
   return L;
 }
 
-// Power of two that brings a largest magnitude (fp32 bits) into [2^14, 2^15), and its inverse;
-// held where both are normal numbers.
-__device__ __forceinline__ void f16_scale(uint32_t amax, float* mul, float* inv) {
-  int e = static_cast<int>(amax >> 23) - 127;
-  if (amax == 0u) e = 14;
-  e = max(e, -112);
-  *mul = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
-  *inv = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+// Scale byte of a term: the smallest power of two that keeps the block's largest magnitude
+// within E2M1's 6, so that no term saturates (255 for a block that is not finite).
+__device__ __forceinline__ uint32_t term_scale(uint32_t amax) {
+  const uint32_t s = mx_scale_byte(amax);
+  return s + ((amax & 0x7FFFFFu) > 0x400000u && amax >= 0x01000000u && s < 255u ? 1u : 0u);
+}
+// Byte of (row n < 48, block b of the 128-value tile) in a scale tile
+__device__ __forceinline__ uint32_t sf_at(int n, int b) {
+  return (n & 31) * 16 + (n >> 5) * 4 + b;
 }
 
 // ------------------------------------------------------------------------------ router
@@ -90,57 +106,74 @@ struct RouterParams {
   int T, d, E;
   DevErr* err;
   int32_t* clear;  // counters, contiguous
-  int n_clear;
-  float* xs;
-  uint16_t* x16;
+  int64_t n_clear;
+  uint8_t* xq;
+  uint8_t* xs;
 };
 
 constexpr int kRouterExperts = 2;  // per CTA
 constexpr int kRouterThreads = 256;
 
-// CTA b: token b as fp16 (b < T), then the logits of experts 2 b and 2 b + 1: warp w sums the
-// 128-value pieces w, w + 8, ... of d for every token, lanes then warps are added in a fixed
-// order.
+// CTA b: its share of the counters, token b in MXFP4 terms (b < T), then the logits of experts
+// 2 b and 2 b + 1: warp w sums the 128-value pieces w, w + 8, ... of d for every token, lanes
+// then warps are added in a fixed order.
 template <int TB>
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams p) {
   griddep_wait();
   __shared__ float red[8][TB][kRouterExperts];
-  __shared__ uint32_t amax_sh[8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (blockIdx.x == 0) {
-    for (int i = threadIdx.x; i < p.n_clear; i += kRouterThreads) p.clear[i] = 0;
-    if (threadIdx.x == 0) *p.err = DevErr{};
-  }
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(kRouterThreads) + threadIdx.x; i < p.n_clear;
+       i += static_cast<int64_t>(gridDim.x) * kRouterThreads)
+    p.clear[i] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = DevErr{};
   if (static_cast<int>(blockIdx.x) < p.T) {
-    const uint16_t* xr = p.x + static_cast<int64_t>(blockIdx.x) * p.d;
-    uint32_t amax = 0;
-    for (int c = threadIdx.x * 8; c < p.d; c += kRouterThreads * 8) {
-      const uint4 u = ld_v4(xr + c);
+    const int t = blockIdx.x, row_bytes = p.d / 2;
+    const uint16_t* xr = p.x + static_cast<int64_t>(t) * p.d;
+    for (int c0 = 0; c0 < p.d; c0 += kRouterThreads * 8) {  // d is a multiple of 128: whole blocks
+      const int c = c0 + threadIdx.x * 8;
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (c < p.d) u = ld_v4(xr + c);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        amax = max(amax, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
-    }
-    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-    if (lane == 0) amax_sh[warp] = amax;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = max(amax, amax_sh[i]);
-    float mul, inv;
-    f16_scale(amax, &mul, &inv);
-    uint16_t* o = p.x16 + static_cast<int64_t>(blockIdx.x) * p.d;
-    for (int c = threadIdx.x * 8; c < p.d; c += kRouterThreads * 8) {
-      const uint4 u = ld_v4(xr + c);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      uint32_t h[4];
+      float v[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const __half2 v = __floats2half2_rn(bf16lo(w[i]) * mul, bf16hi(w[i]) * mul);
-        h[i] = *reinterpret_cast<const uint32_t*>(&v);
+        v[2 * i] = bf16lo(w[i]);
+        v[2 * i + 1] = bf16hi(w[i]);
       }
-      st_v4(o + c, make_uint4(h[0], h[1], h[2], h[3]));
+#pragma unroll
+      for (int r = 0; r < kTerms; ++r) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+        amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+        const uint32_t s = term_scale(amax);
+        const float inv = mx_inverse_scale(s), f = mx_scale(s);
+        float z[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] = s == 255u ? 0.0f : v[i] * inv;
+        const uint32_t code = e2m1x8(z);
+        uint32_t h[4];
+        e2m1x8_to_half(code, h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+          v[2 * i] = fmaf(-q.x, f, v[2 * i]);  // exact: at most 24 bits are left
+          v[2 * i + 1] = fmaf(-q.y, f, v[2 * i + 1]);
+        }
+        const int n = t * kTerms + r;
+        if (c < p.d) {
+          *reinterpret_cast<uint32_t*>(p.xq + n * static_cast<int64_t>(row_bytes) + c / 2) = code;
+          if ((lane & 3) == 0) {
+            const int b = (c >> 5) & 3;
+            uint8_t* o = p.T <= kTok
+                             ? p.xs + static_cast<int64_t>(c >> 7) * kMxTileBytes + sf_at(n, b)
+                             : p.xs + (static_cast<int64_t>(c >> 7) * p.T * kTerms + n) * 4 + b;
+            *o = static_cast<uint8_t>(s);
+          }
+        }
+      }
     }
-    if (threadIdx.x == 0) p.xs[blockIdx.x] = inv;
   }
   if (!p.router) return;
   const int e0 = blockIdx.x * kRouterExperts;
@@ -201,36 +234,39 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams
 struct ExpertParams {
   const float* logits;
   int T, d, E, k, dff;
-  int tok;            // token columns kept per stage: min(T, 8)
+  int cols, n, parts;  // token columns, N of the MMAs, K ranges of W1 and W3
   int stages;
   uint32_t stage_bytes;
   const uint8_t *s1, *s3, *s2;
   int64_t s1_bytes, s2_bytes;  // scale bytes per expert
-  const float* xs;
-  const uint16_t* x16;
-  float* hs;
-  uint16_t* h16;
-  float* y;
+  const uint8_t *xq, *xs;      // the tokens' terms
+  uint8_t *gq, *gs, *hq, *hs;  // terms of gathered tokens and of h, per group
+  float *part, *y;
   uint16_t* out;
-  int32_t *ticket, *done1, *done2;
+  int32_t *ticket, *cnt1, *done1, *done2, *xdone;
   DevErr* err;
   uint64_t wait_ns;
-  // W1 and W3: boxes of 16 rows (8 j + i, i < 4) of 128 bytes, W2: of 32 rows; where a row is a
-  // whole number of 128-byte pieces (wide), a box holds four of them side by side
-  CUtensorMap map1, map3, map2;
+  // codes of W1, W3, W2 (boxes of 128 rows) and of x and h terms (boxes of n rows), 128 bytes
+  // wide; where rows are whole numbers of 128-byte pieces (wide) a box holds two of them
+  CUtensorMap map1, map3, map2, mapx, maph;
   int wide1, wide2;
 };
 
-// A unit's token group: expert, tokens (bits), first row of its h and y rows.
+// Up to 8 tokens of an expert: their bits, and the row of the first in `part` and y.
 struct Group {
   int32_t e;
   uint32_t tokens;
   int32_t row0;
   int32_t n;
 };
+struct Unit {
+  int32_t kind;  // 0: no more work, 1: W1 or W3 rows, 2: W2 rows
+  int32_t group, tile, q;  // q: matrix + 2 * K range
+};
 struct StageMeta {
-  int32_t kind;  // 0: no more work, 1: h unit, 2: y unit
-  int32_t group, tile, ks;
+  Unit u;
+  int32_t nkt;    // K tiles of this stage
+  int32_t flags;  // 1: first stage of its unit, 2: last
 };
 
 struct Shared {
@@ -240,19 +276,19 @@ struct Shared {
   float gate[kMaxT][kMaxK];
   uint16_t slot_e[kMaxT][kMaxK];
   StageMeta meta[kMaxStages];
-  uint64_t bars[3 * kMaxStages + 2 * kEpi];
-  StageMeta unit[kEpi];  // the unit whose partial sums a buffer holds
+  Unit acc_unit[2];
+  uint64_t bars[2 * kMaxStages + 5];
   int32_t groups;
   int32_t abort_flag;
+  uint32_t tmem;
 };
-// behind Shared: kEpi buffers of partial sums [word][token][32 rows]
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, uint32_t bar, int x,
-                                            int y, int z, int w) {
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint32_t bar, int x,
@@ -262,93 +298,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint3
       " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
-}
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ float2 lds_f2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(a));
-  return v;
-}
-// byte i of a scale word as a factor (0 stands for 2^-127, which is 0 beside any other
-// block; 255 is handled for the whole row)
-__device__ __forceinline__ float scale_of(uint32_t w, int i) {
-  return __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
-}
-
-// One stage of one warp: word w of the scales, i.e. 4 blocks of 32 values, for one 16-row half
-// (`rows`: its 16 x 128-byte box, `sc`: its words).  KIND 2: the activations' own factors (16
-// values each) are applied to the two halves of a block.
-template <int KIND>
-__device__ __forceinline__ void multiply(uint32_t rows, uint32_t sc, uint32_t act, uint32_t hs,
-                                         int w, int lane, int tok, float (&acc)[4],
-                                         uint32_t (&bad)[2]) {
-  const int g = lane >> 2, t = lane & 3;
-  const uint32_t r0 = rows + g * 128 + 4 * t;
-  const uint32_t b0 = act + min(g, tok - 1) * kActRow + (w * 128 + 8 * t) * 2;
-  const uint32_t h0 = hs + min(2 * t, tok - 1) * kHsRow + w * 32;
-  const uint32_t h1 = hs + min(2 * t + 1, tok - 1) * kHsRow + w * 32;
-  // every shared-memory read of the stage first: a warp has little else to hide their latency
-  uint32_t wv[4][2];
-  uint4 x[4];
-  float2 f0[4], f1[4];
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const uint32_t chunk = (((w & 1) * 4 + b) ^ g) << 4;
-    wv[b][0] = lds32(r0 + chunk);
-    wv[b][1] = lds32(r0 + 1024 + chunk);
-    x[b] = lds128(b0 + b * 64);
-    if constexpr (KIND == 2) {
-      f0[b] = lds_f2(h0 + b * 8);
-      f1[b] = lds_f2(h1 + b * 8);
-    }
-  }
-  const uint32_t slo = lds32(sc + g * 4), shi = lds32(sc + (8 + g) * 4);
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    uint32_t a[4], c[4];
-    e2m1x8_to_half(wv[b][0], a);
-    e2m1x8_to_half(wv[b][1], c);
-    float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    mma_f16(p, a[0], c[0], a[1], c[1], x[b].x, x[b].y);
-    if constexpr (KIND == 2) {
-      float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma_f16(q, a[2], c[2], a[3], c[3], x[b].z, x[b].w);
-      p[0] = fmaf(q[0], f0[b].y, p[0] * f0[b].x);
-      p[1] = fmaf(q[1], f1[b].y, p[1] * f1[b].x);
-      p[2] = fmaf(q[2], f0[b].y, p[2] * f0[b].x);
-      p[3] = fmaf(q[3], f1[b].y, p[3] * f1[b].x);
-    } else {
-      mma_f16(p, a[2], c[2], a[3], c[3], x[b].z, x[b].w);
-    }
-    acc[0] = fmaf(p[0], scale_of(slo, b), acc[0]);
-    acc[1] = fmaf(p[1], scale_of(slo, b), acc[1]);
-    acc[2] = fmaf(p[2], scale_of(shi, b), acc[2]);
-    acc[3] = fmaf(p[3], scale_of(shi, b), acc[3]);
-  }
-  bad[0] |= __vcmpeq4(slo, 0xFFFFFFFFu);
-  bad[1] |= __vcmpeq4(shi, 0xFFFFFFFFu);
 }
 
 template <int EPL>
@@ -373,6 +322,41 @@ __device__ __forceinline__ int row_of(const Shared& sh, int t, int j) {
   return sh.base[e] + __popc(sh.mask[e] & ((1u << t) - 1u));
 }
 
+// Rows of gathered tokens: the terms of a group's tokens and their scale words, in the layout
+// that h has.  By one warp.
+__device__ void gather_group(const ExpertParams& p, const Shared& sh, int gi, int lane) {
+  const Group gr = sh.group[gi];
+  const int row_bytes = p.d / 2, kt = p.d / 128, rows = p.cols * kTerms;
+  uint32_t left = gr.tokens;
+  for (int c = 0; c < gr.n; ++c, left &= left - 1u) {
+    const int t = __ffs(left) - 1;
+    // a token's terms are neighbours on both sides
+    const uint8_t* src = p.xq + static_cast<int64_t>(t) * kTerms * row_bytes;
+    uint8_t* dst = p.gq + (static_cast<int64_t>(gi) * rows + c * kTerms) * row_bytes;
+    const int n16 = kTerms * row_bytes / 16;
+    for (int i = lane; i < n16; i += 32 * 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + 32 * j < n16) v[j] = ld_v4(src + 16 * (i + 32 * j));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (i + 32 * j < n16) st_v4(dst + 16 * (i + 32 * j), v[j]);
+    }
+    for (int i = lane; i < kt * kTerms; i += 32) {
+      const int tile = i / kTerms, r = i % kTerms;
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(
+          p.xs + (static_cast<int64_t>(tile) * p.T * kTerms + t * kTerms + r) * 4);
+      *reinterpret_cast<uint32_t*>(p.gs + (static_cast<int64_t>(gi) * kt + tile) * kMxTileBytes +
+                                   sf_at(c * kTerms + r, 0)) = w;
+    }
+  }
+  fence_proxy_async_global();
+  __threadfence();
+  __syncwarp();
+  if (lane == 0) red_release_add(p.xdone + gi, 1);
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     few_experts_kernel(const __grid_constant__ ExpertParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -381,32 +365,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   Shared& sh = *reinterpret_cast<Shared*>(
       smem_raw + (base - raw) + static_cast<size_t>(p.stages) * p.stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.stages;
-  const auto full = [&](int s) { return smem_u32(&sh.bars[s]); };
-  const auto empty = [&](int s) { return smem_u32(&sh.bars[kMaxStages + s]); };
-  const auto told = [&](int s) { return smem_u32(&sh.bars[2 * kMaxStages + s]); };
-  const auto rfull = [&](int i) { return smem_u32(&sh.bars[3 * kMaxStages + i]); };
-  const auto rfree = [&](int i) { return smem_u32(&sh.bars[3 * kMaxStages + kEpi + i]); };
-  float* red = reinterpret_cast<float*>(&sh + 1);
-  const int red_floats = kParts * p.tok * 32;
+  const uint32_t S = p.stages;
+  const auto full = [&](uint32_t s) { return smem_u32(&sh.bars[s]); };
+  const auto empty = [&](uint32_t s) { return smem_u32(&sh.bars[kMaxStages + s]); };
+  const auto tfull = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + a]); };
+  const auto tempty = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + 2 + a]); };
+  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 4]);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&sh.abort_flag);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(full(s), 33);  // the weights' producer with the bytes, 32 lanes' own copies
-      mbar_init(empty(s), kCons);
-      mbar_init(told(s), 1);   // the stage's meta is written
+    for (uint32_t s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
     }
-    for (int i = 0; i < kEpi; ++i) {
-      mbar_init(rfull(i), kCons);
-      mbar_init(rfree(i), 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 2);   // the accumulator is complete, its unit is written down
+      mbar_init(tempty(a), 4);
     }
+    mbar_init(drain, 1);
     fence_mbar_init();
     sh.abort_flag = 0;
     tma_prefetch_desc(&p.map1);
     tma_prefetch_desc(&p.map3);
     tma_prefetch_desc(&p.map2);
+    tma_prefetch_desc(&p.mapx);
+    tma_prefetch_desc(&p.maph);
   }
+  if (warp == 2) tmem_alloc(smem_u32(&sh.tmem), 512);
   for (int e = threadIdx.x; e < p.E; e += kThreads) sh.mask[e] = 0u;
   __syncthreads();
   griddep_wait();
@@ -451,271 +436,271 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) sh.groups = groups;
   }
+  tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const bool direct = p.T <= kTok;  // column = token; else column = place in the group
   const int groups = sh.groups;
-  const int hu = p.dff / kUnitH, yu = p.d / kUnitY;
-  const int n1 = groups * hu, n_units = n1 + groups * yu;
-  const int kt1 = p.d / 128, kt2 = p.dff / 128;  // scale words per row
+  const int ht = p.dff / 128, yt = p.d / 128, Q = 2 * p.parts;
+  const int n0 = direct ? 0 : groups, n1 = n0 + groups * ht * Q, n_units = n1 + groups * yt;
+  const int kt1 = p.d / 128, kt2 = p.dff / 128;
+  const int st1 = (kt1 + kStageKt - 1) / kStageKt, st2 = (kt2 + kStageKt - 1) / kStageKt;
 
   if (warp == 0) {
-    // ---------------------------------------------------------------- weights
-    if (lane == 0) {
-      uint32_t it = 0, s = 0, phase = 1;  // phase: parity of the empty barrier's last use
-      bool ok = true;
-      int next = atomicAdd(p.ticket, 1);
-      while (true) {
-        const int u = next;
-        const bool work = u < n_units;
-        if (work) next = atomicAdd(p.ticket, 1);  // used after this unit's loads
-        const bool first = u < n1;
-        const int v = first ? u : u - n1, per = first ? hu : yu;
-        const int gi = v / per, tile = v % per;
-        const int kt = work ? (first ? kt1 : kt2) : 1;
-        const int e = work ? sh.group[gi].e : 0;
-        const CUtensorMap* ma = first ? &p.map1 : &p.map2;
+    // ---------------------------------------------------------------- loads
+    uint32_t it = 0, s = 0, phase = 1;
+    bool ok = true;
+    int next = 0;
+    if (lane == 0) next = atomicAdd(p.ticket, 1);
+    while (true) {
+      const int u = __shfl_sync(0xFFFFFFFFu, next, 0);
+      const bool work = u < n_units;
+      if (lane == 0 && work) next = atomicAdd(p.ticket, 1);  // used after this unit's loads
+      if (u < n0) {
+        gather_group(p, sh, u, lane);
+        continue;
+      }
+      if (lane == 0) {
+        Unit un = {0, 0, 0, 0};
+        int ks0 = 0, ks1 = 1;
+        if (work && u < n1) {
+          const int v = u - n0, w = v % (ht * Q);
+          un = Unit{1, v / (ht * Q), w / Q, w % Q};
+          ks0 = st1 * (un.q >> 1) / p.parts;
+          ks1 = st1 * ((un.q >> 1) + 1) / p.parts;
+        } else if (work) {
+          un = Unit{2, (u - n1) / yt, (u - n1) % yt, 0};
+          ks1 = st2;
+        }
+        const int e = sh.group[un.group].e;
+        const bool first = un.kind == 1;
         const bool wide = first ? p.wide1 : p.wide2;
-        const int y = first ? 4 * (tile & 1) : e * p.d + kUnitY * tile;
-        const int z = e * (p.dff / 8) + 4 * (tile >> 1);
-        for (int ks = 0; 8 * ks < kt; ++ks) {
-          if (it >= static_cast<uint32_t>(S))
-            ok = mbar_wait(empty(s), phase, abort_flag, p.err, 70, p.wait_ns);
+        const int kt = first ? kt1 : kt2;
+        const CUtensorMap* mw = first ? ((un.q & 1) ? &p.map3 : &p.map1) : &p.map2;
+        const CUtensorMap* mx = first ? &p.mapx : &p.maph;
+        const int wrow = (first ? e * p.dff : e * p.d) + 128 * un.tile;
+        const int xrow = first && direct ? 0 : un.group * p.cols * kTerms;
+        const uint8_t* sfa =
+            (first ? ((un.q & 1) ? p.s3 : p.s1) + e * p.s1_bytes : p.s2 + e * p.s2_bytes) +
+            static_cast<int64_t>(un.tile) * kt * kMxTileBytes;
+        const uint8_t* sfb = first ? (direct ? p.xs : p.gs + static_cast<int64_t>(un.group) * kt * kMxTileBytes)
+                                   : p.hs + static_cast<int64_t>(un.group) * kt * kMxTileBytes;
+        // what the activations have to wait for: a y unit for all h of its group (four 32-row
+        // quarters per tile), an h unit for its gathered tokens
+        const int32_t* flag = first ? (direct ? nullptr : p.xdone + un.group) : p.done1 + un.group;
+        const int target = first ? 1 : 4 * ht;
+        const uint32_t bbytes = p.n * 128u;
+        for (int ks = ks0; ks < ks1; ++ks) {
+          if (it >= S) ok = mbar_wait(empty(s), phase, abort_flag, p.err, 70, p.wait_ns);
           if (!ok) break;
-          sh.meta[s] = StageMeta{work ? (first ? 1 : 2) : 0, gi, tile, ks};
-          mbar_arrive(told(s));
-          const uint32_t st = base + s * p.stage_bytes;
-          const int boxes = work ? (min(8, kt - 8 * ks) + 1) / 2 : 0;
+          const int nkt = min(kStageKt, kt - kStageKt * ks);
+          sh.meta[s] = StageMeta{un, nkt, (ks == ks0 ? 1 : 0) | (ks == ks1 - 1 ? 2 : 0)};
+          const uint32_t st = base + s * p.stage_bytes, stb = st + kABytes;
+          const uint32_t ssa = stb + 2 * bbytes, ssb = ssa + kSfBytes;
+          const int pieces = (nkt + 1) / 2;
           if (!work) {
             mbar_arrive(full(s));
-          } else if (wide) {
-            mbar_arrive_expect_tx(full(s), kWBytes);  // pieces past the row's end are zeros
-            if (first) {
-              tma_load_4d(st, ma, full(s), 0, y, z, 4 * ks);
-              tma_load_4d(st + kWBytes / 2, &p.map3, full(s), 0, y, z, 4 * ks);
-            } else {
-              tma_load_3d(st, ma, full(s), 0, y, 4 * ks);
-            }
           } else {
-            mbar_arrive_expect_tx(full(s), boxes * 4096);
-            for (int c = 0; c < boxes; ++c) {
-              const int x = ks * (kStageK / 2) + 128 * c;
-              if (first) {
-                tma_load_3d(st + 2048 * c, ma, full(s), x, y, z);
-                tma_load_3d(st + kWBytes / 2 + 2048 * c, &p.map3, full(s), x, y, z);
-              } else {
-                tma_load_2d(st + 4096 * c, ma, full(s), x, y);
-              }
+            const uint32_t code_bytes = wide ? kABytes + 2 * bbytes : pieces * (kABytes / 2 + bbytes);
+            mbar_arrive_expect_tx(full(s), code_bytes + 2 * nkt * kMxTileBytes);
+            if (wide) {
+              tma_load_3d(st, mw, full(s), 0, wrow, 2 * ks);  // pieces past the row's end are zeros
+            } else {
+              for (int c = 0; c < pieces; ++c)
+                tma_load_2d(st + c * (kABytes / 2), mw, full(s), (2 * ks + c) * 128, wrow);
             }
+            bulk_load(ssa, sfa + static_cast<int64_t>(ks) * kSfBytes, nkt * kMxTileBytes, full(s));
+            if (flag) {
+              wait_count(flag, target, abort_flag, p.err, 71, p.wait_ns);
+              fence_proxy_async_global();
+              flag = nullptr;
+            }
+            if (wide) {
+              tma_load_3d(stb, mx, full(s), 0, xrow, 2 * ks);
+            } else {
+              for (int c = 0; c < pieces; ++c)
+                tma_load_2d(stb + c * bbytes, mx, full(s), (2 * ks + c) * 128, xrow);
+            }
+            bulk_load(ssb, sfb + static_cast<int64_t>(ks) * kSfBytes, nkt * kMxTileBytes, full(s));
           }
           ++it;
-          if (++s == static_cast<uint32_t>(S)) {
+          if (++s == S) {
             s = 0;
             phase ^= 1;
           }
         }
-        if (!ok || !work) break;
       }
-      // copies still in flight land before the CTA ends
-      if (*abort_flag)
-        for (uint32_t i = it > static_cast<uint32_t>(S) ? it - S : 0; i < it; ++i)
-          mbar_wait(full(i % S), (i / S) & 1, nullptr, p.err, 72, p.wait_ns);
+      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      if (!ok || !work) break;
     }
-  } else if (warp == kThreads / 32 - 1) {
-    // ---------------------------------------------------------------- scales, activations
-    uint32_t s = 0, phase = 0;
-    while (true) {
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(told(s), phase, abort_flag, p.err, 76, p.wait_ns)))
-        break;
-      const StageMeta m = sh.meta[s];
-      if (m.kind == 0) {
-        mbar_arrive(full(s));
-        break;
+    // copies still in flight land before the CTA ends
+    if (lane == 0 && *abort_flag)
+      for (uint32_t i = it > S ? it - S : 0; i < it; ++i)
+        mbar_wait(full(i % S), (i / S) & 1, nullptr, p.err, 72, p.wait_ns);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMAs
+    if (lane == 0) {
+      uint32_t s = 0, phase = 0, units = 0;
+      const uint32_t idesc = idesc_mxf4(128, p.n);
+      const uint32_t bbytes = p.n * 128u;
+      while (true) {
+        if (!mbar_wait(full(s), phase, abort_flag, p.err, 73, p.wait_ns)) break;
+        tc_fence_after();
+        const StageMeta m = sh.meta[s];
+        const uint32_t acc = units & 1, tacc = tmem + acc * kAccCols;
+        if ((m.flags & 1) && units >= 2) {
+          if (!mbar_wait(tempty(acc), (units / 2 - 1) & 1, abort_flag, p.err, 74, p.wait_ns)) break;
+          tc_fence_after();
+        }
+        if (m.u.kind == 0) {
+          sh.acc_unit[acc] = m.u;
+          mbar_arrive(tfull(acc));
+          mbar_arrive(tfull(acc));
+          break;
+        }
+        const uint32_t st = base + s * p.stage_bytes, stb = st + kABytes;
+        const uint32_t ssa = stb + 2 * bbytes, ssb = ssa + kSfBytes;
+        const uint32_t tsf = tmem + kSfCol0 + s * kSfCols;
+        for (int i = 0; i < m.nkt; ++i) {
+          tmem_cp_scales(tsf + 4 * i, ssa + i * kMxTileBytes);
+          tmem_cp_scales(tsf + 4 * kStageKt + 4 * i, ssb + i * kMxTileBytes);
+        }
+        for (int j = 0; j < 2 * m.nkt; ++j) {
+          const uint32_t id = (j & 1) * 2;
+          umma_mxf4(tacc, smem_desc_sw128(st + (j >> 2) * (kABytes / 2), 16, 1024) + 2 * (j & 3),
+                    smem_desc_sw128(stb + (j >> 2) * bbytes, 16, 1024) + 2 * (j & 3),
+                    idesc | (id << 4) | (id << 29), tsf + 4 * (j >> 1),
+                    tsf + 4 * kStageKt + 4 * (j >> 1), !(m.flags & 1) || j > 0);
+        }
+        umma_commit(empty(s));
+        if (m.flags & 2) {
+          sh.acc_unit[acc] = m.u;
+          umma_commit(tfull(acc));
+          mbar_arrive(tfull(acc));
+          ++units;
+        }
+        if (++s == S) {
+          s = 0;
+          phase ^= 1;
+        }
       }
-      const bool first = m.kind == 1;
-      const Group gr = sh.group[m.group];
-      const int kt = first ? kt1 : kt2;
-      const int words = min(8, kt - 8 * m.ks);
-      const uint32_t sc = base + s * p.stage_bytes + kWBytes;
-      const uint32_t act = sc + kScBytes, hsm = act + p.tok * kActRow;
-      {
-        // this lane's weight row
-        const int r = first ? 32 * (m.tile >> 1) + 8 * ((lane & 15) >> 2) + 4 * (m.tile & 1) + (lane & 3)
-                            : kUnitY * m.tile + lane;
-        const uint8_t* sp =
-            (first ? (lane < 16 ? p.s1 : p.s3) + gr.e * p.s1_bytes : p.s2 + gr.e * p.s2_bytes) +
-            (static_cast<int64_t>(r >> 7) * kt + 8 * m.ks) * kMxTileBytes + (r & 31) * 16 +
-            ((r >> 5) & 3) * 4;
-        const uint32_t dst = sc + lane * 4;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (j < words) cp_async_4(dst + j * 128, sp + j * kMxTileBytes);
-      }
-      // a y unit's activations are there once all h units of its group are
-      if (!first && m.ks == 0 &&
-          !__all_sync(0xFFFFFFFFu, wait_count(p.done1 + m.group, hu, abort_flag, p.err, 71, p.wait_ns)))
-        break;
-      uint32_t left = gr.tokens;
-      for (int i = 0; i < gr.n; ++i, left &= left - 1u) {
-        const uint16_t* src =
-            (first ? p.x16 + static_cast<int64_t>(__ffs(left) - 1) * p.d
-                   : p.h16 + static_cast<int64_t>(gr.row0 + i) * p.dff) + m.ks * kStageK + lane * 8;
-        const uint32_t dst = act + i * kActRow + lane * 16;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)  // a word of scales stands for 16 pieces of 16 bytes
-          if (j * 32 + lane < words * 16) cp_async_16(dst + j * 512, src + j * 256);
-      }
-      if (!first) {
-        // the factors of 16 values each: 32 bytes per word, two pieces of 16 bytes
-        for (int i = lane; i < gr.n * 16; i += 32)
-          if ((i & 15) < words * 2)
-            cp_async_16(hsm + (i >> 4) * kHsRow + (i & 15) * 16,
-                        p.hs + static_cast<int64_t>(gr.row0 + (i >> 4)) * (p.dff / 16) +
-                            m.ks * (kStageK / 16) + (i & 15) * 4);
-      }
-      cp_async_arrive_noinc(full(s));
-      if (++s == static_cast<uint32_t>(S)) {
-        s = 0;
-        phase ^= 1;
-      }
+      umma_commit(drain);  // every MMA issued is complete before TMEM is freed
+      mbar_wait(drain, 0, nullptr, p.err, 75, p.wait_ns);
     }
-    cp_async_wait_all();
-  } else if (warp <= kCons) {
-    // ---------------------------------------------------------------- consumers
-    const int w = (warp - 1) & 7, half = (warp - 1) >> 3, g = lane >> 2, tc = 2 * (lane & 3);
-    float acc[4] = {};
-    uint32_t bad[2] = {};
-    uint32_t units = 0, s = 0, phase = 0;
-    while (true) {
-      if (!mbar_wait(full(s), phase, abort_flag, p.err, 73, p.wait_ns)) break;
-      const StageMeta m = sh.meta[s];
-      if (m.kind == 0) break;
-      const uint32_t st = base + s * p.stage_bytes;
-      const uint32_t sc = st + kWBytes, act = sc + kScBytes, hsm = act + p.tok * kActRow;
-      const int kt = m.kind == 1 ? kt1 : kt2;
-      if (8 * m.ks + w < kt) {
-        const uint32_t scw = sc + (w * 32 + half * 16) * 4;
-        // h: [W1 | W3] of four 16-row boxes each; y: four 32-row boxes
-        if (m.kind == 1)
-          multiply<1>(st + half * (kWBytes / 2) + (w >> 1) * 2048, scw, act, hsm, w, lane, p.tok, acc, bad);
-        else
-          multiply<2>(st + (w >> 1) * 4096 + half * 2048, scw, act, hsm, w, lane, p.tok, acc, bad);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(empty(s));
-      if (++s == static_cast<uint32_t>(S)) {
-        s = 0;
-        phase ^= 1;
-      }
-      if (8 * (m.ks + 1) < kt) continue;
-
-      // end of a unit: the partial sums go to the epilogue warp whose turn it is
-      const int buf = units % kEpi;
-      if (units >= kEpi &&
-          !mbar_wait(rfree(buf), (units / kEpi - 1) & 1, abort_flag, p.err, 74, p.wait_ns))
-        break;
-      float* r = red + buf * red_floats + w * p.tok * 32;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (bad[i >> 1]) acc[i] = __uint_as_float(0x7FC00000u);  // a NaN scale in the row
-        const int n = tc + (i & 1);
-        if (n < p.tok) r[n * 32 + 16 * half + 8 * (i >> 1) + g] = acc[i];
-        acc[i] = 0.0f;
-      }
-      bad[0] = bad[1] = 0u;
-      if (warp == 1 && lane == 0) sh.unit[buf] = m;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(rfull(buf));
-      ++units;
-    }
-    // no more units: each epilogue warp gets an empty one
-    if (!*abort_flag && warp <= kEpi) {
-      const uint32_t last = units + warp - 1;
-      const int buf = last % kEpi;
-      // all warps have written every unit that this one follows
-      bool ok = true;
-      if (last >= kEpi)
-        ok = mbar_wait(rfree(buf), (last / kEpi - 1) & 1, abort_flag, p.err, 74, p.wait_ns);
-      if (ok && lane == 0) {
-        sh.unit[buf].kind = 0;
-        for (int i = 0; i < kCons; ++i) mbar_arrive(rfull(buf));
-      }
-    }
-  } else {
-    // ---------------------------------------------------------------- epilogue
-    const int ew = warp - 1 - kCons;
-    const float* r = red + ew * red_floats;
+  } else if (warp >= 4) {
+    // ---------------------------------------------------------------- finishing units
+    const int qd = warp - 4;  // rows 32 qd .. of the tile
     for (uint32_t i = 0;; ++i) {
-      if (!mbar_wait(rfull(ew), i & 1, abort_flag, p.err, 75, p.wait_ns)) break;
-      const StageMeta m = sh.unit[ew];
-      if (m.kind == 0) break;
-      const Group& gr = sh.group[m.group];
-      if (m.kind == 1) {
-        // two tokens at a time, 16 columns of h each: rows 0..15 are W1's sums, 16..31 W3's
-        const int c = lane & 15;
-        uint32_t tokens = gr.tokens;
-        for (int n0 = 0; n0 < gr.n; n0 += 2) {
-          const int n = n0 + (lane >> 4);
-          float h = 0.0f;
-          if (n < gr.n) {
-            const float* rn = r + n * 32 + c;
-            float a = 0.0f, b = 0.0f;
+      const uint32_t acc = i & 1;
+      if (!mbar_wait(tfull(acc), (i >> 1) & 1, abort_flag, p.err, 76, p.wait_ns)) break;
+      const Unit un = sh.acc_unit[acc];
+      if (un.kind == 0) break;
+      tc_fence_after();
+      const uint32_t tacc = tmem + acc * kAccCols + (static_cast<uint32_t>(32 * qd) << 16);
+      float v[kMaxN];
 #pragma unroll
-            for (int v = 0; v < kParts; ++v) {
-              a += rn[v * p.tok * 32];
-              b += rn[v * p.tok * 32 + 16];
-            }
-            const uint32_t tk = (lane >> 4) ? tokens & (tokens - 1u) : tokens;
-            const float xs = __ldg(p.xs + __ffs(tk) - 1);
-            a *= xs;
-            b *= xs;
-            h = a / (1.0f + expf(-a)) * b;
-          }
-          tokens &= tokens - 1u;
-          tokens &= tokens - 1u;
-          uint32_t amax = __float_as_uint(h) & 0x7FFFFFFFu;
+      for (int c = 0; c < kMaxN; c += 16) {
+        float x[16];
+        if (c < p.n) {
+          tmem_ld16(tacc + c, x);
 #pragma unroll
-          for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-          float mul, inv;
-          f16_scale(amax, &mul, &inv);
-          if (n < gr.n) {
-            const int64_t row = gr.row0 + n;
-            p.h16[row * p.dff + 32 * (m.tile >> 1) + 8 * (c >> 2) + 4 * (m.tile & 1) + (c & 3)] =
-                __half_as_ushort(__float2half_rn(h * mul));
-            if (c == 0) p.hs[row * (p.dff / 16) + m.tile] = inv;
-          }
+          for (int j = 0; j < 16; ++j) v[c + j] = x[j];
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(rfree(ew));
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) red_release_add(p.done1 + m.group, 1);
-      } else {
-        const int col = kUnitY * m.tile + lane;
-        for (int n = 0; n < gr.n; ++n) {
-          const float* rn = r + n * 32 + lane;
-          float v = 0.0f;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty(acc));
+      const Group gr = sh.group[un.group];
+      const auto active = [&](int c) { return direct ? ((gr.tokens >> c) & 1u) != 0u : c < gr.n; };
+      const auto row_at = [&](int c) {
+        return gr.row0 + (direct ? __popc(gr.tokens & ((1u << c) - 1u)) : c);
+      };
+      const auto sum = [&](int c) {  // the terms' products, the smallest first
+        float a = v[c * kTerms + kTerms - 1];
 #pragma unroll
-          for (int i2 = 0; i2 < kParts; ++i2) v += rn[i2 * p.tok * 32];
-          __stcg(p.y + static_cast<int64_t>(gr.row0 + n) * p.d + col, v);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(rfree(ew));
+        for (int r = kTerms - 2; r >= 0; --r) a += v[c * kTerms + r];
+        return a;
+      };
+      if (un.kind == 1) {
+        // this K range's sums of 32 columns of x W1 or x W3
+        float* slot = p.part + 32 * qd + lane;
+        const int64_t at = static_cast<int64_t>(un.tile) * Q;  // of a row's ht * Q slots of 128
+#pragma unroll
+        for (int c = 0; c < kTok; ++c)
+          if (active(c))
+            __stcg(slot + ((row_at(c) * static_cast<int64_t>(ht) * Q) + at + un.q) * 128, sum(c));
         __threadfence();
         __syncwarp();
         int last = 0;
-        if (lane == 0) last = atomicAdd(p.done2 + m.tile, gr.n) + gr.n == p.T * p.k;
-        if (__shfl_sync(0xFFFFFFFFu, last, 0)) {
-          // the last rows of these 32 columns: combine them, in slot order
-          __threadfence();
-          for (int t = 0; t < p.T; ++t) {
-            float o = 0.0f;
-            for (int j = 0; j < p.k; ++j)
-              o = fmaf(sh.gate[t][j],
-                       __ldcg(p.y + static_cast<int64_t>(row_of(sh, t, j)) * p.d + col), o);
-            p.out[static_cast<int64_t>(t) * p.d + col] = bf16_bits(o);
+        if (lane == 0)
+          last = atomicAdd(p.cnt1 + (un.group * ht + un.tile) * 4 + qd, 1) == Q - 1;
+        if (!__shfl_sync(0xFFFFFFFFu, last, 0)) continue;
+        __threadfence();
+        // all ranges of both are there: h of a 32-value block per token, in MXFP4 terms
+        const int row_bytes = p.dff / 2;
+        for (int c = 0; c < p.cols; ++c) {
+          if (!active(c)) continue;
+          const float* src = slot + ((row_at(c) * static_cast<int64_t>(ht) * Q) + at) * 128;
+          float a = 0.0f, b = 0.0f;
+          for (int q = 0; q < p.parts; ++q) {
+            a += __ldcg(src + (2 * q) * 128);
+            b += __ldcg(src + (2 * q + 1) * 128);
           }
+          float h = a / (1.0f + expf(-a)) * b;
+          uint8_t* hq = p.hq + (static_cast<int64_t>(un.group) * p.cols + c) * kTerms * row_bytes +
+                        64 * un.tile + 16 * qd;
+          uint8_t* hs = p.hs + (static_cast<int64_t>(un.group) * ht + un.tile) * kMxTileBytes;
+#pragma unroll
+          for (int r = 0; r < kTerms; ++r) {
+            const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
+            const uint32_t s = term_scale(amax);
+            float z[8] = {s == 255u ? 0.0f : h * mx_inverse_scale(s), 0, 0, 0, 0, 0, 0, 0};
+            uint32_t code = e2m1x8(z) & 15u;
+            uint32_t hh[4];
+            e2m1x8_to_half(code, hh);
+            h = fmaf(-__half2float(__ushort_as_half(static_cast<uint16_t>(hh[0]))), mx_scale(s), h);
+            // eight lanes' codes in the first one's word
+            code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
+            code |= __shfl_down_sync(0xFFFFFFFFu, code, 2) << 8;
+            code |= __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16;
+            if ((lane & 7) == 0)
+              *reinterpret_cast<uint32_t*>(hq + r * static_cast<int64_t>(row_bytes) + lane / 2) = code;
+            if (lane == 0) hs[sf_at(c * kTerms + r, qd)] = static_cast<uint8_t>(s);
+          }
+        }
+        fence_proxy_async_global();
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) red_release_add(p.done1 + un.group, 1);
+      } else {
+        const int col = 128 * un.tile + 32 * qd + lane;
+#pragma unroll
+        for (int c = 0; c < kTok; ++c)
+          if (active(c)) __stcg(p.y + static_cast<int64_t>(row_at(c)) * p.d + col, sum(c));
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0)
+          last = atomicAdd(p.done2 + 4 * un.tile + qd, gr.n) + gr.n == p.T * p.k;
+        if (!__shfl_sync(0xFFFFFFFFu, last, 0)) continue;
+        __threadfence();
+        // the last rows of these 32 columns: combine them, in slot order
+        for (int t = 0; t < p.T; ++t) {
+          float o = 0.0f;
+          for (int j = 0; j < p.k; ++j)
+            o = fmaf(sh.gate[t][j],
+                     __ldcg(p.y + static_cast<int64_t>(row_of(sh, t, j)) * p.d + col), o);
+          p.out[static_cast<int64_t>(t) * p.d + col] = bf16_bits(o);
         }
       }
     }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
 }
 
@@ -730,39 +715,25 @@ moe_status_t check_few(int64_t T, int d, int E, int k, int dff) {
   return MOE_OK;
 }
 
-// Map of weight rows for units of h (16 rows 8 j + i, i < 4: the half of a 32-row block that
-// shares a factor of h) or of y (32 rows), 128-byte swizzle.  `pieces` (a row is a whole number
-// of 128-byte pieces): the pieces are an outer dimension, and a box holds four of them, so a
-// stage is one copy per matrix; issuing eight 2 KB boxes per stage instead took the producer
-// 1700 cycles, over twice the stage's share of the memory time.  Otherwise a box is one piece,
-// zeros past the row's end.
-CUtensorMap make_weight_map(const void* base, uint64_t inner, uint64_t rows, bool h, bool pieces,
-                            cudaError_t* st) {
+// Map of `rows` rows of `inner` bytes, boxes of 128 bytes x box_rows, 128-byte swizzle.  `wide`:
+// inner is a multiple of 128; the 128-byte pieces of a row are an outer dimension and a box
+// holds two, so a stage is one copy.  (Issuing a copy takes its thread some 170 cycles: eight of
+// them per 16 KB stage held the stream at 2 TB/s.)  Otherwise a box is one piece, zeros past the
+// row's end.
+CUtensorMap make_piece_map(const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
+                           bool wide, cudaError_t* st) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   CUtensorMap m = {};
   auto enc = reinterpret_cast<Encode>(tensor_map_encoder());
-  cuuint64_t dims[4], strides[3];
-  cuuint32_t box[4];
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  cuuint32_t n = 0;
-  const auto dim = [&](uint64_t size, uint64_t stride, uint32_t b) {
-    dims[n] = size;
-    if (n) strides[n - 1] = stride;
-    box[n++] = b;
-  };
-  dim(pieces ? 128 : inner, 1, 128);
-  if (h) {
-    dim(8, inner, 4);
-    dim(rows / 8, 8 * inner, 4);
-  } else {
-    dim(rows, inner, 32);
-  }
-  if (pieces) dim(inner / 128, 128, 4);
-  if (!enc || enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, n, const_cast<void*>(base), dims, strides, box,
-                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint64_t dims[3] = {wide ? 128 : inner, rows, inner / 128};
+  const cuuint64_t strides[2] = {inner, 128};
+  const cuuint32_t box[3] = {128, box_rows, 2};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  if (!enc || enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, wide ? 3 : 2, const_cast<void*>(base), dims,
+                  strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     *st = cudaErrorInvalidValue;
@@ -784,7 +755,7 @@ extern "C" {
 
 size_t moe_few_workspace_bytes(int64_t T, int d, int E, int k, int d_ff) {
   if (check_few(T, d, E, k, d_ff) != MOE_OK) return 0;
-  return few_layout(T, d, k, d_ff).total;
+  return few_layout(T, d, E, k, d_ff).total;
 }
 
 moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float* router,
@@ -800,9 +771,11 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
     if (!q || !aligned16(q)) return MOE_ERR_INVALID_ARG;
   if (router && !aligned16(router)) return MOE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return MOE_ERR_INVALID_ARG;
-  const FewLayout L = few_layout(T, d, k, d_ff);
+  const FewLayout L = few_layout(T, d, E, k, d_ff);
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
   char* w = static_cast<char*>(ws);
+  const auto bytes = [&](size_t at) { return reinterpret_cast<uint8_t*>(w + at); };
+  const auto ints = [&](size_t at) { return reinterpret_cast<int32_t*>(w + at); };
 
   RouterParams r = {};
   r.x = x;
@@ -812,45 +785,55 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   r.d = d;
   r.E = E;
   r.err = reinterpret_cast<DevErr*>(w + L.err);
-  r.clear = reinterpret_cast<int32_t*>(w + L.ticket);
-  r.n_clear = static_cast<int>((L.xs - L.ticket) / 4);
-  r.xs = reinterpret_cast<float*>(w + L.xs);
-  r.x16 = reinterpret_cast<uint16_t*>(w + L.x16);
+  r.clear = ints(L.ticket);
+  r.n_clear = static_cast<int64_t>((L.clear_end - L.ticket) / 4);
+  r.xq = bytes(L.xq);
+  r.xs = bytes(L.xs);
 
   ExpertParams p = {};
   cudaError_t st = cudaSuccess;
   p.logits = logits;
-  p.T = static_cast<int>(T);
+  p.T = r.T;
   p.d = d;
   p.E = E;
   p.k = k;
   p.dff = d_ff;
-  p.tok = static_cast<int>(T < kTok ? T : kTok);
-  p.stage_bytes = static_cast<uint32_t>((kWBytes + kScBytes + p.tok * (kActRow + kHsRow) + 1023) / 1024 * 1024);
-  const size_t red_bytes = static_cast<size_t>(kEpi) * kParts * p.tok * 32 * sizeof(float);
-  const size_t room = 232448 - 1024 - sizeof(Shared) - red_bytes;
+  p.cols = L.cols;
+  p.n = (L.cols * kTerms + 15) / 16 * 16;
+  p.parts = L.parts;
+  p.stage_bytes = kABytes + 2 * p.n * 128 + 2 * kSfBytes;
+  const size_t room = 232448 - 1024 - sizeof(Shared);
   p.stages = static_cast<int>(room / p.stage_bytes < kMaxStages ? room / p.stage_bytes : kMaxStages);
   p.s1 = w1_scales;
   p.s3 = w3_scales;
   p.s2 = w2_scales;
   p.s1_bytes = mx_scale_bytes(d_ff, d);
   p.s2_bytes = mx_scale_bytes(d, d_ff);
+  p.xq = r.xq;
   p.xs = r.xs;
-  p.x16 = r.x16;
-  p.hs = reinterpret_cast<float*>(w + L.hs);
-  p.h16 = reinterpret_cast<uint16_t*>(w + L.h16);
+  p.gq = bytes(L.gq);
+  p.gs = bytes(L.gs);
+  p.hq = bytes(L.hq);
+  p.hs = bytes(L.hs);
+  p.part = reinterpret_cast<float*>(w + L.part);
   p.y = reinterpret_cast<float*>(w + L.y);
   p.out = out;
-  p.ticket = reinterpret_cast<int32_t*>(w + L.ticket);
-  p.done1 = reinterpret_cast<int32_t*>(w + L.done1);
-  p.done2 = reinterpret_cast<int32_t*>(w + L.done2);
+  p.ticket = ints(L.ticket);
+  p.cnt1 = ints(L.cnt1);
+  p.done1 = ints(L.done1);
+  p.done2 = ints(L.done2);
+  p.xdone = ints(L.xdone);
   p.err = r.err;
   p.wait_ns = wait_limit_ns();
   p.wide1 = d % 256 == 0;
   p.wide2 = d_ff % 256 == 0;
-  p.map1 = make_weight_map(W1q, d / 2, static_cast<uint64_t>(E) * d_ff, true, p.wide1, &st);
-  p.map3 = make_weight_map(W3q, d / 2, static_cast<uint64_t>(E) * d_ff, true, p.wide1, &st);
-  p.map2 = make_weight_map(W2q, d_ff / 2, static_cast<uint64_t>(E) * d, false, p.wide2, &st);
+  const uint64_t rows = static_cast<uint64_t>(L.cols) * kTerms, groups = static_cast<uint64_t>(L.groups);
+  p.map1 = make_piece_map(W1q, d / 2, static_cast<uint64_t>(E) * d_ff, 128, p.wide1, &st);
+  p.map3 = make_piece_map(W3q, d / 2, static_cast<uint64_t>(E) * d_ff, 128, p.wide1, &st);
+  p.map2 = make_piece_map(W2q, d_ff / 2, static_cast<uint64_t>(E) * d, 128, p.wide2, &st);
+  p.mapx = make_piece_map(T <= kTok ? p.xq : p.gq, d / 2, T <= kTok ? rows : groups * rows, p.n,
+                          p.wide1, &st);
+  p.maph = make_piece_map(p.hq, d_ff / 2, groups * rows, p.n, p.wide2, &st);
   if (st != cudaSuccess) return MOE_ERR_CUDA;
 
   int rgrid = router ? (E + kRouterExperts - 1) / kRouterExperts : 1;
@@ -871,8 +854,8 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
       return MOE_ERR_CUDA;
     attr_set_mask.fetch_or(bit, std::memory_order_release);
   }
-  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + sizeof(Shared) + red_bytes;
-  const int64_t units = T * k * (d_ff / kUnitH + d / kUnitY);
+  const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + sizeof(Shared);
+  const int64_t units = T * k * (d_ff / 128 * 2 * L.parts + d / 128);
   const int sms = num_sms_of_current_device();
   st = launch_pdl(few_experts_kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)),
                   dim3(kThreads), smem, stream, p);
