@@ -104,6 +104,7 @@ struct RouterParams {
   const float* router;  // null: the logits are given
   float* logits;
   int T, d, E;
+  int conv;  // the first CTAs, which write x in terms
   DevErr* err;
   int32_t* clear;  // counters, contiguous
   int64_t n_clear;
@@ -114,25 +115,28 @@ struct RouterParams {
 constexpr int kRouterExperts = 2;  // per CTA
 constexpr int kRouterThreads = 256;
 
-// CTA b: its share of the counters, token b in MXFP4 terms (b < T), then the logits of experts
-// 2 b and 2 b + 1: warp w sums the 128-value pieces w, w + 8, ... of d for every token, lanes
-// then warps are added in a fixed order.
+// Every CTA clears its share of the counters; the first `conv` write x in MXFP4 terms; each of
+// the others computes the logits of two experts for up to TB tokens (blockIdx.y: which): warp w
+// sums the 128-value pieces w, w + 8, ... of d, lanes then warps are added in a fixed order.
 template <int TB>
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams p) {
   griddep_wait();
   __shared__ float red[8][TB][kRouterExperts];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kRouterThreads) + threadIdx.x; i < p.n_clear;
-       i += static_cast<int64_t>(gridDim.x) * kRouterThreads)
-    p.clear[i] = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = DevErr{};
-  if (static_cast<int>(blockIdx.x) < p.T) {
-    const int t = blockIdx.x, row_bytes = p.d / 2;
-    const uint16_t* xr = p.x + static_cast<int64_t>(t) * p.d;
-    for (int c0 = 0; c0 < p.d; c0 += kRouterThreads * 8) {  // d is a multiple of 128: whole blocks
-      const int c = c0 + threadIdx.x * 8;
+  if (blockIdx.y == 0) {
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(kRouterThreads) + threadIdx.x; i < p.n_clear;
+         i += static_cast<int64_t>(gridDim.x) * kRouterThreads)
+      p.clear[i] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = DevErr{};
+  }
+  if (static_cast<int>(blockIdx.x) < p.conv) {
+    // 2048 values of a token: d is a multiple of 128, so blocks are whole
+    const int per = (p.d + kRouterThreads * 8 - 1) / (kRouterThreads * 8);
+    for (int i0 = blockIdx.x; blockIdx.y == 0 && i0 < p.T * per; i0 += p.conv) {
+      const int t = i0 / per, row_bytes = p.d / 2;
+      const int c = (i0 % per) * kRouterThreads * 8 + threadIdx.x * 8;
       uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (c < p.d) u = ld_v4(xr + c);
+      if (c < p.d) u = ld_v4(p.x + static_cast<int64_t>(t) * p.d + c);
       const uint32_t w[4] = {u.x, u.y, u.z, u.w};
       float v[8];
 #pragma unroll
@@ -175,16 +179,16 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams
       }
     }
   }
-  if (!p.router) return;
-  const int e0 = blockIdx.x * kRouterExperts;
-  if (e0 >= p.E) return;
+  const int e0 = (static_cast<int>(blockIdx.x) - p.conv) * kRouterExperts;
+  if (e0 < 0 || e0 >= p.E) return;
+  const int t0 = blockIdx.y * TB, tn = min(TB, p.T - t0);
   const int ne = min(kRouterExperts, p.E - e0);
   const float* r0 = p.router + static_cast<int64_t>(e0) * p.d;
   const float* r1 = r0 + (ne > 1 ? p.d : 0);
   float acc[TB][kRouterExperts];
 #pragma unroll
   for (int t = 0; t < TB; ++t) acc[t][0] = acc[t][1] = 0.0f;
-  constexpr int U = TB <= 8 ? 7 : 2;  // pieces of the router in flight
+  constexpr int U = 7;  // pieces of the router in flight
   for (int c0 = warp * 128; c0 < p.d; c0 += U * 1024) {
     float4 a[U], b[U];
 #pragma unroll
@@ -198,13 +202,17 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = c0 + u * 1024 + lane * 4;
-      if (c >= p.d) continue;
+      // loads without branches, so that they run ahead of the sums: past d the factors are zero
+      const int c = min(c0 + u * 1024, p.d - 128) + lane * 4;
+      const bool in = c0 + u * 1024 < p.d;
+      uint2 xv[TB];
 #pragma unroll
-      for (int t = 0; t < TB; ++t) {
-        if (t < p.T) {
-          const uint2 xv = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<int64_t>(t) * p.d + c));
-          const float x0 = bf16lo(xv.x), x1 = bf16hi(xv.x), x2 = bf16lo(xv.y), x3 = bf16hi(xv.y);
+      for (int t = 0; t < TB; ++t)
+        xv[t] = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<int64_t>(t0 + min(t, tn - 1)) * p.d + c));
+      if (in) {
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          const float x0 = bf16lo(xv[t].x), x1 = bf16hi(xv[t].x), x2 = bf16lo(xv[t].y), x3 = bf16hi(xv[t].y);
           acc[t][0] = fmaf(x3, a[u].w, fmaf(x2, a[u].z, fmaf(x1, a[u].y, fmaf(x0, a[u].x, acc[t][0]))));
           acc[t][1] = fmaf(x3, b[u].w, fmaf(x2, b[u].z, fmaf(x1, b[u].y, fmaf(x0, b[u].x, acc[t][1]))));
         }
@@ -221,12 +229,12 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams
       if (lane == 0) red[warp][t][j] = v;
     }
   __syncthreads();
-  for (int i = threadIdx.x; i < p.T * ne; i += kRouterThreads) {
+  for (int i = threadIdx.x; i < tn * ne; i += kRouterThreads) {
     const int t = i / ne, j = i % ne;
     float v = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) v += red[w][t][j];
-    p.logits[static_cast<int64_t>(t) * p.E + e0 + j] = v;
+    p.logits[static_cast<int64_t>(t0 + t) * p.E + e0 + j] = v;
   }
 }
 
@@ -453,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int next = 0;
     if (lane == 0) next = atomicAdd(p.ticket, 1);
-    while (true) {
+    while (ok) {
       const int u = __shfl_sync(0xFFFFFFFFu, next, 0);
       const bool work = u < n_units;
       if (lane == 0 && work) next = atomicAdd(p.ticket, 1);  // used after this unit's loads
@@ -461,44 +469,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         gather_group(p, sh, u, lane);
         continue;
       }
-      if (lane == 0) {
-        Unit un = {0, 0, 0, 0};
-        int ks0 = 0, ks1 = 1;
-        if (work && u < n1) {
-          const int v = u - n0, w = v % (ht * Q);
-          un = Unit{1, v / (ht * Q), w / Q, w % Q};
-          ks0 = st1 * (un.q >> 1) / p.parts;
-          ks1 = st1 * ((un.q >> 1) + 1) / p.parts;
-        } else if (work) {
-          un = Unit{2, (u - n1) / yt, (u - n1) % yt, 0};
-          ks1 = st2;
-        }
-        const int e = sh.group[un.group].e;
-        const bool first = un.kind == 1;
-        const bool wide = first ? p.wide1 : p.wide2;
-        const int kt = first ? kt1 : kt2;
-        const CUtensorMap* mw = first ? ((un.q & 1) ? &p.map3 : &p.map1) : &p.map2;
-        const CUtensorMap* mx = first ? &p.mapx : &p.maph;
-        const int wrow = (first ? e * p.dff : e * p.d) + 128 * un.tile;
-        const int xrow = first && direct ? 0 : un.group * p.cols * kTerms;
-        const uint8_t* sfa =
-            (first ? ((un.q & 1) ? p.s3 : p.s1) + e * p.s1_bytes : p.s2 + e * p.s2_bytes) +
-            static_cast<int64_t>(un.tile) * kt * kMxTileBytes;
-        const uint8_t* sfb = first ? (direct ? p.xs : p.gs + static_cast<int64_t>(un.group) * kt * kMxTileBytes)
-                                   : p.hs + static_cast<int64_t>(un.group) * kt * kMxTileBytes;
-        // what the activations have to wait for: a y unit for all h of its group (four 32-row
-        // quarters per tile), an h unit for its gathered tokens
-        const int32_t* flag = first ? (direct ? nullptr : p.xdone + un.group) : p.done1 + un.group;
-        const int target = first ? 1 : 4 * ht;
-        const uint32_t bbytes = p.n * 128u;
-        for (int ks = ks0; ks < ks1; ++ks) {
-          if (it >= S) ok = mbar_wait(empty(s), phase, abort_flag, p.err, 70, p.wait_ns);
-          if (!ok) break;
-          const int nkt = min(kStageKt, kt - kStageKt * ks);
+      Unit un = {0, 0, 0, 0};
+      int ks0 = 0, ks1 = 1;
+      if (work && u < n1) {
+        const int v = u - n0, w = v % (ht * Q);
+        un = Unit{1, v / (ht * Q), w / Q, w % Q};
+        ks0 = st1 * (un.q >> 1) / p.parts;
+        ks1 = st1 * ((un.q >> 1) + 1) / p.parts;
+      } else if (work) {
+        un = Unit{2, (u - n1) / yt, (u - n1) % yt, 0};
+        ks1 = st2;
+      }
+      const int e = sh.group[un.group].e;
+      const bool first = un.kind == 1;
+      const bool wide = first ? p.wide1 : p.wide2;
+      const int kt = first ? kt1 : kt2;
+      const CUtensorMap* mw = first ? ((un.q & 1) ? &p.map3 : &p.map1) : &p.map2;
+      const CUtensorMap* mx = first ? &p.mapx : &p.maph;
+      const int wrow = (first ? e * p.dff : e * p.d) + 128 * un.tile;
+      const int xrow = first && direct ? 0 : un.group * p.cols * kTerms;
+      const uint8_t* sfa =
+          (first ? ((un.q & 1) ? p.s3 : p.s1) + e * p.s1_bytes : p.s2 + e * p.s2_bytes) +
+          static_cast<int64_t>(un.tile) * kt * kMxTileBytes;
+      const uint8_t* sfb = first ? (direct ? p.xs : p.gs + static_cast<int64_t>(un.group) * kt * kMxTileBytes)
+                                 : p.hs + static_cast<int64_t>(un.group) * kt * kMxTileBytes;
+      // what the activations have to wait for: a y unit for all h of its group (four 32-row
+      // quarters per tile), an h unit for its gathered tokens
+      const int32_t* flag = first ? (direct ? nullptr : p.xdone + un.group) : p.done1 + un.group;
+      const int target = first ? 1 : 4 * ht;
+      const uint32_t bbytes = p.n * 128u;
+      for (int ks = ks0; ks < ks1; ++ks) {
+        if (it >= S) ok = warp_wait(empty(s), phase, abort_flag, p.err, 70, p.wait_ns);
+        if (!ok) break;
+        const int nkt = min(kStageKt, kt - kStageKt * ks);
+        const uint32_t st = base + s * p.stage_bytes, stb = st + kABytes;
+        const uint32_t ssa = stb + 2 * bbytes, ssb = ssa + kSfBytes;
+        const int pieces = (nkt + 1) / 2;
+        if (elect_one()) {
           sh.meta[s] = StageMeta{un, nkt, (ks == ks0 ? 1 : 0) | (ks == ks1 - 1 ? 2 : 0)};
-          const uint32_t st = base + s * p.stage_bytes, stb = st + kABytes;
-          const uint32_t ssa = stb + 2 * bbytes, ssb = ssa + kSfBytes;
-          const int pieces = (nkt + 1) / 2;
           if (!work) {
             mbar_arrive(full(s));
           } else {
@@ -514,7 +522,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (flag) {
               wait_count(flag, target, abort_flag, p.err, 71, p.wait_ns);
               fence_proxy_async_global();
-              flag = nullptr;
             }
             if (wide) {
               tma_load_3d(stb, mx, full(s), 0, xrow, 2 * ks);
@@ -524,70 +531,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             bulk_load(ssb, sfb + static_cast<int64_t>(ks) * kSfBytes, nkt * kMxTileBytes, full(s));
           }
-          ++it;
-          if (++s == S) {
-            s = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        flag = nullptr;
+        ++it;
+        if (++s == S) {
+          s = 0;
+          phase ^= 1;
         }
       }
-      ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
-      if (!ok || !work) break;
+      if (!work) break;
     }
     // copies still in flight land before the CTA ends
-    if (lane == 0 && *abort_flag)
+    if (*abort_flag)
       for (uint32_t i = it > S ? it - S : 0; i < it; ++i)
         mbar_wait(full(i % S), (i / S) & 1, nullptr, p.err, 72, p.wait_ns);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
-    if (lane == 0) {
-      uint32_t s = 0, phase = 0, units = 0;
-      const uint32_t idesc = idesc_mxf4(128, p.n);
-      const uint32_t bbytes = p.n * 128u;
-      while (true) {
-        if (!mbar_wait(full(s), phase, abort_flag, p.err, 73, p.wait_ns)) break;
+    uint32_t s = 0, phase = 0, units = 0;
+    const uint32_t idesc = idesc_mxf4(128, p.n);
+    const uint32_t bbytes = p.n * 128u;
+    while (warp_wait(full(s), phase, abort_flag, p.err, 73, p.wait_ns)) {
+      tc_fence_after();
+      const StageMeta m = sh.meta[s];
+      const uint32_t acc = units & 1, tacc = tmem + acc * kAccCols;
+      if ((m.flags & 1) && units >= 2) {
+        if (!warp_wait(tempty(acc), (units / 2 - 1) & 1, abort_flag, p.err, 74, p.wait_ns)) break;
         tc_fence_after();
-        const StageMeta m = sh.meta[s];
-        const uint32_t acc = units & 1, tacc = tmem + acc * kAccCols;
-        if ((m.flags & 1) && units >= 2) {
-          if (!mbar_wait(tempty(acc), (units / 2 - 1) & 1, abort_flag, p.err, 74, p.wait_ns)) break;
-          tc_fence_after();
-        }
-        if (m.u.kind == 0) {
+      }
+      if (m.u.kind == 0) {
+        if (elect_one()) {
           sh.acc_unit[acc] = m.u;
           mbar_arrive(tfull(acc));
           mbar_arrive(tfull(acc));
-          break;
         }
-        const uint32_t st = base + s * p.stage_bytes, stb = st + kABytes;
-        const uint32_t ssa = stb + 2 * bbytes, ssb = ssa + kSfBytes;
-        const uint32_t tsf = tmem + kSfCol0 + s * kSfCols;
-        for (int i = 0; i < m.nkt; ++i) {
-          tmem_cp_scales(tsf + 4 * i, ssa + i * kMxTileBytes);
-          tmem_cp_scales(tsf + 4 * kStageKt + 4 * i, ssb + i * kMxTileBytes);
+        break;
+      }
+      const uint32_t st = base + s * p.stage_bytes, stb = st + kABytes;
+      const uint32_t ssa = stb + 2 * bbytes, ssb = ssa + kSfBytes;
+      const uint32_t tsf = tmem + kSfCol0 + s * kSfCols;
+      if (elect_one()) {
+#pragma unroll
+        for (int i = 0; i < kStageKt; ++i) {
+          if (i < m.nkt) {
+            tmem_cp_scales(tsf + 4 * i, ssa + i * kMxTileBytes);
+            tmem_cp_scales(tsf + 4 * kStageKt + 4 * i, ssb + i * kMxTileBytes);
+          }
         }
-        for (int j = 0; j < 2 * m.nkt; ++j) {
-          const uint32_t id = (j & 1) * 2;
-          umma_mxf4(tacc, smem_desc_sw128(st + (j >> 2) * (kABytes / 2), 16, 1024) + 2 * (j & 3),
-                    smem_desc_sw128(stb + (j >> 2) * bbytes, 16, 1024) + 2 * (j & 3),
-                    idesc | (id << 4) | (id << 29), tsf + 4 * (j >> 1),
-                    tsf + 4 * kStageKt + 4 * (j >> 1), !(m.flags & 1) || j > 0);
+        const uint64_t da = smem_desc_sw128(st, 16, 1024), db = smem_desc_sw128(stb, 16, 1024);
+#pragma unroll
+        for (int j = 0; j < 2 * kStageKt; ++j) {
+          if (j < 2 * m.nkt) {
+            const uint32_t id = (j & 1) * 2;
+            umma_mxf4(tacc, da + (j >> 2) * (kABytes / 2 / 16) + 2 * (j & 3),
+                      db + (j >> 2) * (bbytes / 16) + 2 * (j & 3), idesc | (id << 4) | (id << 29),
+                      tsf + 4 * (j >> 1), tsf + 4 * kStageKt + 4 * (j >> 1),
+                      !(m.flags & 1) || j > 0);
+          }
         }
         umma_commit(empty(s));
         if (m.flags & 2) {
           sh.acc_unit[acc] = m.u;
           umma_commit(tfull(acc));
           mbar_arrive(tfull(acc));
-          ++units;
-        }
-        if (++s == S) {
-          s = 0;
-          phase ^= 1;
         }
       }
-      umma_commit(drain);  // every MMA issued is complete before TMEM is freed
-      mbar_wait(drain, 0, nullptr, p.err, 75, p.wait_ns);
+      __syncwarp();
+      if (m.flags & 2) ++units;
+      if (++s == S) {
+        s = 0;
+        phase ^= 1;
+      }
     }
+    __syncwarp();
+    if (elect_one()) umma_commit(drain);  // every MMA issued is complete before TMEM is freed
+    mbar_wait(drain, 0, nullptr, p.err, 75, p.wait_ns);
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- finishing units
     const int qd = warp - 4;  // rows 32 qd .. of the tile
@@ -742,7 +760,8 @@ CUtensorMap make_piece_map(const void* base, uint64_t inner, uint64_t rows, uint
 
 template <int TB>
 cudaError_t launch_router(const RouterParams& p, int grid, cudaStream_t s) {
-  return launch_pdl(few_router_kernel<TB>, dim3(grid), dim3(kRouterThreads), 0, s, p);
+  return launch_pdl(few_router_kernel<TB>, dim3(grid, p.router ? (p.T + TB - 1) / TB : 1),
+                    dim3(kRouterThreads), 0, s, p);
 }
 
 }  // namespace
@@ -836,12 +855,12 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   p.maph = make_piece_map(p.hq, d_ff / 2, groups * rows, p.n, p.wide2, &st);
   if (st != cudaSuccess) return MOE_ERR_CUDA;
 
-  int rgrid = router ? (E + kRouterExperts - 1) / kRouterExperts : 1;
-  if (rgrid < T) rgrid = static_cast<int>(T);
+  const int64_t conv = T * ((d + kRouterThreads * 8 - 1) / (kRouterThreads * 8));
+  r.conv = static_cast<int>(conv < 152 ? conv : 152);
+  const int rgrid = r.conv + (router ? (E + kRouterExperts - 1) / kRouterExperts : 0);
   st = T <= 1   ? launch_router<1>(r, rgrid, stream)
        : T <= 4 ? launch_router<4>(r, rgrid, stream)
-       : T <= 8 ? launch_router<8>(r, rgrid, stream)
-                : launch_router<32>(r, rgrid, stream);
+                : launch_router<8>(r, rgrid, stream);
   if (st != cudaSuccess) return MOE_ERR_CUDA;
 
   static std::atomic<unsigned long long> attr_set_mask{0ull};

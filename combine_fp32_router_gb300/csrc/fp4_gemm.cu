@@ -171,90 +171,95 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   const int nks = (p.kt + 1) / 2;
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-        const Tile t = decode(p, first_block, first_row, tile);
-        const int bi = t.nvalid <= 16 ? 0 : (t.nvalid <= 64 ? 1 : (t.nvalid <= 128 ? 2 : 3));
-        const uint32_t bbytes = (bi == 0 ? 16 : (bi == 1 ? 64 : (bi == 2 ? 128 : kRows))) * 128;
-        const CUtensorMap* mb = &p.mapB[bi];
-        const int rt0 = t.row0 / 128, rt1 = (t.row0 + t.nvalid - 1) / 128;
-        const uint8_t* sfa = p.sb + t.e * p.sb_bytes + static_cast<int64_t>(t.n0 / 128) * p.kt * kMxTileBytes;
-        const uint8_t* sfb = p.sa + static_cast<int64_t>(rt0) * p.kt * kMxTileBytes;
-        const int wrow = t.e * p.N + t.n0;
-        for (int ks = 0; ks < nks; ++ks, ++it) {
-          const int s = it % kStages;
-          if (it >= kStages &&
-              !mbar_wait(empty(s), (it / kStages - 1) & 1, abort_flag, err, 61, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          const uint32_t st = base + s * kStageBytes;
-          const uint32_t sfbytes = min(2, p.kt - 2 * ks) * kMxTileBytes;
-          const int nsb = rt1 - rt0 + 1;
+    uint32_t it = 0, s = 0, phase = 1;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
+      const Tile t = decode(p, first_block, first_row, tile);
+      const int bi = t.nvalid <= 16 ? 0 : (t.nvalid <= 64 ? 1 : (t.nvalid <= 128 ? 2 : 3));
+      const uint32_t bbytes = (bi == 0 ? 16 : (bi == 1 ? 64 : (bi == 2 ? 128 : kRows))) * 128;
+      const CUtensorMap* mb = &p.mapB[bi];
+      const int rt0 = t.row0 / 128, nsb = (t.row0 + t.nvalid - 1) / 128 - rt0 + 1;
+      const uint8_t* sfa = p.sb + t.e * p.sb_bytes + static_cast<int64_t>(t.n0 / 128) * p.kt * kMxTileBytes;
+      const uint8_t* sfb = p.sa + static_cast<int64_t>(rt0) * p.kt * kMxTileBytes;
+      const uint8_t* sfb1 = sfb + static_cast<int64_t>(p.kt) * kMxTileBytes;
+      const int wrow = t.e * p.N + t.n0;
+      for (int ks = 0; ks < nks; ++ks, ++it) {
+        if (it >= kStages) ok = warp_wait(empty(s), phase, abort_flag, err, 61, p.wait_ns);
+        if (!ok) break;
+        const uint32_t st = base + s * kStageBytes, ssf = st + kABytes + kBBytes;
+        const uint32_t sfbytes = min(2, p.kt - 2 * ks) * kMxTileBytes;
+        if (elect_one()) {
           mbar_arrive_expect_tx(full(s), kABytes + bbytes + sfbytes * (1 + nsb));
           tma_load_2d(st, &p.mapA, full(s), ks * 128, wrow);
           tma_load_2d(st + kABytes, mb, full(s), ks * 128, t.row0);
-          bulk_load(st + kABytes + kBBytes, sfa + 2 * ks * kMxTileBytes, sfbytes, full(s));
-          for (int i = 0; i < nsb; ++i)
-            bulk_load(st + kABytes + kBBytes + kSfaBytes + i * 2 * kMxTileBytes,
-                      sfb + (static_cast<int64_t>(i) * p.kt + 2 * ks) * kMxTileBytes, sfbytes,
-                      full(s));
+          bulk_load(ssf, sfa + 2 * ks * kMxTileBytes, sfbytes, full(s));
+          bulk_load(ssf + kSfaBytes, sfb + 2 * ks * kMxTileBytes, sfbytes, full(s));
+          if (nsb > 1)
+            bulk_load(ssf + kSfaBytes + 2 * kMxTileBytes, sfb1 + 2 * ks * kMxTileBytes, sfbytes, full(s));
+        }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
         }
       }
-      // copies still in flight land before the CTA ends (only after an abort are there any
-      // that the MMA warp has not waited for)
-      if (*abort_flag)
-        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-          mbar_wait(full(i % kStages), (i / kStages) & 1, nullptr, err, 62, p.wait_ns);
     }
+    // copies still in flight land before the CTA ends (only after an abort are there any that
+    // the MMA warp has not waited for)
+    if (*abort_flag)
+      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+        mbar_wait(full(i % kStages), (i / kStages) & 1, nullptr, err, 62, p.wait_ns);
   } else if (warp == 1) {
-    if (lane == 0) {
-      uint32_t it = 0, n = 0;
-      bool ok = true;
-      for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n) {
-        const Tile t = decode(p, first_block, first_row, tile);
-        const uint32_t acc = n & 1, tacc = tmem + acc * kRows;
-        if (n >= 2 && !mbar_wait(tempty(acc), (n / 2 - 1) & 1, abort_flag, err, 63, p.wait_ns))
-          break;
+    uint32_t s = 0, phase = 0, n = 0;
+    bool ok = true;
+    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n) {
+      const Tile t = decode(p, first_block, first_row, tile);
+      const uint32_t acc = n & 1, tacc = tmem + acc * kRows;
+      if (n >= 2 && !warp_wait(tempty(acc), (n / 2 - 1) & 1, abort_flag, err, 63, p.wait_ns)) break;
+      tc_fence_after();
+      // the block may start in the middle of a scale tile (row 64 of it: column 2)
+      const uint32_t sf_shift = (t.row0 % 128) / 32;
+      const int nsb = (t.row0 + t.nvalid - 1) / 128 - t.row0 / 128 + 1;
+      const uint32_t idesc = idesc_mxf4(128, (t.nvalid + 15) / 16 * 16);
+      for (int ks = 0; ks < nks; ++ks) {
+        ok = warp_wait(full(s), phase, abort_flag, err, 64, p.wait_ns);
+        if (!ok) break;
         tc_fence_after();
-        // the block may start in the middle of a scale tile (row 64 of it: column 2)
-        const uint32_t sf_shift = (t.row0 % 128) / 32;
-        const int nsb = (t.row0 + t.nvalid - 1) / 128 - t.row0 / 128 + 1;
-        const uint32_t idesc = idesc_mxf4(128, (t.nvalid + 15) / 16 * 16);
-        for (int ks = 0; ks < nks; ++ks, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(full(s), (it / kStages) & 1, abort_flag, err, 64, p.wait_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t st = base + s * kStageBytes;
-          const uint32_t ssf = st + kABytes + kBBytes;
-          const uint32_t tsf = tmem + kSfCol0 + s * kSfCols;
-          const int nkt = min(2, p.kt - 2 * ks);
-          for (int i = 0; i < nkt; ++i) {
-            tmem_cp_scales(tsf + 4 * i, ssf + i * kMxTileBytes);
-            for (int j = 0; j < nsb; ++j)
-              tmem_cp_scales(tsf + 8 + 8 * i + 4 * j,
-                             ssf + kSfaBytes + (2 * j + i) * kMxTileBytes);
+        const uint32_t st = base + s * kStageBytes;
+        const uint32_t ssf = st + kABytes + kBBytes;
+        const uint32_t tsf = tmem + kSfCol0 + s * kSfCols;
+        const int nkt = min(2, p.kt - 2 * ks);
+        if (elect_one()) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (i < nkt) {
+              tmem_cp_scales(tsf + 4 * i, ssf + i * kMxTileBytes);
+              tmem_cp_scales(tsf + 8 + 8 * i, ssf + kSfaBytes + i * kMxTileBytes);
+              if (nsb > 1) tmem_cp_scales(tsf + 12 + 8 * i, ssf + kSfaBytes + (2 + i) * kMxTileBytes);
+            }
           }
           const uint64_t da = smem_desc_sw128(st, 16, 1024);
           const uint64_t db = smem_desc_sw128(st + kABytes, 16, 1024);
-          for (int j = 0; j < 2 * nkt; ++j) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
             const uint32_t id = (j & 1) * 2;
-            umma_mxf4(tacc, da + 2 * j, db + 2 * j, idesc | (id << 4) | (id << 29),
-                      tsf + 4 * (j >> 1), tsf + 8 + 8 * (j >> 1) + sf_shift, ks > 0 || j > 0);
+            if (j < 2 * nkt)
+              umma_mxf4(tacc, da + 2 * j, db + 2 * j, idesc | (id << 4) | (id << 29),
+                        tsf + 4 * (j >> 1), tsf + 8 + 8 * (j >> 1) + sf_shift, ks > 0 || j > 0);
           }
           umma_commit(empty(s));
+          if (ks == nks - 1) umma_commit(tfull(acc));
         }
-        if (ok) umma_commit(tfull(acc));
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
+        }
       }
-      // every MMA issued is complete before TMEM is freed
-      umma_commit(drain);
-      mbar_wait(drain, 0, nullptr, err, 65, p.wait_ns);
     }
+    __syncwarp();
+    if (elect_one()) umma_commit(drain);  // every MMA issued is complete before TMEM is freed
+    mbar_wait(drain, 0, nullptr, err, 65, p.wait_ns);
   } else if (warp >= 4) {
     const int q = warp - 4;
     uint32_t n = 0;
