@@ -39,12 +39,17 @@ constexpr int kPartStages = 4;           // stages of a K range of W1 and W3 (at
 constexpr uint32_t kABytes = 128 * kStageKt * 64;
 constexpr uint32_t kSfBytes = kStageKt * kMxTileBytes;
 constexpr int kMaxStages = 5;
-constexpr uint32_t kAccCols = 64;        // TMEM: two accumulators, then the stages' scales
-constexpr uint32_t kSfCol0 = 2 * kAccCols;
+// Four groups of four warps finish units in turn, each with an accumulator of its own: publishing
+// a unit's sums (store, fence, counter) and, for the last of a tile, SwiGLU and the terms of h
+// take 2 to 4 us, about as long as streaming the next unit's weights.  With one group the stream
+// waited for it: 320 us instead of 255 us for 16 tokens over 64 experts.
+constexpr int kGroups = 4;
+constexpr uint32_t kAccCols = 64;        // TMEM: the accumulators, then the stages' scales
+constexpr uint32_t kSfCol0 = kGroups * kAccCols;
 constexpr uint32_t kSfCols = 8 * kStageKt;
 static_assert(kSfCol0 + kMaxStages * kSfCols <= 512 && kMaxN <= static_cast<int>(kAccCols), "TMEM columns");
-// warp 0 loads, 1 issues MMAs, 2 owns TMEM, 4..7 finish units
-constexpr int kThreads = 256;
+// warp 0 loads, 1 issues MMAs, 2 owns TMEM, 4 on finish units
+constexpr int kThreads = 128 + 128 * kGroups;
 
 struct FewLayout {
   size_t err, ticket, cnt1, done1, done2, xdone, clear_end, xq, xs, gq, gs, hq, hs, part, y, total;
@@ -284,8 +289,8 @@ struct Shared {
   float gate[kMaxT][kMaxK];
   uint16_t slot_e[kMaxT][kMaxK];
   StageMeta meta[kMaxStages];
-  Unit acc_unit[2];
-  uint64_t bars[2 * kMaxStages + 5];
+  Unit acc_unit[kGroups];
+  uint64_t bars[2 * kMaxStages + 2 * kGroups + 1];
   int32_t groups;
   int32_t abort_flag;
   uint32_t tmem;
@@ -377,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const auto full = [&](uint32_t s) { return smem_u32(&sh.bars[s]); };
   const auto empty = [&](uint32_t s) { return smem_u32(&sh.bars[kMaxStages + s]); };
   const auto tfull = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + a]); };
-  const auto tempty = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + 2 + a]); };
-  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 4]);
+  const auto tempty = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + kGroups + a]); };
+  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 2 * kGroups]);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&sh.abort_flag);
 
   if (threadIdx.x == 0) {
@@ -386,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < kGroups; ++a) {
       mbar_init(tfull(a), 2);   // the accumulator is complete, its unit is written down
       mbar_init(tempty(a), 4);
     }
@@ -554,18 +559,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (warp_wait(full(s), phase, abort_flag, p.err, 73, p.wait_ns)) {
       tc_fence_after();
       const StageMeta m = sh.meta[s];
-      const uint32_t acc = units & 1, tacc = tmem + acc * kAccCols;
-      if ((m.flags & 1) && units >= 2) {
-        if (!warp_wait(tempty(acc), (units / 2 - 1) & 1, abort_flag, p.err, 74, p.wait_ns)) break;
-        tc_fence_after();
-      }
-      if (m.u.kind == 0) {
-        if (elect_one()) {
-          sh.acc_unit[acc] = m.u;
-          mbar_arrive(tfull(acc));
-          mbar_arrive(tfull(acc));
+      if (m.u.kind == 0) {  // no more work: every group gets that as its next unit
+        for (int i = 0; i < kGroups; ++i, ++units) {
+          const uint32_t a = units % kGroups;
+          if (units >= kGroups &&
+              !warp_wait(tempty(a), (units / kGroups - 1) & 1, abort_flag, p.err, 74, p.wait_ns))
+            break;
+          if (elect_one()) {
+            sh.acc_unit[a] = m.u;
+            mbar_arrive(tfull(a));
+            mbar_arrive(tfull(a));
+          }
+          __syncwarp();
         }
         break;
+      }
+      const uint32_t acc = units % kGroups, tacc = tmem + acc * kAccCols;
+      if ((m.flags & 1) && units >= kGroups) {
+        if (!warp_wait(tempty(acc), (units / kGroups - 1) & 1, abort_flag, p.err, 74, p.wait_ns)) break;
+        tc_fence_after();
       }
       const uint32_t st = base + s * p.stage_bytes, stb = st + kABytes;
       const uint32_t ssa = stb + 2 * bbytes, ssb = ssa + kSfBytes;
@@ -608,10 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(drain, 0, nullptr, p.err, 75, p.wait_ns);
   } else if (warp >= 4) {
     // ---------------------------------------------------------------- finishing units
-    const int qd = warp - 4;  // rows 32 qd .. of the tile
+    const int qd = warp & 3;             // rows 32 qd .. of the tile
+    const uint32_t acc = (warp >> 2) - 1;  // this group's accumulator
     for (uint32_t i = 0;; ++i) {
-      const uint32_t acc = i & 1;
-      if (!mbar_wait(tfull(acc), (i >> 1) & 1, abort_flag, p.err, 76, p.wait_ns)) break;
+      if (!mbar_wait(tfull(acc), i & 1, abort_flag, p.err, 76, p.wait_ns)) break;
       const Unit un = sh.acc_unit[acc];
       if (un.kind == 0) break;
       tc_fence_after();
