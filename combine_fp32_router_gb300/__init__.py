@@ -236,20 +236,37 @@ _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
            torch.float32: MOE_DTYPE_F32}
 
 
+# The 4-bit entry points run in a few microseconds, about as long as marshalling a call takes:
+# they pass addresses as plain ints and size checks stay in Python.
+def _addr(t):
+    if not t.is_contiguous():
+        raise ValueError("tensor arguments must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    if device.type != "cuda":
+        raise ValueError("tensor arguments must be CUDA tensors: got %s" % device)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _dtype(dt):
-    if dt not in _DTYPES:
-        raise ValueError("dtype must be bfloat16, float16 or float32: got %s" % dt)
-    return _DTYPES[dt]
+    try:
+        return _DTYPES[dt]
+    except KeyError:
+        raise ValueError("dtype must be bfloat16, float16 or float32: got %s" % dt) from None
 
 
 def moe_fp4_row_bytes(cols):
     """Bytes of the codes of one MXFP4 row of ``cols`` values."""
-    return int(_lib.moe_fp4_row_bytes(int(cols)))
+    return (cols + 127) // 128 * 64 if cols > 0 else 0
 
 
 def moe_fp4_scale_bytes(rows, cols):
     """Bytes of the scales of a rows x cols MXFP4 matrix."""
-    return int(_lib.moe_fp4_scale_bytes(int(rows), int(cols)))
+    return (rows + 127) // 128 * ((cols + 127) // 128) * 512 if rows > 0 and cols > 0 else 0
 
 
 def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
@@ -257,17 +274,20 @@ def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
     (q [rows, moe_fp4_row_bytes(cols)] uint8, scales [moe_fp4_scale_bytes(rows, cols)] uint8),
     written into ``q`` and ``scales`` where they are given (see include/moe.h)."""
     rows, cols = x.shape
-    if cols > 1 and x.stride(1) != 1:
+    stride, one = x.stride()
+    if one != 1 and cols > 1:
         raise ValueError("the values of a row must be contiguous")
+    dt, kb, sb = _dtype(x.dtype), moe_fp4_row_bytes(cols), moe_fp4_scale_bytes(rows, cols)
     if q is None:
-        q = torch.empty(rows, moe_fp4_row_bytes(cols), dtype=torch.uint8, device=x.device)
+        q = torch.empty((rows, kb), dtype=torch.uint8, device=x.device)
+    elif _nbytes(q) < rows * kb:
+        raise ValueError("q too small for %d x %d values" % (rows, cols))
     if scales is None:
-        scales = torch.empty(moe_fp4_scale_bytes(rows, cols), dtype=torch.uint8, device=x.device)
-    if _nbytes(q) < rows * moe_fp4_row_bytes(cols) or \
-            _nbytes(scales) < moe_fp4_scale_bytes(rows, cols):
-        raise ValueError("q or scales too small for %d x %d values" % (rows, cols))
-    _check(_lib.moe_quantize_rows_fp4(ctypes.c_void_p(x.data_ptr()), _dtype(x.dtype), rows, cols,
-                                      x.stride(0), _ptr(q), _ptr(scales), _stream(stream)),
+        scales = torch.empty(sb, dtype=torch.uint8, device=x.device)
+    elif _nbytes(scales) < sb:
+        raise ValueError("scales too small for %d x %d values" % (rows, cols))
+    _check(_lib.moe_quantize_rows_fp4(x.data_ptr(), dt, rows, cols, stride, _addr(q),
+                                      _addr(scales), _raw_stream(stream, x.device)),
            "moe_quantize_rows_fp4")
     return q, scales
 
@@ -275,14 +295,16 @@ def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
 def moe_dequantize_rows_fp4(q, scales, cols, dtype=torch.bfloat16, stream=None):
     """The values of one MXFP4 matrix (q [rows, bytes]) or of a group of them
     (q [E, rows, bytes], scales [E, ...]) as a new tensor [..., rows, cols] of ``dtype``."""
-    groups = q.shape[0] if q.dim() == 3 else 1
-    rows = q.shape[-2]
-    if q.shape[-1] != moe_fp4_row_bytes(cols) or \
+    shape = q.shape
+    groups, rows = (shape[0], shape[1]) if len(shape) == 3 else (1, shape[0])
+    dt = _dtype(dtype)
+    if shape[-1] != moe_fp4_row_bytes(cols) or \
             _nbytes(scales) < groups * moe_fp4_scale_bytes(rows, cols):
         raise ValueError("q or scales do not hold rows of %d values" % cols)
-    out = torch.empty(*q.shape[:-1], cols, dtype=dtype, device=q.device)
-    _check(_lib.moe_dequantize_rows_fp4(_ptr(q), _ptr(scales), groups, rows, cols, _dtype(dtype),
-                                        _ptr(out), _stream(stream)), "moe_dequantize_rows_fp4")
+    out = torch.empty((*shape[:-1], cols), dtype=dtype, device=q.device)
+    _check(_lib.moe_dequantize_rows_fp4(_addr(q), _addr(scales), groups, rows, cols, dt,
+                                        out.data_ptr(), _raw_stream(stream, q.device)),
+           "moe_dequantize_rows_fp4")
     return out
 
 
@@ -292,9 +314,10 @@ def moe_quantize_weights_fp4(W, stream=None):
     E, K, N = W.shape
     if W.dtype != torch.bfloat16:
         raise ValueError("W must be bfloat16: got %s" % W.dtype)
-    Wq = torch.empty(E, N, moe_fp4_row_bytes(K), dtype=torch.uint8, device=W.device)
-    sc = torch.empty(E, moe_fp4_scale_bytes(N, K), dtype=torch.uint8, device=W.device)
-    _check(_lib.moe_quantize_weights_fp4(_ptr(W), E, K, N, _ptr(Wq), _ptr(sc), _stream(stream)),
+    Wq = torch.empty((E, N, moe_fp4_row_bytes(K)), dtype=torch.uint8, device=W.device)
+    sc = torch.empty((E, moe_fp4_scale_bytes(N, K)), dtype=torch.uint8, device=W.device)
+    _check(_lib.moe_quantize_weights_fp4(_addr(W), E, K, N, Wq.data_ptr(), sc.data_ptr(),
+                                         _raw_stream(stream, W.device)),
            "moe_quantize_weights_fp4")
     return Wq, sc
 
@@ -304,18 +327,20 @@ def moe_gemm_fp4(aq, a_scales, bq, b_scales, out, K, counts=None, stream=None):
     bq [E, N, bytes] (or [N, bytes]).  ``counts`` (int32 device tensor [E]): expert e's rows
     start on a 128-row boundary after expert e - 1's; without it E is 1 (see include/moe.h)."""
     rows, N = out.shape
-    E = bq.shape[0] if bq.dim() == 3 else 1
+    ash, bsh = aq.shape, bq.shape
+    E = bsh[0] if len(bsh) == 3 else 1
     kb = moe_fp4_row_bytes(K)
-    if aq.shape[-1] != kb or bq.shape[-1] != kb or aq.shape[0] < rows or bq.shape[-2] != N:
+    if ash[-1] != kb or bsh[-1] != kb or ash[0] < rows or bsh[-2] != N:
         raise ValueError("aq, bq and out do not fit one product over %d values" % K)
     if _nbytes(a_scales) < moe_fp4_scale_bytes(rows, K) or \
             _nbytes(b_scales) < E * moe_fp4_scale_bytes(N, K):
         raise ValueError("a_scales or b_scales too small")
     if counts is not None and (counts.dtype != torch.int32 or counts.numel() != E):
         raise ValueError("counts must hold one int32 per expert")
-    _check(_lib.moe_gemm_fp4(_ptr(aq), _ptr(a_scales), rows, _ptr(counts), _ptr(bq),
-                             _ptr(b_scales), E, N, K, _ptr(out), _dtype(out.dtype),
-                             _stream(stream)), "moe_gemm_fp4")
+    _check(_lib.moe_gemm_fp4(_addr(aq), _addr(a_scales), rows,
+                             None if counts is None else _addr(counts), _addr(bq),
+                             _addr(b_scales), E, N, K, _addr(out), _dtype(out.dtype),
+                             _raw_stream(stream, out.device)), "moe_gemm_fp4")
 
 
 def moe_gemm_fp4_get_error(stream=None):
@@ -335,18 +360,23 @@ def moe_forward_few_fp4(x, logits, router, W1q, W3q, W2q, w1_scales, w3_scales, 
     computed and written; None: they are read."""
     T, d = x.shape
     E, d_ff, kb = W1q.shape
-    if kb != d // 2 or W3q.shape != W1q.shape or tuple(W2q.shape) != (E, d, d_ff // 2) or \
-            tuple(logits.shape) != (T, E) or out.shape != x.shape or \
-            (router is not None and tuple(router.shape) != (E, d)):
+    if kb != moe_fp4_row_bytes(d) or W3q.shape != W1q.shape or \
+            W2q.shape != (E, d, moe_fp4_row_bytes(d_ff)) or logits.shape != (T, E) or \
+            out.shape != (T, d) or (router is not None and router.shape != (E, d)):
         raise ValueError("the arguments' shapes do not fit one layer")
     if x.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or \
             logits.dtype != torch.float32 or \
             (router is not None and router.dtype != torch.float32):
         raise ValueError("x and out are bfloat16, logits and router float32")
-    _check(_lib.moe_forward_few_fp4(_ptr(x), _ptr(logits), _ptr(router), _ptr(W1q), _ptr(W3q),
-                                    _ptr(W2q), _ptr(w1_scales), _ptr(w3_scales),
-                                    _ptr(w2_scales), T, d, E, k, d_ff, _ptr(out), _ptr(ws),
-                                    _nbytes(ws), _stream(stream)), "moe_forward_few_fp4")
+    if min(_nbytes(w1_scales), _nbytes(w3_scales)) < E * moe_fp4_scale_bytes(d_ff, d) or \
+            _nbytes(w2_scales) < E * moe_fp4_scale_bytes(d, d_ff):
+        raise ValueError("scales too small for the weights")
+    _check(_lib.moe_forward_few_fp4(_addr(x), _addr(logits),
+                                    None if router is None else _addr(router), _addr(W1q),
+                                    _addr(W3q), _addr(W2q), _addr(w1_scales), _addr(w3_scales),
+                                    _addr(w2_scales), T, d, E, k, d_ff, _addr(out), _addr(ws),
+                                    _nbytes(ws), _raw_stream(stream, x.device)),
+           "moe_forward_few_fp4")
 
 
 class ForwardGraph:

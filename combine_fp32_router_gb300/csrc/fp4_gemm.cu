@@ -2,15 +2,21 @@
 // (tcgen05.mma kind::mxf4, one E8M0 scale per 32 values, fp32 accumulation):
 //   out[r, n] = sum_k A[r, k] B[e(r)][n, k],  rows grouped by expert in 128-row segments.
 //
-// One persistent launch.  A tile is 128 weight rows (the M operand) x a block of up to 192
-// activation rows of one expert (the N operand, so a block costs MMAs for the rows it has):
-//   warp 0      producer: codes by 2-D TMA (128-byte swizzle), scale tiles by bulk copies
-//   warp 1      one lane: scale tiles shared memory -> TMEM (tcgen05.cp), then the MMAs, which
-//               the hardware runs in that order
-//   warp 2      TMEM allocator
-//   warps 4..7  epilogue: accumulator column = output row, lane = output column, so a warp
-//               stores 32 neighbouring outputs of a row at a time
-// The K order of every output is that of its stages, whatever the other rows are.
+// One persistent launch.  A tile is weight rows (the M operand) x a block of activation rows of
+// one expert (the N operand, so a block costs MMAs for the rows it has), in one of two shapes:
+//   pairs    256 weight rows x up to 192 rows on a CTA pair (cta_group::2): each CTA loads its
+//            half of both, 31 KB per 256 values of K for 128 x 192 outputs
+//   singles  128 weight rows x up to 64 rows on one CTA, where pairs would leave SMs idle
+// Both add the same products in the same order: K runs through the tensor cores 64 values at a
+// time, whatever the other rows are.  Warps:
+//   0      producer: codes by TMA (128-byte swizzle), scale tiles by TMA (plain)
+//   1      scale tiles shared memory -> TMEM (tcgen05.cp), then the MMAs, which the hardware
+//          runs in that order
+//   2      TMEM allocator, 3 the experts' first rows and blocks
+//   4..7   epilogue: accumulator column = output row, lane = output column
+// Bound by what an SM can take in (measured: some 100 GB/s) once a block is full: a 128 x 192
+// tile on single CTAs needs 43 KB for the same work and ran the 8192 x 7168 x 7168 product at
+// 4.8 PFLOP/s.
 #include <cuda.h>
 
 #include <atomic>
@@ -21,113 +27,151 @@
 
 namespace moe {
 
-CUtensorMap make_map_u8(const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
-                        cudaError_t* st);
-
 namespace {
 
 // Device-side problems of the 4-bit product (a bounded wait that ran out, counts that do not
 // fit the rows): first error since moe_gemm_fp4_get_error last read it.
 __device__ DevErr g_gemm_err;
 
-constexpr int kRows = 192;  // N of a tile: two 192-column accumulators + scales fill TMEM
-constexpr int kStages = 5;
-constexpr int kKStage = 256;                   // values of K per stage (128 bytes of codes)
-constexpr uint32_t kABytes = 128 * 128;        // weight codes
-constexpr uint32_t kBBytes = kRows * 128;      // activation codes
-constexpr uint32_t kSfaBytes = 2 * kMxTileBytes;
-constexpr uint32_t kSfbBytes = 4 * kMxTileBytes;  // up to two 128-row tiles
-constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-constexpr uint32_t kSfCols = 24;               // TMEM columns of a stage's scales: 8 + 16
-constexpr uint32_t kSfCol0 = 2 * kRows;
-static_assert(kSfCol0 + kStages * kSfCols <= 512, "TMEM columns");
-static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
-constexpr int kBars = 2 * kStages + 5;
+template <bool PAIR>
+struct Cfg {
+  static constexpr int kRows = PAIR ? 192 : 64;  // N of a tile
+  static constexpr int kLocal = PAIR ? kRows / 2 : kRows;  // rows a CTA loads
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kStages = PAIR ? 5 : 8;
+  static constexpr int kSfTiles = PAIR ? 2 : 1;  // 128-row scale tiles a block can touch
+  static constexpr uint32_t kABytes = 128 * 128;
+  static constexpr uint32_t kBBytes = kLocal * 128;
+  static constexpr uint32_t kSfaBytes = 2 * kMxTileBytes;
+  static constexpr uint32_t kSfbBytes = 2 * kSfTiles * kMxTileBytes;
+  static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+  static constexpr uint32_t kSfCols = 8 + 8 * kSfTiles;  // TMEM columns of a stage's scales
+  static constexpr uint32_t kSfCol0 = 2 * kRows;
+  static constexpr uint32_t kTmemCols = PAIR ? 512 : 256;
+  static_assert(kSfCol0 + kStages * kSfCols <= kTmemCols, "TMEM columns");
+  static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
+};
+constexpr int kBoxes = 4;  // box heights of the activation rows: 16, 32, 64, and 96 (pairs)
 constexpr int kThreads = 256;
+constexpr int kMaxStages = 8;
+constexpr int kTrRow = 36;  // words of a transpose row: 32 columns, padded against bank conflicts
 
 struct Params {
-  const uint8_t* sa;  // scales of the activation rows
-  const uint8_t* sb;  // scales of the weights, [E] arrays of sb_bytes
   const int32_t* counts;
-  int64_t rows, sb_bytes;
-  int N, kt, E, nt;   // outputs, 128-value K tiles, experts, 128-row weight tiles per expert
+  int64_t rows;
+  int N, kt, E, nt;   // outputs, 128-value K tiles, experts, weight tiles per expert
+  int sf_tiles;       // 128-row scale tiles per expert
   int64_t ldo;
+  int vec;  // output rows start on 16 bytes
   void* out;
   uint64_t wait_ns;
-  CUtensorMap mapA;      // weight codes, boxes of 128 rows
-  CUtensorMap mapB[4];   // activation codes, boxes of 16, 64, 128 and 192 rows
+  CUtensorMap mapA, mapSa;          // weight codes (boxes of 128 rows) and scale tiles
+  CUtensorMap mapB[kBoxes], mapSb;  // activation codes and scale tiles
 };
 
-constexpr size_t kTable = 2 * (kMaxE + 1) * sizeof(int32_t);
-constexpr size_t kSmemBytes = kStages * kStageBytes + 1024 + 8 * kBars + 64 + kTable;
-static_assert(kSmemBytes <= 232448, "fits the opt-in shared memory of a CTA (227 KB)");
+// behind the stages
+struct Shared {
+  uint64_t bars[2 * kMaxStages + 5];
+  uint32_t tmem;
+  int32_t abort_flag;
+  uint32_t consumed, peer_issued;          // fills used by MMAs, fills issued by the peer
+  uint32_t tx[kMaxStages], peer_tx[kMaxStages];  // bytes of the fill in a stage
+  int32_t first_block[kMaxE + 1], first_row[kMaxE + 1];
+  alignas(16) uint32_t transpose[4 * 16 * kTrRow];
+};
+template <bool PAIR>
+constexpr size_t smem_bytes() {
+  return Cfg<PAIR>::kStages * Cfg<PAIR>::kStageBytes + 1024 + sizeof(Shared);
+}
+static_assert(smem_bytes<true>() <= 232448 && smem_bytes<false>() <= 232448,
+              "fits the opt-in shared memory of a CTA (227 KB)");
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (8ull << 32) | (1ull << 46);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
+__device__ __forceinline__ void umma_mxf4_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                               uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;"
+      "\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
       : "memory");
 }
+
 struct Tile {
   int e, row0, nvalid, n0;
+  int box;    // index of the box height
+  int local;  // rows each CTA loads
 };
 
 // first_block[e], first_row[e]: blocks and rows before expert e (E + 1 entries each)
-__device__ __forceinline__ Tile decode(const Params& p, const int32_t* first_block,
-                                       const int32_t* first_row, int64_t tile) {
+template <bool PAIR>
+__device__ __forceinline__ Tile decode(const Params& p, const Shared& sh, int64_t tile) {
+  constexpr int R = Cfg<PAIR>::kRows;
   const int b = static_cast<int>(tile / p.nt);
   int lo = 0, hi = p.E;  // the last expert with first_block[e] <= b
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
-    if (first_block[mid] <= b) lo = mid;
+    if (sh.first_block[mid] <= b) lo = mid;
     else hi = mid;
   }
   Tile t;
   t.e = lo;
-  const int i = b - first_block[lo];
-  t.row0 = first_row[lo] + i * kRows;
+  const int i = b - sh.first_block[lo];
+  t.row0 = sh.first_row[lo] + i * R;
   const int cnt = p.counts ? p.counts[lo] : static_cast<int>(p.rows);
-  t.nvalid = min(cnt - i * kRows, kRows);
-  t.n0 = static_cast<int>(tile % p.nt) * 128;
+  t.nvalid = min(cnt - i * R, R);
+  t.n0 = static_cast<int>(tile % p.nt) * (PAIR ? 256 : 128);
+  const int half = PAIR ? (t.nvalid + 1) / 2 : t.nvalid;
+  t.box = half <= 16 ? 0 : (half <= 32 ? 1 : (half <= 64 ? 2 : 3));
+  t.local = t.box == 3 ? 96 : 16 << t.box;
   return t;
 }
 
-template <bool F32>
+template <bool F32, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<PAIR>;
+  constexpr uint32_t S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  uint8_t* sm = smem_raw + (base - raw);
-  const uint32_t bars = base + kStages * kStageBytes;
-  const auto full = [&](int s) { return bars + 8u * s; };
-  const auto empty = [&](int s) { return bars + 8u * (kStages + s); };
-  const auto tfull = [&](int s) { return bars + 8u * (2 * kStages + s); };
-  const auto tempty = [&](int s) { return bars + 8u * (2 * kStages + 2 + s); };
-  const uint32_t drain = bars + 8u * (2 * kStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kStages * kStageBytes + 8 * kBars);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  int32_t* first_block = reinterpret_cast<int32_t*>(tmem_slot + 4);
-  int32_t* first_row = first_block + kMaxE + 1;
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (base - raw) + S * C::kStageBytes);
+  const auto full = [&](uint32_t s) { return smem_u32(&sh.bars[s]); };
+  const auto empty = [&](uint32_t s) { return smem_u32(&sh.bars[kMaxStages + s]); };
+  const auto tfull = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + a]); };
+  const auto tempty = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + 2 + a]); };
+  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 4]);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(&sh.abort_flag);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / C::kCtas, units = gridDim.x / C::kCtas;
   DevErr* err = &g_gemm_err;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full(s), 1);
+    for (uint32_t s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);  // rank 0's: its arming arrival and both CTAs' bytes
       mbar_init(empty(s), 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(tfull(s), 1);
-      mbar_init(tempty(s), 4);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), 4 * C::kCtas);  // rank 0's: an arrival of every epilogue warp
     }
     mbar_init(drain, 1);
     fence_mbar_init();
-    *abort_flag = 0;
+    sh.abort_flag = 0;
+    sh.consumed = sh.peer_issued = 0u;
     tma_prefetch_desc(&p.mapA);
+    tma_prefetch_desc(&p.mapSa);
+    tma_prefetch_desc(&p.mapSb);
   }
-  if (warp == 2) tmem_alloc(smem_u32(tmem_slot), 512);
+  if (warp == 2) {
+    if constexpr (PAIR) tmem_alloc_pair(smem_u32(&sh.tmem), C::kTmemCols);
+    else tmem_alloc(smem_u32(&sh.tmem), C::kTmemCols);
+  }
   griddep_wait();
   if (warp == 3) {  // the experts' first blocks and rows
     int nb = 0, nr = 0;
@@ -138,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       if (e < p.E) c = p.counts ? p.counts[e] : static_cast<int>(p.rows);
       bad |= c < 0 || c > p.rows;
       if (bad) c = 0;
-      int b = (c + kRows - 1) / kRows, r = p.counts ? (c + 127) / 128 : 0;
+      int b = (c + C::kRows - 1) / C::kRows, r = p.counts ? (c + 127) / 128 : 0;
       const int b_own = b, r_own = r;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -149,8 +193,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         }
       }
       if (e < p.E) {
-        first_block[e] = nb + b - b_own;
-        first_row[e] = (nr + r - r_own) * 128;
+        sh.first_block[e] = nb + b - b_own;
+        sh.first_row[e] = (nr + r - r_own) * 128;
         // the last row that is read has to exist (the padding after it need not)
         bad |= static_cast<int64_t>(nr + r - r_own) * 128 + c > p.rows;
       }
@@ -159,150 +203,225 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     }
     bad = __any_sync(0xFFFFFFFFu, bad);
     if (lane == 0) {
-      first_block[p.E] = bad ? 0 : nb;  // no block at all when the counts do not fit
-      if (bad) set_error(err, MOE_ERR_DEVICE_BOUNDS, 60);
+      sh.first_block[p.E] = bad ? 0 : nb;  // no block at all when the counts do not fit
+      if (bad && rank == 0) set_error(err, MOE_ERR_DEVICE_BOUNDS, 60);
     }
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // the peer's barriers are initialised
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  const int64_t tiles = static_cast<int64_t>(first_block[p.E]) * p.nt;
+  const uint32_t tmem = sh.tmem;
+  const int64_t tiles = static_cast<int64_t>(sh.first_block[p.E]) * p.nt;
   const int nks = (p.kt + 1) / 2;
+  uint32_t issued = 0;  // fills that this CTA's producer issued
 
   if (warp == 0) {
-    uint32_t it = 0, s = 0, phase = 1;
+    uint32_t s = 0, phase = 1;
     bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x) {
-      const Tile t = decode(p, first_block, first_row, tile);
-      const int bi = t.nvalid <= 16 ? 0 : (t.nvalid <= 64 ? 1 : (t.nvalid <= 128 ? 2 : 3));
-      const uint32_t bbytes = (bi == 0 ? 16 : (bi == 1 ? 64 : (bi == 2 ? 128 : kRows))) * 128;
-      const CUtensorMap* mb = &p.mapB[bi];
-      const int rt0 = t.row0 / 128, nsb = (t.row0 + t.nvalid - 1) / 128 - rt0 + 1;
-      const uint8_t* sfa = p.sb + t.e * p.sb_bytes + static_cast<int64_t>(t.n0 / 128) * p.kt * kMxTileBytes;
-      const uint8_t* sfb = p.sa + static_cast<int64_t>(rt0) * p.kt * kMxTileBytes;
-      const uint8_t* sfb1 = sfb + static_cast<int64_t>(p.kt) * kMxTileBytes;
-      const int wrow = t.e * p.N + t.n0;
-      for (int ks = 0; ks < nks; ++ks, ++it) {
-        if (it >= kStages) ok = warp_wait(empty(s), phase, abort_flag, err, 61, p.wait_ns);
+    const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
+      if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, x, y);
+      else tma_load_2d(dst, m, bar, x, y);
+    };
+    for (int64_t tile = unit; ok && tile < tiles; tile += units) {
+      const Tile t = decode<PAIR>(p, sh, tile);
+      const CUtensorMap* mb = &p.mapB[t.box];
+      const uint32_t bytes = C::kABytes + t.local * 128u + C::kSfaBytes + C::kSfbBytes;
+      const int wrow = t.e * p.N + t.n0 + 128 * rank, brow = t.row0 + t.local * rank;
+      const int wtile = t.e * p.sf_tiles + t.n0 / 128 + rank, btile = t.row0 / 128;
+      for (int ks = 0; ks < nks; ++ks) {
+        if (issued >= S) ok = warp_wait(empty(s), phase, abort_flag, err, 61, p.wait_ns);
         if (!ok) break;
-        const uint32_t st = base + s * kStageBytes, ssf = st + kABytes + kBBytes;
-        const uint32_t sfbytes = min(2, p.kt - 2 * ks) * kMxTileBytes;
+        const uint32_t st = base + s * C::kStageBytes, ssf = st + C::kABytes + C::kBBytes;
+        const uint32_t bar = PAIR ? mapa_shared(full(s), 0) : full(s);
         if (elect_one()) {
-          mbar_arrive_expect_tx(full(s), kABytes + bbytes + sfbytes * (1 + nsb));
-          tma_load_2d(st, &p.mapA, full(s), ks * 128, wrow);
-          tma_load_2d(st + kABytes, mb, full(s), ks * 128, t.row0);
-          bulk_load(ssf, sfa + 2 * ks * kMxTileBytes, sfbytes, full(s));
-          bulk_load(ssf + kSfaBytes, sfb + 2 * ks * kMxTileBytes, sfbytes, full(s));
-          if (nsb > 1)
-            bulk_load(ssf + kSfaBytes + 2 * kMxTileBytes, sfb1 + 2 * ks * kMxTileBytes, sfbytes, full(s));
+          sh.tx[s] = bytes;
+          if (rank == 0) mbar_arrive_expect_tx(full(s), bytes * C::kCtas);
+          load(st, &p.mapA, bar, ks * 128, wrow);
+          load(st + C::kABytes, mb, bar, ks * 128, brow);
+          load(ssf, &p.mapSa, bar, ks * 256, wtile);  // in words; zeros past the last K tile
+          load(ssf + C::kSfaBytes, &p.mapSb, bar, ks * 256, btile);
         }
         __syncwarp();
-        if (++s == kStages) {
+        ++issued;
+        if (++s == S) {
           s = 0;
           phase ^= 1;
         }
       }
     }
-    // copies still in flight land before the CTA ends (only after an abort are there any that
-    // the MMA warp has not waited for)
-    if (*abort_flag)
-      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-        mbar_wait(full(i % kStages), (i / kStages) & 1, nullptr, err, 62, p.wait_ns);
-  } else if (warp == 1) {
-    uint32_t s = 0, phase = 0, n = 0;
+  } else if (warp == 1 && rank == 0) {
+    uint32_t s = 0, phase = 0, n = 0, used = 0;
     bool ok = true;
-    for (int64_t tile = blockIdx.x; ok && tile < tiles; tile += gridDim.x, ++n) {
-      const Tile t = decode(p, first_block, first_row, tile);
-      const uint32_t acc = n & 1, tacc = tmem + acc * kRows;
+    for (int64_t tile = unit; ok && tile < tiles; tile += units, ++n) {
+      const Tile t = decode<PAIR>(p, sh, tile);
+      const uint32_t acc = n & 1, tacc = tmem + acc * C::kRows;
       if (n >= 2 && !warp_wait(tempty(acc), (n / 2 - 1) & 1, abort_flag, err, 63, p.wait_ns)) break;
       tc_fence_after();
-      // the block may start in the middle of a scale tile (row 64 of it: column 2)
+      // the block may start inside a scale tile (row 64 of it: column 2)
       const uint32_t sf_shift = (t.row0 % 128) / 32;
-      const int nsb = (t.row0 + t.nvalid - 1) / 128 - t.row0 / 128 + 1;
-      const uint32_t idesc = idesc_mxf4(128, (t.nvalid + 15) / 16 * 16);
+      const uint32_t idesc = idesc_mxf4(128 * C::kCtas, t.local * C::kCtas);
       for (int ks = 0; ks < nks; ++ks) {
         ok = warp_wait(full(s), phase, abort_flag, err, 64, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
-        const uint32_t st = base + s * kStageBytes;
-        const uint32_t ssf = st + kABytes + kBBytes;
-        const uint32_t tsf = tmem + kSfCol0 + s * kSfCols;
+        const uint32_t st = base + s * C::kStageBytes;
+        const uint32_t ssf = st + C::kABytes + C::kBBytes;
+        const uint32_t tsf = tmem + C::kSfCol0 + s * C::kSfCols;
         const int nkt = min(2, p.kt - 2 * ks);
         if (elect_one()) {
+          const auto copy = [&](uint32_t dst, uint32_t src) {
+            if constexpr (PAIR) tmem_cp_scales_pair(dst, src);
+            else tmem_cp_scales(dst, src);
+          };
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             if (i < nkt) {
-              tmem_cp_scales(tsf + 4 * i, ssf + i * kMxTileBytes);
-              tmem_cp_scales(tsf + 8 + 8 * i, ssf + kSfaBytes + i * kMxTileBytes);
-              if (nsb > 1) tmem_cp_scales(tsf + 12 + 8 * i, ssf + kSfaBytes + (2 + i) * kMxTileBytes);
+              copy(tsf + 4 * i, ssf + i * kMxTileBytes);
+#pragma unroll
+              for (int j = 0; j < C::kSfTiles; ++j)
+                copy(tsf + 8 + 4 * (C::kSfTiles * i + j), ssf + C::kSfaBytes + (2 * j + i) * kMxTileBytes);
             }
           }
           const uint64_t da = smem_desc_sw128(st, 16, 1024);
-          const uint64_t db = smem_desc_sw128(st + kABytes, 16, 1024);
+          const uint64_t db = smem_desc_sw128(st + C::kABytes, 16, 1024);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t id = (j & 1) * 2;
-            if (j < 2 * nkt)
-              umma_mxf4(tacc, da + 2 * j, db + 2 * j, idesc | (id << 4) | (id << 29),
-                        tsf + 4 * (j >> 1), tsf + 8 + 8 * (j >> 1) + sf_shift, ks > 0 || j > 0);
+            const uint32_t id = (j & 1) * 2, d = idesc | (id << 4) | (id << 29);
+            const uint32_t sfa = tsf + 4 * (j >> 1);
+            const uint32_t sfb = tsf + 8 + 4 * C::kSfTiles * (j >> 1) + sf_shift;
+            if (j < 2 * nkt) {
+              if constexpr (PAIR) umma_mxf4_pair(tacc, da + 2 * j, db + 2 * j, d, sfa, sfb, ks > 0 || j > 0);
+              else umma_mxf4(tacc, da + 2 * j, db + 2 * j, d, sfa, sfb, ks > 0 || j > 0);
+            }
           }
-          umma_commit(empty(s));
-          if (ks == nks - 1) umma_commit(tfull(acc));
+          if constexpr (PAIR) {
+            umma_commit_pair(empty(s), 3);
+            if (ks == nks - 1) umma_commit_pair(tfull(acc), 3);
+          } else {
+            umma_commit(empty(s));
+            if (ks == nks - 1) umma_commit(tfull(acc));
+          }
         }
         __syncwarp();
-        if (++s == kStages) {
+        ++used;
+        if (++s == S) {
           s = 0;
           phase ^= 1;
         }
       }
     }
     __syncwarp();
-    if (elect_one()) umma_commit(drain);  // every MMA issued is complete before TMEM is freed
+    if (elect_one()) {  // every MMA issued is complete before TMEM is freed
+      sh.consumed = used;
+      if constexpr (PAIR) umma_commit_pair(drain, 1);
+      else umma_commit(drain);
+    }
     mbar_wait(drain, 0, nullptr, err, 65, p.wait_ns);
   } else if (warp >= 4) {
     const int q = warp - 4;
+    uint32_t* tr = sh.transpose + q * 16 * kTrRow;
     uint32_t n = 0;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, ++n) {
-      const Tile t = decode(p, first_block, first_row, tile);
+    for (int64_t tile = unit; tile < tiles; tile += units, ++n) {
+      const Tile t = decode<PAIR>(p, sh, tile);
       const uint32_t acc = n & 1;
       if (!mbar_wait(tfull(acc), (n / 2) & 1, abort_flag, err, 66, p.wait_ns)) break;
       tc_fence_after();
-      const uint32_t tacc = tmem + acc * kRows + (static_cast<uint32_t>(32 * q) << 16);
-      const int col = t.n0 + 32 * q + lane;
+      const uint32_t tacc = tmem + acc * C::kRows + (static_cast<uint32_t>(32 * q) << 16);
+      const int col0 = t.n0 + 128 * rank + 32 * q;  // this warp's 32 output columns
       for (int r0 = 0; r0 < t.nvalid; r0 += 32) {
         float a[16], b[16];
         tmem_ld16x2(tacc + r0, tacc + r0 + 16, a, b);
         if (r0 + 32 >= t.nvalid) {  // the last read of this accumulator
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(tempty(acc));
+          if (lane == 0) {
+            if constexpr (PAIR) mbar_arrive_cluster_relaxed(mapa_shared(tempty(acc), 0));
+            else mbar_arrive(tempty(acc));
+          }
         }
-        if (col < p.N) {
-          const int64_t at = static_cast<int64_t>(t.row0 + r0) * p.ldo + col;
+        const int left = t.nvalid - r0;  // rows of this chunk (may exceed 32)
+        if (F32 || !p.vec) {
+          const int col = col0 + lane;
+          if (col < p.N) {
+            const int64_t at = static_cast<int64_t>(t.row0 + r0) * p.ldo + col;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float v = j < 16 ? a[j & 15] : b[j & 15];
-            if (r0 + j < t.nvalid) {
-              if constexpr (F32) static_cast<float*>(p.out)[at + j * p.ldo] = v;
-              else static_cast<uint16_t*>(p.out)[at + j * p.ldo] = bf16_bits(v);
+            for (int j = 0; j < 32; ++j) {
+              const float v = j < 16 ? a[j & 15] : b[j & 15];
+              if (j < left) {
+                if constexpr (F32) static_cast<float*>(p.out)[at + j * p.ldo] = v;
+                else static_cast<uint16_t*>(p.out)[at + j * p.ldo] = bf16_bits(v);
+              }
             }
           }
+        } else {
+          // rows 2 i and 2 i + 1 of a column as one word, through shared memory: a lane then
+          // holds eight columns of two rows and stores 16 bytes of each (storing 2 bytes per
+          // lane instead took longer than the MMAs of a tile with K = 2048)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            tr[i * kTrRow + lane] = i < 8 ? pack_bf16x2(a[2 * i & 15], a[(2 * i + 1) & 15])
+                                          : pack_bf16x2(b[2 * i & 15], b[(2 * i + 1) & 15]);
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int i = (lane >> 2) + 8 * h, c = 8 * (lane & 3);
+            const uint4 u = *reinterpret_cast<const uint4*>(&tr[i * kTrRow + c]);
+            const uint4 w = *reinterpret_cast<const uint4*>(&tr[i * kTrRow + c + 4]);
+            if (col0 + c < p.N) {
+              uint16_t* o = static_cast<uint16_t*>(p.out) +
+                            static_cast<int64_t>(t.row0 + r0 + 2 * i) * p.ldo + col0 + c;
+              if (2 * i < left)
+                st_v4(o, make_uint4(__byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410),
+                                    __byte_perm(w.x, w.y, 0x5410), __byte_perm(w.z, w.w, 0x5410)));
+              if (2 * i + 1 < left)
+                st_v4(o + p.ldo,
+                      make_uint4(__byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632),
+                                 __byte_perm(w.x, w.y, 0x7632), __byte_perm(w.z, w.w, 0x7632)));
+            }
+          }
+          __syncwarp();
         }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
+  // After an abort, loads may still be in flight: they land before TMEM is released and the
+  // CTAs exit.  With pairs all complete on rank 0's barriers: rank 1 reports its fills, rank 0
+  // balances the bytes of fills that only one CTA issued and waits, then both leave together.
+  if constexpr (PAIR) {
+    if (rank == 1 && warp == 0 && lane == 0) {
+      st_shared_cluster_u32(mapa_shared(smem_u32(&sh.peer_issued), 0), issued);
+      for (uint32_t s = 0; s < S; ++s)
+        st_shared_cluster_u32(mapa_shared(smem_u32(&sh.peer_tx[s]), 0), sh.tx[s]);
+    }
+    cluster_sync_all();
+  }
+  if (rank == 0 && warp == 0 && lane == 0) {
+    const uint32_t peer = PAIR ? *const_cast<volatile uint32_t*>(&sh.peer_issued) : issued;
+    const uint32_t end = issued > peer ? issued : peer;
+    for (uint32_t f = *const_cast<volatile uint32_t*>(&sh.consumed); f < end; ++f) {
+      const uint32_t s = f % S;
+      if (f >= issued) mbar_arrive_expect_tx(full(s), sh.peer_tx[s]);
+      else if (f >= peer) mbar_complete_tx(full(s), sh.tx[s]);
+      mbar_wait(full(s), (f / S) & 1, nullptr, err, 62, p.wait_ns);
+    }
+  }
+  if constexpr (PAIR) {
+    __syncthreads();
+    cluster_sync_all();  // no load, remote arrival or MMA into the peer after this point
+  }
   if (warp == 2) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
   }
 }
 
-template <bool F32>
-cudaError_t launch(const Params& p, int grid, cudaStream_t s) {
-  auto kern = gemm_fp4_kernel<F32>;
+template <bool F32, bool PAIR>
+cudaError_t launch(const Params& p, int units, cudaStream_t s) {
+  auto kern = gemm_fp4_kernel<F32, PAIR>;
   static std::atomic<unsigned long long> attr_set_mask{0ull};
   int dev = 0;
   cudaError_t st = cudaGetDevice(&dev);
@@ -310,25 +429,38 @@ cudaError_t launch(const Params& p, int grid, cudaStream_t s) {
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (bit == 0ull || !(attr_set_mask.load(std::memory_order_acquire) & bit)) {
     st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kSmemBytes));
+                              static_cast<int>(smem_bytes<PAIR>()));
     if (st != cudaSuccess) return st;
     attr_set_mask.fetch_or(bit, std::memory_order_release);
   }
-  return launch_pdl(kern, dim3(grid), dim3(kThreads), kSmemBytes, s, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(Cfg<PAIR>::kCtas * units));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<PAIR>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-}  // namespace
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                            const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                            const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// 2-D map of `rows` rows of `inner` bytes, 128-byte swizzle, boxes of 128 bytes x box_rows
-// (bytes past the row's end and rows past the last are read as zeros).
-CUtensorMap make_map_u8(const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
-                        cudaError_t* st) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                              const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                              const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// Codes: `rows` rows of `inner` bytes, 128-byte swizzle, boxes of 128 bytes x box_rows (bytes
+// past the row's end and rows past the last are read as zeros).
+CUtensorMap code_map(const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
+                     cudaError_t* st) {
   CUtensorMap m = {};
   auto enc = reinterpret_cast<Encode>(tensor_map_encoder());
   const cuuint64_t dims[2] = {inner, rows};
@@ -342,6 +474,53 @@ CUtensorMap make_map_u8(const void* base, uint64_t inner, uint64_t rows, uint32_
     *st = cudaErrorInvalidValue;
   return m;
 }
+
+// Scale tiles: `tiles` rows of kt tiles (128 words each), boxes of two tiles x box_tiles rows.
+CUtensorMap scale_map(const void* base, int kt, uint64_t tiles, uint32_t box_tiles, cudaError_t* st) {
+  CUtensorMap m = {};
+  auto enc = reinterpret_cast<Encode>(tensor_map_encoder());
+  const cuuint64_t dims[2] = {128ull * kt, tiles};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kt) * kMxTileBytes};
+  const cuuint32_t box[2] = {256, box_tiles};
+  const cuuint32_t ones[2] = {1, 1};
+  if (!enc || enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides,
+                  box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    *st = cudaErrorInvalidValue;
+  return m;
+}
+
+// Pairs when their tiles give every pair of SMs work, or when there are more rows than singles
+// take in one block and the weights are shared by all: measured on GB300.
+bool use_pairs(int64_t rows, int N, int E, bool grouped, int sms) {
+  const int64_t blocks = (rows + Cfg<true>::kRows - 1) / Cfg<true>::kRows + (grouped ? E / 2 : 0);
+  return blocks * ((N + 255) / 256) >= sms / 2;
+}
+
+template <bool PAIR>
+cudaError_t run(Params& p, const uint8_t* a, const uint8_t* a_scales, const uint8_t* b,
+                const uint8_t* b_scales, int K, int out_dtype, int sms, cudaStream_t stream) {
+  using C = Cfg<PAIR>;
+  cudaError_t st = cudaSuccess;
+  const uint64_t inner = static_cast<uint64_t>(mx_cols(K) / 2);
+  p.nt = (p.N + 128 * C::kCtas - 1) / (128 * C::kCtas);
+  p.mapA = code_map(b, inner, static_cast<uint64_t>(p.E) * p.N, 128, &st);
+  p.mapSa = scale_map(b_scales, p.kt, static_cast<uint64_t>(p.E) * p.sf_tiles, 1, &st);
+  p.mapSb = scale_map(a_scales, p.kt, static_cast<uint64_t>((p.rows + 127) / 128), C::kSfTiles, &st);
+  const int boxes[kBoxes] = {16, 32, 64, 96};
+  for (int i = 0; i < (PAIR ? 4 : 3); ++i)  // no block has more than `rows`
+    if (i == 0 || p.rows > boxes[i - 1])
+      p.mapB[i] = code_map(a, inner, static_cast<uint64_t>(p.rows), boxes[i], &st);
+  if (st != cudaSuccess) return st;
+  const int64_t blocks = (p.rows + C::kRows - 1) / C::kRows + (p.counts ? p.E : 0);
+  const int64_t tiles = blocks * p.nt;
+  const int units = static_cast<int>(tiles < sms / C::kCtas ? tiles : sms / C::kCtas);
+  return out_dtype == MOE_DTYPE_F32 ? launch<true, PAIR>(p, units, stream)
+                                    : launch<false, PAIR>(p, units, stream);
+}
+
+}  // namespace
 
 }  // namespace moe
 
@@ -363,31 +542,22 @@ moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t row
   if (E > kMaxE || N > kMaxFp4Cols || K > kMaxFp4Cols || rows > INT32_MAX - 256 ||
       static_cast<int64_t>(E) * N > INT32_MAX)
     return MOE_ERR_UNSUPPORTED;
-  const uint64_t inner = static_cast<uint64_t>(mx_cols(K) / 2);
-  cudaError_t st = cudaSuccess;
   Params p = {};
-  p.sa = a_scales;
-  p.sb = b_scales;
   p.counts = counts;
   p.rows = rows;
-  p.sb_bytes = mx_scale_bytes(N, K);
   p.N = N;
   p.kt = static_cast<int>(mx_cols(K) / 128);
   p.E = E;
-  p.nt = (N + 127) / 128;
+  p.sf_tiles = (N + 127) / 128;
   p.ldo = N;
+  p.vec = N % 8 == 0;
   p.out = out;
   p.wait_ns = wait_limit_ns();
-  p.mapA = make_map_u8(b, inner, static_cast<uint64_t>(E) * N, 128, &st);
-  const uint32_t boxes[4] = {16, 64, 128, kRows};
-  for (int i = 0; i < 4; ++i)
-    p.mapB[i] = make_map_u8(a, inner, static_cast<uint64_t>(rows), boxes[i], &st);
   const int sms = num_sms_of_current_device();
-  if (st != cudaSuccess) return MOE_ERR_CUDA;
-  const int64_t blocks = (rows + kRows - 1) / kRows + (counts ? E : 0);
-  const int64_t tiles = blocks * p.nt;
-  const int grid = static_cast<int>(tiles < sms ? tiles : sms);
-  st = out_dtype == MOE_DTYPE_F32 ? launch<true>(p, grid, stream) : launch<false>(p, grid, stream);
+  const cudaError_t st =
+      use_pairs(rows, N, E, counts != nullptr, sms)
+          ? run<true>(p, a, a_scales, b, b_scales, K, out_dtype, sms, stream)
+          : run<false>(p, a, a_scales, b, b_scales, K, out_dtype, sms, stream);
   return st == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
