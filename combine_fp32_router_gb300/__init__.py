@@ -237,26 +237,31 @@ _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
 
 
 # The 4-bit entry points run in a few microseconds, about as long as marshalling a call takes:
-# they pass addresses as plain ints and size checks stay in Python.
+# they pass addresses as plain ints, keep size checks in Python and read the current stream's
+# handle without building a Stream object (2 us each).
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _addr(t):
     if not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
     return t.data_ptr()
 
 
-def _raw_stream(stream, device):
+def _raw_stream(stream, t):
     if stream is not None:
         return stream.cuda_stream
-    if device.type != "cuda":
-        raise ValueError("tensor arguments must be CUDA tensors: got %s" % device)
-    return torch.cuda.current_stream(device).cuda_stream
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    return _current_raw_stream(t.get_device())
 
 
 def _dtype(dt):
-    try:
-        return _DTYPES[dt]
-    except KeyError:
-        raise ValueError("dtype must be bfloat16, float16 or float32: got %s" % dt) from None
+    code = _DTYPES.get(dt)
+    if code is None:
+        raise ValueError("dtype must be bfloat16, float16 or float32: got %s" % dt)
+    return code
 
 
 def moe_fp4_row_bytes(cols):
@@ -287,7 +292,7 @@ def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
     elif _nbytes(scales) < sb:
         raise ValueError("scales too small for %d x %d values" % (rows, cols))
     _check(_lib.moe_quantize_rows_fp4(x.data_ptr(), dt, rows, cols, stride, _addr(q),
-                                      _addr(scales), _raw_stream(stream, x.device)),
+                                      _addr(scales), _raw_stream(stream, x)),
            "moe_quantize_rows_fp4")
     return q, scales
 
@@ -303,7 +308,7 @@ def moe_dequantize_rows_fp4(q, scales, cols, dtype=torch.bfloat16, stream=None):
         raise ValueError("q or scales do not hold rows of %d values" % cols)
     out = torch.empty((*shape[:-1], cols), dtype=dtype, device=q.device)
     _check(_lib.moe_dequantize_rows_fp4(_addr(q), _addr(scales), groups, rows, cols, dt,
-                                        out.data_ptr(), _raw_stream(stream, q.device)),
+                                        out.data_ptr(), _raw_stream(stream, q)),
            "moe_dequantize_rows_fp4")
     return out
 
@@ -317,7 +322,7 @@ def moe_quantize_weights_fp4(W, stream=None):
     Wq = torch.empty((E, N, moe_fp4_row_bytes(K)), dtype=torch.uint8, device=W.device)
     sc = torch.empty((E, moe_fp4_scale_bytes(N, K)), dtype=torch.uint8, device=W.device)
     _check(_lib.moe_quantize_weights_fp4(_addr(W), E, K, N, Wq.data_ptr(), sc.data_ptr(),
-                                         _raw_stream(stream, W.device)),
+                                         _raw_stream(stream, W)),
            "moe_quantize_weights_fp4")
     return Wq, sc
 
@@ -340,7 +345,7 @@ def moe_gemm_fp4(aq, a_scales, bq, b_scales, out, K, counts=None, stream=None):
     _check(_lib.moe_gemm_fp4(_addr(aq), _addr(a_scales), rows,
                              None if counts is None else _addr(counts), _addr(bq),
                              _addr(b_scales), E, N, K, _addr(out), _dtype(out.dtype),
-                             _raw_stream(stream, out.device)), "moe_gemm_fp4")
+                             _raw_stream(stream, out)), "moe_gemm_fp4")
 
 
 def moe_gemm_fp4_get_error(stream=None):
@@ -375,7 +380,7 @@ def moe_forward_few_fp4(x, logits, router, W1q, W3q, W2q, w1_scales, w3_scales, 
                                     None if router is None else _addr(router), _addr(W1q),
                                     _addr(W3q), _addr(W2q), _addr(w1_scales), _addr(w3_scales),
                                     _addr(w2_scales), T, d, E, k, d_ff, _addr(out), _addr(ws),
-                                    _nbytes(ws), _raw_stream(stream, x.device)),
+                                    _nbytes(ws), _raw_stream(stream, x)),
            "moe_forward_few_fp4")
 
 

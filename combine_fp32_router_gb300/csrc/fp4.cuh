@@ -62,6 +62,21 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
+// One such code, and the value of one
+__device__ __forceinline__ uint32_t e2m1(float v) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "mov.b32 %0, {a, a, a, a};\n\t}"
+      : "=r"(r)
+      : "f"(v), "f"(0.0f));
+  return r & 15u;
+}
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+  const uint32_t m = code & 7u;
+  const float v = m <= 4u ? 0.5f * static_cast<float>(m) : (m < 7u ? static_cast<float>(m) - 2.0f : 6.0f);
+  return (code & 8u) ? -v : v;
+}
 // Eight codes (four bytes) -> four half2 pairs, exact
 __device__ __forceinline__ void e2m1x8_to_half(uint32_t w, uint32_t (&h)[4]) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"

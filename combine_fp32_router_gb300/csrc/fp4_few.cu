@@ -76,7 +76,7 @@ FewLayout few_layout(int64_t T, int d, int E, int k, int dff) {
   L.ticket = take(4);
   L.cnt1 = take(G * (dff / 32) * 4);
   L.done1 = take(G * 4);
-  L.done2 = take(static_cast<size_t>(d / 32) * 4);
+  L.done2 = take(static_cast<size_t>(T) * (d / 32) * 4);
   L.xdone = take(G * 4);
   L.clear_end = at;
   L.xq = take(T * kTerms * (d / 2));
@@ -294,7 +294,7 @@ struct Shared {
   Unit acc_unit[kGroups];
   uint64_t bars[3 * kMaxStages + 2 * kGroups + 1];
   int2 total[kMaxE / 32];  // rows and groups of 32 experts
-  int32_t groups;
+  int32_t groups, ticket;
   int32_t abort_flag;
   uint32_t tmem;
 };
@@ -388,38 +388,29 @@ __device__ __forceinline__ int row_of(const Shared& sh, int t, int j) {
   return sh.base[e] + __popc(sh.mask[e] & ((1u << t) - 1u));
 }
 
-// Rows of gathered tokens: the terms of a group's tokens and their scale words, in the layout
-// that h has.  By one warp.
-__device__ void gather_group(const ExpertParams& p, const Shared& sh, int gi, int lane) {
+// The terms of a group's tokens and their scale words, copied into the layout that h has.  By
+// the whole CTA: 16 bytes of codes per thread, then the scale words.
+__device__ void gather_group(const ExpertParams& p, const Shared& sh, int gi) {
   const Group gr = sh.group[gi];
   const int row_bytes = p.d / 2, kt = p.d / 128, rows = p.cols * kTerms;
-  uint32_t left = gr.tokens;
-  for (int c = 0; c < gr.n; ++c, left &= left - 1u) {
+  const int n16 = kTerms * row_bytes / 16, words = kt * kTerms;  // of a token
+  for (int i = threadIdx.x; i < gr.n * (n16 + words); i += kThreads) {
+    const int c = i / (n16 + words), o = i % (n16 + words);
+    uint32_t left = gr.tokens;
+    for (int j = 0; j < c; ++j) left &= left - 1u;
     const int t = __ffs(left) - 1;
-    // a token's terms are neighbours on both sides
-    const uint8_t* src = p.xq + static_cast<int64_t>(t) * kTerms * row_bytes;
-    uint8_t* dst = p.gq + (static_cast<int64_t>(gi) * rows + c * kTerms) * row_bytes;
-    const int n16 = kTerms * row_bytes / 16;
-    for (int i = lane; i < n16; i += 32 * 8) {
-      uint4 v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + 32 * j < n16) v[j] = ld_v4(src + 16 * (i + 32 * j));
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (i + 32 * j < n16) st_v4(dst + 16 * (i + 32 * j), v[j]);
-    }
-    for (int i = lane; i < kt * kTerms; i += 32) {
-      const int tile = i / kTerms, r = i % kTerms;
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(
-          p.xs + (static_cast<int64_t>(tile) * p.T * kTerms + t * kTerms + r) * 4);
+    if (o < n16) {
+      st_v4(p.gq + (static_cast<int64_t>(gi) * rows + c * kTerms) * row_bytes + 16 * o,
+            ld_v4(p.xq + static_cast<int64_t>(t) * kTerms * row_bytes + 16 * o));
+    } else {
+      const int tile = (o - n16) / kTerms, r = (o - n16) % kTerms;
       *reinterpret_cast<uint32_t*>(p.gs + (static_cast<int64_t>(gi) * kt + tile) * kMxTileBytes +
-                                   sf_at(c * kTerms + r, 0)) = w;
+                                   sf_at(c * kTerms + r, 0)) =
+          __ldcg(reinterpret_cast<const uint32_t*>(
+              p.xs + (static_cast<int64_t>(tile) * p.T * kTerms + t * kTerms + r) * 4));
     }
   }
   fence_proxy_async_global();
-  __syncwarp();
-  if (lane == 0) red_release_add(p.xdone + gi, 1);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -523,6 +514,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ht = p.dff / 128, yt = p.d / 128, Q = 2 * p.parts;
   const int n0 = direct ? 0 : groups, n1 = n0 + groups * ht * Q, n_units = n1 + groups * yt;
   const int kt1 = p.d / 128, kt2 = p.dff / 128;
+  if (!direct) {  // the first units: gathering
+    while (true) {
+      if (threadIdx.x == 0) sh.ticket = next;
+      __syncthreads();
+      const int u = sh.ticket;
+      if (u >= n0) break;
+      gather_group(p, sh, u);
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        red_release_add(p.xdone + u, 1);
+        next = atomicAdd(p.ticket, 1);
+      }
+    }
+  }
   const int st1 = (kt1 + kStageKt - 1) / kStageKt, st2 = (kt2 + kStageKt - 1) / kStageKt;
 
   if (warp == 0) {
@@ -533,10 +538,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int u = __shfl_sync(0xFFFFFFFFu, next, 0);
       const bool work = u < n_units;
       if (lane == 0 && work) next = atomicAdd(p.ticket, 1);  // used after this unit's loads
-      if (u < n0) {
-        gather_group(p, sh, u, lane);
-        continue;
-      }
       Unit un = {0, 0, 0, 0};
       int ks0 = 0, ks1 = 1;
       if (work && u < n1) {
@@ -740,15 +741,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = kTerms - 2; r >= 0; --r) a += v[c * kTerms + r];
         return a;
       };
-      if (un.kind == 1) {
-        // this K range's sums of 32 columns of x W1 or x W3
-        float* slot = p.part + 32 * qd + lane;
-        const int64_t at = static_cast<int64_t>(un.tile) * Q;  // of a row's ht * Q slots of 128
+      // 32 columns of this K range's x W1 or x W3, or of y, per token
+      const bool first = un.kind == 1;
+      float* dst = first ? p.part + (static_cast<int64_t>(un.tile) * Q + un.q) * 128 + 32 * qd + lane
+                         : p.y + 128 * un.tile + 32 * qd + lane;
+      const int64_t row_stride = first ? static_cast<int64_t>(ht) * Q * 128 : p.d;
 #pragma unroll
-        for (int c = 0; c < kTok; ++c)
-          if (active(c))
-            __stcg(slot + ((row_at(c) * static_cast<int64_t>(ht) * Q) + at + un.q) * 128, sum(c));
-        __syncwarp();
+      for (int c = 0; c < kTok; ++c)
+        if (active(c)) __stcg(dst + row_at(c) * row_stride, sum(c));
+      __syncwarp();
+      if (first) {
         int last = 0;
         if (lane == 0) last = add_acq_rel(p.cnt1 + (un.group * ht + un.tile) * 4 + qd, 1) == Q - 1;
         last = __shfl_sync(0xFFFFFFFFu, last, 0);
@@ -756,33 +758,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!last) continue;
         // all ranges of both are there: h of a 32-value block per token, in MXFP4 terms
         const int row_bytes = p.dff / 2;
+#pragma unroll 1
         for (int c = 0; c < p.cols; ++c) {
           if (!active(c)) continue;
-          const float* src = slot + ((row_at(c) * static_cast<int64_t>(ht) * Q) + at) * 128;
+          const float* src = dst + row_at(c) * row_stride - un.q * 128;
           float a = 0.0f, b = 0.0f;
+#pragma unroll 4
           for (int q = 0; q < p.parts; ++q) {
             a += __ldcg(src + (2 * q) * 128);
             b += __ldcg(src + (2 * q + 1) * 128);
           }
           float h = a / (1.0f + expf(-a)) * b;
           uint8_t* hq = p.hq + (static_cast<int64_t>(un.group) * p.cols + c) * kTerms * row_bytes +
-                        64 * un.tile + 16 * qd;
+                        64 * un.tile + 16 * qd + lane / 2;
           uint8_t* hs = p.hs + (static_cast<int64_t>(un.group) * ht + un.tile) * kMxTileBytes;
-#pragma unroll
-          for (int r = 0; r < kTerms; ++r) {
+#pragma unroll 1
+          for (int r = 0; r < kTerms; ++r, hq += row_bytes) {
             const uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(h) & 0x7FFFFFFFu);
             const uint32_t s = term_scale(amax);
-            float z[8] = {s == 255u ? 0.0f : h * mx_inverse_scale(s), 0, 0, 0, 0, 0, 0, 0};
-            uint32_t code = e2m1x8(z) & 15u;
-            uint32_t hh[4];
-            e2m1x8_to_half(code, hh);
-            h = fmaf(-__half2float(__ushort_as_half(static_cast<uint16_t>(hh[0]))), mx_scale(s), h);
+            const uint32_t mine = e2m1(s == 255u ? 0.0f : h * mx_inverse_scale(s));
+            h = fmaf(-e2m1_value(mine), mx_scale(s), h);
             // eight lanes' codes in the first one's word
+            uint32_t code = mine;
             code |= __shfl_down_sync(0xFFFFFFFFu, code, 1) << 4;
             code |= __shfl_down_sync(0xFFFFFFFFu, code, 2) << 8;
             code |= __shfl_down_sync(0xFFFFFFFFu, code, 4) << 16;
-            if ((lane & 7) == 0)
-              *reinterpret_cast<uint32_t*>(hq + r * static_cast<int64_t>(row_bytes) + lane / 2) = code;
+            if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(hq) = code;
             if (lane == 0) hs[sf_at(c * kTerms + r, qd)] = static_cast<uint8_t>(s);
           }
         }
@@ -790,24 +791,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) red_release_add(p.done1 + un.group, 1);
       } else {
-        const int col = 128 * un.tile + 32 * qd + lane;
-#pragma unroll
-        for (int c = 0; c < kTok; ++c)
-          if (active(c)) __stcg(p.y + static_cast<int64_t>(row_at(c)) * p.d + col, sum(c));
+        // lane c: token c's arrival at these 32 columns; who brings the k-th row of a token
+        // combines it, in slot order
+        bool last = false;
+        if (lane < kTok && active(lane)) {
+          uint32_t left = gr.tokens;
+          if (!direct)
+            for (int j = 0; j < lane; ++j) left &= left - 1u;
+          const int t = direct ? lane : __ffs(left) - 1;
+          last = add_acq_rel(p.done2 + t * (p.d / 32) + 4 * un.tile + qd, 1) == p.k - 1;
+        }
+        uint32_t ready = __ballot_sync(0xFFFFFFFFu, last);
         __syncwarp();
-        int last = 0;
-        if (lane == 0)
-          last = add_acq_rel(p.done2 + 4 * un.tile + qd, gr.n) + gr.n == p.T * p.k;
-        last = __shfl_sync(0xFFFFFFFFu, last, 0);
-        __syncwarp();  // the lanes' loads come after lane 0's acquire
-        if (!last) continue;
-        // the last rows of these 32 columns: combine them, in slot order
-        for (int t = 0; t < p.T; ++t) {
+        const float* y = p.y + 128 * un.tile + 32 * qd + lane;
+#pragma unroll 1
+        for (; ready; ready &= ready - 1u) {
+          uint32_t left = gr.tokens;
+          const int c = __ffs(ready) - 1;
+          if (!direct)
+            for (int j = 0; j < c; ++j) left &= left - 1u;
+          const int t = direct ? c : __ffs(left) - 1;
           float o = 0.0f;
-          for (int j = 0; j < p.k; ++j)
-            o = fmaf(sh.gate[t][j],
-                     __ldcg(p.y + static_cast<int64_t>(row_of(sh, t, j)) * p.d + col), o);
-          p.out[static_cast<int64_t>(t) * p.d + col] = bf16_bits(o);
+#pragma unroll 1
+          for (int jb = 0; jb < p.k; jb += 4) {
+            float v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (jb + j < p.k) v[j] = __ldcg(y + static_cast<int64_t>(row_of(sh, t, jb + j)) * p.d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (jb + j < p.k) o = fmaf(sh.gate[t][jb + j], v[j], o);
+          }
+          p.out[static_cast<int64_t>(t) * p.d + 128 * un.tile + 32 * qd + lane] = bf16_bits(o);
         }
       }
     }
