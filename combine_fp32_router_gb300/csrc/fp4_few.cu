@@ -38,7 +38,7 @@ constexpr int kStageKt = 4;              // 128-value K tiles per stage
 constexpr int kPartStages = 4;           // stages of a K range of W1 and W3 (at most)
 constexpr uint32_t kABytes = 128 * kStageKt * 64;
 constexpr uint32_t kSfBytes = kStageKt * kMxTileBytes;
-constexpr int kMaxStages = 5;
+constexpr int kMaxStages = 4;  // 160 KB in flight per SM; more only lengthens every other round trip
 // Four groups of four warps finish units in turn, each with an accumulator of its own: publishing
 // a unit's sums (store, fence, counter) and, for the last of a tile, SwiGLU and the terms of h
 // take 2 to 4 us, about as long as streaming the next unit's weights.  With one group the stream
@@ -52,7 +52,7 @@ static_assert(kSfCol0 + kMaxStages * kSfCols <= 512 && kMaxN <= static_cast<int>
 constexpr int kThreads = 128 + 128 * kGroups;
 
 struct FewLayout {
-  size_t err, ticket, cnt1, done1, done2, xdone, clear_end, xq, xs, gq, gs, hq, hs, part, y, total;
+  size_t err, ticket, done1, xdone, clear_end, xq, xs, gq, gs, hq, hs, part, y, total;
   int cols, parts;
   int64_t groups;
 };
@@ -74,9 +74,7 @@ FewLayout few_layout(int64_t T, int d, int E, int k, int dff) {
   const size_t rows = static_cast<size_t>(L.cols) * kTerms;
   L.err = take(sizeof(DevErr));
   L.ticket = take(4);
-  L.cnt1 = take(G * (dff / 32) * 4);
   L.done1 = take(G * 4);
-  L.done2 = take(static_cast<size_t>(T) * (d / 32) * 4);
   L.xdone = take(G * 4);
   L.clear_end = at;
   L.xq = take(T * kTerms * (d / 2));
@@ -98,6 +96,50 @@ __device__ __forceinline__ uint32_t term_scale(uint32_t amax) {
   const uint32_t s = mx_scale_byte(amax);
   return s + ((amax & 0x7FFFFFu) > 0x400000u && amax >= 0x01000000u && s < 255u ? 1u : 0u);
 }
+// Sums that pass between CTAs (of K ranges, and the rows of y) are their own arrival flags: the
+// router's launch fills their places with this NaN, which no sum is stored as, and who needs
+// them reads until it is gone.  (A counter needs the stores released first, which took 5 us
+// per unit under the weight stream.)
+constexpr uint32_t kNotYet = 0xFFFFFFFFu;
+__device__ __forceinline__ void put_sum(float* p, float v) {
+  const uint32_t u = __float_as_uint(v);
+  asm volatile("st.relaxed.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(u == kNotYet ? 0x7FFFFFFFu : u)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t look(const float* p) {
+  uint32_t u;
+  asm volatile("ld.relaxed.gpu.global.u32 %0, [%1];" : "=r"(u) : "l"(p) : "memory");
+  return u;
+}
+// n <= 8 sums (0 past them) for a whole warp, each lane its own, from at(0), at(1), ...  False
+// after `limit_ns` or an abort.
+template <typename At>
+__device__ __forceinline__ bool get_sums(const At& at, int n, float (&v)[8], volatile int* abort_flag,
+                                         DevErr* err, int site, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+  for (uint32_t turn = 0;; ++turn) {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = i < n ? look(at(i)) : 0u;
+    bool there = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      there = there && u[i] != kNotYet;
+      v[i] = __uint_as_float(u[i]);
+    }
+    if (__all_sync(0xFFFFFFFFu, there)) return true;
+    if (turn == 64) t0 = global_ns();
+    if (turn > 64 && (turn & 63u) == 0u) {
+      const bool late = global_ns() - t0 > limit_ns;
+      if (late) {
+        *abort_flag = 1;
+        set_error(err, MOE_ERR_TIMEOUT, site);
+      }
+      if (__any_sync(0xFFFFFFFFu, late || *abort_flag != 0)) return false;
+    }
+  }
+}
+
 // Byte of (row n < 48, block b of the 128-value tile) in a scale tile
 __device__ __forceinline__ uint32_t sf_at(int n, int b) {
   return (n & 31) * 16 + (n >> 5) * 4 + b;
@@ -113,6 +155,8 @@ struct RouterParams {
   DevErr* err;
   int32_t* clear;  // counters, contiguous
   int64_t n_clear;
+  uint4* places;   // of sums that pass between CTAs, to be marked kNotYet
+  int64_t n_places;  // in 16 bytes
   uint8_t* xq;
   uint8_t* xs;
 };
@@ -120,7 +164,7 @@ struct RouterParams {
 constexpr int kRouterExperts = 2;  // per CTA
 constexpr int kRouterThreads = 256;
 
-// Every CTA clears its share of the counters; the first `conv` write x in MXFP4 terms; each of
+// Every CTA clears its share of the counters and marks its share of the sums' places; the first `conv` write x in MXFP4 terms; each of
 // the others computes the logits of two experts for up to TB tokens (blockIdx.y: which): warp w
 // sums the 128-value pieces w, w + 8, ... of d, lanes then warps are added in a fixed order.
 template <int TB>
@@ -134,6 +178,9 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams
     for (int64_t i = blockIdx.x * static_cast<int64_t>(kRouterThreads) + threadIdx.x; i < p.n_clear;
          i += static_cast<int64_t>(gridDim.x) * kRouterThreads)
       p.clear[i] = 0;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(kRouterThreads) + threadIdx.x; i < p.n_places;
+         i += static_cast<int64_t>(gridDim.x) * kRouterThreads)
+      p.places[i] = make_uint4(kNotYet, kNotYet, kNotYet, kNotYet);
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.err = DevErr{};
   }
   if (static_cast<int>(blockIdx.x) < p.conv) {
@@ -258,7 +305,7 @@ struct ExpertParams {
   uint8_t *gq, *gs, *hq, *hs;  // terms of gathered tokens and of h, per group
   float *part, *y;
   uint16_t* out;
-  int32_t *ticket, *cnt1, *done1, *done2, *xdone;
+  int32_t *ticket, *done1, *xdone;
   DevErr* err;
   uint64_t wait_ns;
   // codes of W1, W3, W2 (boxes of 128 rows) and of x and h terms (boxes of n rows), 128 bytes
@@ -289,6 +336,7 @@ struct Shared {
   uint32_t mask[kMaxE];
   int32_t base[kMaxE];  // first row of an expert's tokens
   float gate[kMaxT][kMaxK];
+  int32_t last_e[kMaxT];  // a token's highest expert
   uint16_t slot_e[kMaxT][kMaxK];
   StageMeta meta[kMaxStages];
   Unit acc_unit[kGroups];
@@ -316,56 +364,44 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint3
       : "memory");
 }
 
-// Arrival on a counter that publishes the warp's stores (made before a __syncwarp) and takes in
-// those of the arrivals before it.
-__device__ __forceinline__ int32_t add_acq_rel(int32_t* p, int32_t v) {
-  int32_t old;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-  return old;
-}
-
-// Top-k and gate of one token by one warp, the same selection and arithmetic as topk_token:
-// lanes keep their own best logit, so a round is one max-reduction and a vote, and only the
-// winner looks through its logits again.  (One token waits for this before anything else can
-// start: 2.0 us instead of 3.0 us for the eight of 256 experts.)
+// Top-k and gate of one token by one warp, the same selection and arithmetic as topk_token.  A
+// lane sorts its logits first (best one on top, ties by index), so a round is a max-reduction
+// over the lanes' best, a vote, and the winner's step to its next one.
 template <int EPL>
 __device__ __forceinline__ void route_token(const ExpertParams& p, Shared& sh, int t, int lane) {
-  uint32_t key[EPL];
+  uint32_t key[EPL], idx[EPL];
 #pragma unroll
-  for (int c = 0; c < EPL; ++c)
-    key[c] = order_key(lane + 32 * c < p.E
-                           ? __ldcg(p.logits + static_cast<int64_t>(t) * p.E + lane + 32 * c)
-                           : 0.0f);
-  uint32_t live = 0;  // bit c: expert lane + 32 c exists and is not yet taken
+  for (int c = 0; c < EPL; ++c) {
+    idx[c] = lane + 32 * c;
+    key[c] = 0u;  // below every logit's key but the NaN with all bits set
+    if (lane + 32 * c < p.E) key[c] = order_key(__ldcg(p.logits + static_cast<int64_t>(t) * p.E + lane + 32 * c));
+    else idx[c] = 0xFFFFu;  // no expert: after every other
+  }
 #pragma unroll
-  for (int c = 0; c < EPL; ++c)
-    if (lane + 32 * c < p.E) live |= 1u << c;
-  uint32_t best = 0, at = 0;  // the lane's largest live key (0 without one) and the first holder
-  const auto rescan = [&] {
-    best = 0;
-    at = 0;
+  for (int a = 1; a < EPL; ++a)  // insertion, as fixed exchanges
 #pragma unroll
-    for (int c = 0; c < EPL; ++c)
-      if (((live >> c) & 1u) && key[c] > best) {
-        best = key[c];
-        at = c;
-      }
-  };
-  rescan();
+    for (int c = a; c > 0; --c) {
+      const bool swap = key[c] > key[c - 1] || (key[c] == key[c - 1] && idx[c] < idx[c - 1]);
+      const uint32_t k0 = swap ? key[c] : key[c - 1], k1 = swap ? key[c - 1] : key[c];
+      const uint32_t i0 = swap ? idx[c] : idx[c - 1], i1 = swap ? idx[c - 1] : idx[c];
+      key[c - 1] = k0;
+      key[c] = k1;
+      idx[c - 1] = i0;
+      idx[c] = i1;
+    }
   int sel_e = 0;
   float sel_v = 0.0f;
   for (int j = 0; j < p.k; ++j) {
-    const uint32_t bk = __reduce_max_sync(0xFFFFFFFFu, best);
-    const bool holds = best == bk && live != 0u;
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, holds);
-    uint32_t e = at * 32 + lane;
-    if (who & (who - 1u)) e = __reduce_min_sync(0xFFFFFFFFu, holds ? e : 0xFFFFFFFFu);  // a tie
-    else e = __shfl_sync(0xFFFFFFFFu, e, __ffs(who) - 1);
-    if ((e & 31u) == static_cast<uint32_t>(lane)) {
-      live &= ~(1u << (e >> 5));
-      rescan();
+    const uint32_t bk = __reduce_max_sync(0xFFFFFFFFu, key[0]);
+    const uint32_t who = __ballot_sync(0xFFFFFFFFu, key[0] == bk);
+    uint32_t e = __shfl_sync(0xFFFFFFFFu, idx[0], __ffs(who) - 1);
+    if (who & (who - 1u)) e = __reduce_min_sync(0xFFFFFFFFu, key[0] == bk ? idx[0] : 0xFFFFu);  // a tie
+    const bool won = idx[0] == e;
+#pragma unroll
+    for (int c = 0; c < EPL; ++c) {
+      key[c] = won ? (c + 1 < EPL ? key[c + 1 < EPL ? c + 1 : c] : 0u) : key[c];
+      idx[c] = won ? (c + 1 < EPL ? idx[c + 1 < EPL ? c + 1 : c] : 0xFFFFu) : idx[c];
     }
-    __syncwarp();
     if (lane == j) {
       sel_e = static_cast<int>(e);
       sel_v = order_value(bk);
@@ -375,11 +411,31 @@ __device__ __forceinline__ void route_token(const ExpertParams& p, Shared& sh, i
   const float ex = lane < p.k ? expf(sel_v - v0) : 0.0f;
   float sum = 0.0f;
   for (int j = 0; j < p.k; ++j) sum += __shfl_sync(0xFFFFFFFFu, ex, j);
+  const int top = __reduce_max_sync(0xFFFFFFFFu, lane < p.k ? sel_e : 0);
   if (lane < p.k) {
     sh.slot_e[t][lane] = static_cast<uint16_t>(sel_e);
     sh.gate[t][lane] = ex / sum;
     atomicOr(&sh.mask[sel_e], 1u << t);
   }
+  if (lane == 0) sh.last_e[t] = top;
+}
+
+// The same for up to 1024 experts, whose sorted lists would not fit the registers.
+__device__ void route_token_any(const ExpertParams& p, Shared& sh, int t, int lane) {
+  float v[kMaxE / 32];
+#pragma unroll
+  for (int c = 0; c < kMaxE / 32; ++c)
+    v[c] = lane + 32 * c < p.E ? __ldcg(p.logits + static_cast<int64_t>(t) * p.E + lane + 32 * c) : 0.0f;
+  int e;
+  float g;
+  topk_token<kMaxE / 32>(v, p.E, p.k, lane, &e, &g);
+  const int top = __reduce_max_sync(0xFFFFFFFFu, lane < p.k ? e : 0);
+  if (lane < p.k) {
+    sh.slot_e[t][lane] = static_cast<uint16_t>(e);
+    sh.gate[t][lane] = g;
+    atomicOr(&sh.mask[e], 1u << t);
+  }
+  if (lane == 0) sh.last_e[t] = top;
 }
 
 // Row of (token, slot) in h and y: rows by (expert, token)
@@ -456,8 +512,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int next = 0;
   if (warp == 0 && lane == 0) next = atomicAdd(p.ticket, 1);
   for (int t = warp; t < p.T; t += kThreads / 32) {
-    if (p.E <= 256) route_token<8>(p, sh, t, lane);
-    else route_token<32>(p, sh, t, lane);
+    if (p.E <= 64) route_token<2>(p, sh, t, lane);
+    else if (p.E <= 256) route_token<8>(p, sh, t, lane);
+    else route_token_any(p, sh, t, lane);
   }
   __syncthreads();
   // groups of up to 8 tokens per chosen expert, in expert order; 32 experts per warp at a time
@@ -748,25 +805,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t row_stride = first ? static_cast<int64_t>(ht) * Q * 128 : p.d;
 #pragma unroll
       for (int c = 0; c < kTok; ++c)
-        if (active(c)) __stcg(dst + row_at(c) * row_stride, sum(c));
-      __syncwarp();
+        if (active(c)) put_sum(dst + row_at(c) * row_stride, sum(c));
       if (first) {
-        int last = 0;
-        if (lane == 0) last = add_acq_rel(p.cnt1 + (un.group * ht + un.tile) * 4 + qd, 1) == Q - 1;
-        last = __shfl_sync(0xFFFFFFFFu, last, 0);
-        __syncwarp();  // the lanes' loads come after lane 0's acquire
-        if (!last) continue;
-        // all ranges of both are there: h of a 32-value block per token, in MXFP4 terms
+        if (un.q != Q - 1) continue;
+        // the last range of W3: the others' units are older, so running CTAs hold them.  h of a
+        // 32-value block per token, in MXFP4 terms
         const int row_bytes = p.dff / 2;
+        bool ok = true;
 #pragma unroll 1
-        for (int c = 0; c < p.cols; ++c) {
+        for (int c = 0; ok && c < p.cols; ++c) {
           if (!active(c)) continue;
           const float* src = dst + row_at(c) * row_stride - un.q * 128;
           float a = 0.0f, b = 0.0f;
-#pragma unroll 4
-          for (int q = 0; q < p.parts; ++q) {
-            a += __ldcg(src + (2 * q) * 128);
-            b += __ldcg(src + (2 * q + 1) * 128);
+#pragma unroll 1
+          for (int q = 0; ok && q < Q; q += 8) {
+            float v[8];
+            ok = get_sums([&](int i) { return src + (q + i) * 128; }, min(8, Q - q), v, abort_flag,
+                          p.err, 78, p.wait_ns);
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              a += v[i];
+              b += v[i + 1];
+            }
           }
           float h = a / (1.0f + expf(-a)) * b;
           uint8_t* hq = p.hq + (static_cast<int64_t>(un.group) * p.cols + c) * kTerms * row_bytes +
@@ -787,43 +847,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) hs[sf_at(c * kTerms + r, qd)] = static_cast<uint8_t>(s);
           }
         }
+        if (!ok) break;
         fence_proxy_async_global();
         __syncwarp();
         if (lane == 0) red_release_add(p.done1 + un.group, 1);
       } else {
-        // lane c: token c's arrival at these 32 columns; who brings the k-th row of a token
-        // combines it, in slot order
-        bool last = false;
-        if (lane < kTok && active(lane)) {
-          uint32_t left = gr.tokens;
-          if (!direct)
-            for (int j = 0; j < lane; ++j) left &= left - 1u;
-          const int t = direct ? lane : __ffs(left) - 1;
-          last = add_acq_rel(p.done2 + t * (p.d / 32) + 4 * un.tile + qd, 1) == p.k - 1;
-        }
-        uint32_t ready = __ballot_sync(0xFFFFFFFFu, last);
-        __syncwarp();
+        // the tokens whose last expert this is are combined here, in slot order; the units of
+        // their other experts are older
         const float* y = p.y + 128 * un.tile + 32 * qd + lane;
+        uint32_t left = gr.tokens;
+        bool ok = true;
 #pragma unroll 1
-        for (; ready; ready &= ready - 1u) {
-          uint32_t left = gr.tokens;
-          const int c = __ffs(ready) - 1;
-          if (!direct)
-            for (int j = 0; j < c; ++j) left &= left - 1u;
-          const int t = direct ? c : __ffs(left) - 1;
+        for (; ok && left; left &= left - 1u) {
+          const int t = __ffs(left) - 1;
+          if (sh.last_e[t] != gr.e) continue;
           float o = 0.0f;
 #pragma unroll 1
-          for (int jb = 0; jb < p.k; jb += 4) {
-            float v[4];
+          for (int jb = 0; ok && jb < p.k; jb += 8) {
+            float v[8];
+            ok = get_sums([&](int i) { return y + static_cast<int64_t>(row_of(sh, t, jb + i)) * p.d; },
+                          min(8, p.k - jb), v, abort_flag, p.err, 79, p.wait_ns);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (jb + j < p.k) v[j] = __ldcg(y + static_cast<int64_t>(row_of(sh, t, jb + j)) * p.d);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 8; ++j)
               if (jb + j < p.k) o = fmaf(sh.gate[t][jb + j], v[j], o);
           }
           p.out[static_cast<int64_t>(t) * p.d + 128 * un.tile + 32 * qd + lane] = bf16_bits(o);
         }
+        if (!ok) break;
       }
     }
   }
@@ -919,6 +969,8 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   r.err = reinterpret_cast<DevErr*>(w + L.err);
   r.clear = ints(L.ticket);
   r.n_clear = static_cast<int64_t>((L.clear_end - L.ticket) / 4);
+  r.places = reinterpret_cast<uint4*>(w + L.part);  // part and y lie side by side
+  r.n_places = static_cast<int64_t>((L.total - L.part) / 16);
   r.xq = bytes(L.xq);
   r.xs = bytes(L.xs);
 
@@ -951,9 +1003,7 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   p.y = reinterpret_cast<float*>(w + L.y);
   p.out = out;
   p.ticket = ints(L.ticket);
-  p.cnt1 = ints(L.cnt1);
   p.done1 = ints(L.done1);
-  p.done2 = ints(L.done2);
   p.xdone = ints(L.xdone);
   p.err = r.err;
   p.wait_ns = wait_limit_ns();
