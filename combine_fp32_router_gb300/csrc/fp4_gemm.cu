@@ -60,6 +60,7 @@ struct Params {
   const int32_t* counts;
   int64_t rows;
   int N, kt, E, nt;   // outputs, 128-value K tiles, experts, weight tiles per expert
+  int mt;             // weight rows of a CTA's tile: 128; 64 or 32 of the 128 (singles)
   int sf_tiles;       // 128-row scale tiles per expert
   int64_t ldo;
   int vec;  // output rows start on 16 bytes
@@ -125,7 +126,7 @@ __device__ __forceinline__ Tile decode(const Params& p, const Shared& sh, int64_
   t.row0 = sh.first_row[lo] + i * R;
   const int cnt = p.counts ? p.counts[lo] : static_cast<int>(p.rows);
   t.nvalid = min(cnt - i * R, R);
-  t.n0 = static_cast<int>(tile % p.nt) * (PAIR ? 256 : 128);
+  t.n0 = static_cast<int>(tile % p.nt) * (PAIR ? 256 : p.mt);
   const int half = PAIR ? (t.nvalid + 1) / 2 : t.nvalid;
   t.box = half <= 16 ? 0 : (half <= 32 ? 1 : (half <= 64 ? 2 : 3));
   t.local = t.box == 3 ? 96 : 16 << t.box;
@@ -226,9 +227,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     for (int64_t tile = unit; ok && tile < tiles; tile += units) {
       const Tile t = decode<PAIR>(p, sh, tile);
       const CUtensorMap* mb = &p.mapB[t.box];
-      const uint32_t bytes = C::kABytes + t.local * 128u + C::kSfaBytes + C::kSfbBytes;
+      const uint32_t bytes = (PAIR ? 128 : p.mt) * 128u + t.local * 128u + C::kSfaBytes + C::kSfbBytes;
       const int wrow = t.e * p.N + t.n0 + 128 * rank, brow = t.row0 + t.local * rank;
       const int wtile = t.e * p.sf_tiles + t.n0 / 128 + rank, btile = t.row0 / 128;
+      // fewer than 128 weight rows lie at their own place among their scale tile's 128 (what is
+      // around them meets outputs that are not stored)
+      const uint32_t aplace = (t.n0 % 128) * 128u;
       for (int ks = 0; ks < nks; ++ks) {
         if (issued >= S) ok = warp_wait(empty(s), phase, abort_flag, err, 61, p.wait_ns);
         if (!ok) break;
@@ -237,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         if (elect_one()) {
           sh.tx[s] = bytes;
           if (rank == 0) mbar_arrive_expect_tx(full(s), bytes * C::kCtas);
-          load(st, &p.mapA, bar, ks * 128, wrow);
+          load(st + aplace, &p.mapA, bar, ks * 128, wrow);
           load(st + C::kABytes, mb, bar, ks * 128, brow);
           load(ssf, &p.mapSa, bar, ks * 256, wtile);  // in words; zeros past the last K tile
           load(ssf + C::kSfaBytes, &p.mapSb, bar, ks * 256, btile);
@@ -328,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       if (!mbar_wait(tfull(acc), (n / 2) & 1, abort_flag, err, 66, p.wait_ns)) break;
       tc_fence_after();
       const uint32_t tacc = tmem + acc * C::kRows + (static_cast<uint32_t>(32 * q) << 16);
-      const int col0 = t.n0 + 128 * rank + 32 * q;  // this warp's 32 output columns
+      const int col0 = t.n0 / 128 * 128 + 128 * rank + 32 * q;  // this warp's 32 output columns
       for (int r0 = 0; r0 < t.nvalid; r0 += 32) {
         float a[16], b[16];
         tmem_ld16x2(tacc + r0, tacc + r0 + 16, a, b);
@@ -340,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
             else mbar_arrive(tempty(acc));
           }
         }
-        const int left = t.nvalid - r0;  // rows of this chunk (may exceed 32)
+        if (!PAIR && (32 * q < t.n0 % 128 || 32 * q >= t.n0 % 128 + p.mt)) continue;  // not of this tile
+        const int left = t.nvalid - r0;         // rows of this chunk (may exceed 32)
         if (F32 || !p.vec) {
           const int col = col0 + lane;
           if (col < p.N) {
@@ -504,8 +509,12 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* a_scales, const uint
   using C = Cfg<PAIR>;
   cudaError_t st = cudaSuccess;
   const uint64_t inner = static_cast<uint64_t>(mx_cols(K) / 2);
-  p.nt = (p.N + 128 * C::kCtas - 1) / (128 * C::kCtas);
-  p.mapA = code_map(b, inner, static_cast<uint64_t>(p.E) * p.N, 128, &st);
+  const int64_t blocks = (p.rows + C::kRows - 1) / C::kRows + (p.counts ? p.E : 0);
+  p.mt = 128;
+  if (!PAIR && !p.counts)
+    while (p.mt > 32 && 2 * blocks * ((p.N + p.mt - 1) / p.mt) <= sms) p.mt /= 2;
+  p.nt = (p.N + p.mt * C::kCtas - 1) / (p.mt * C::kCtas);
+  p.mapA = code_map(b, inner, static_cast<uint64_t>(p.E) * p.N, p.mt, &st);
   p.mapSa = scale_map(b_scales, p.kt, static_cast<uint64_t>(p.E) * p.sf_tiles, 1, &st);
   p.mapSb = scale_map(a_scales, p.kt, static_cast<uint64_t>((p.rows + 127) / 128), C::kSfTiles, &st);
   const int boxes[kBoxes] = {16, 32, 64, 96};
@@ -513,7 +522,6 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* a_scales, const uint
     if (i == 0 || p.rows > boxes[i - 1])
       p.mapB[i] = code_map(a, inner, static_cast<uint64_t>(p.rows), boxes[i], &st);
   if (st != cudaSuccess) return st;
-  const int64_t blocks = (p.rows + C::kRows - 1) / C::kRows + (p.counts ? p.E : 0);
   const int64_t tiles = blocks * p.nt;
   const int units = static_cast<int>(tiles < sms / C::kCtas ? tiles : sms / C::kCtas);
   return out_dtype == MOE_DTYPE_F32 ? launch<true, PAIR>(p, units, stream)
