@@ -496,11 +496,22 @@ CUtensorMap scale_map(const void* base, int kt, uint64_t tiles, uint32_t box_til
   return m;
 }
 
-// Pairs when their tiles give every pair of SMs work, or when there are more rows than singles
-// take in one block and the weights are shared by all: measured on GB300.
-bool use_pairs(int64_t rows, int N, int E, bool grouped, int sms) {
-  const int64_t blocks = (rows + Cfg<true>::kRows - 1) / Cfg<true>::kRows + (grouped ? E / 2 : 0);
-  return blocks * ((N + 255) / 256) >= sms / 2;
+// Pairs or singles, by the time of the rounds of tiles that each takes: a stage costs a single
+// some 390 cycles (its MMAs read 128 weight rows however few columns they have) and a pair
+// 130 + 2.1 per activation row, at least 410.  Measured on GB300, single and pair: 256 rows of
+// N 4096, K 7168 11.0 and 12.1 us; 384 rows of 4096 x 4096 12.2 and 9.2; 777 of 1545 x 2976 11.3
+// and 12.0; 512 of 7168 x 2048 10.7 and 9.4; over 64 experts of 1024 x 2048 300 rows 11.4 and
+// 12.4, 4000 rows 18.7 and 16.4.  With `counts` the experts are taken to have equal shares.
+bool use_pairs(int64_t rows, int N, int E, int sms) {
+  const int64_t share = (rows + E - 1) / E;
+  const auto time = [&](int height, int width, int units, int64_t stage) {
+    const int64_t tiles = E * ((share + height - 1) / height) * ((N + width - 1) / width);
+    return (tiles + units - 1) / units * stage;
+  };
+  const int64_t n = share < Cfg<true>::kRows ? share : Cfg<true>::kRows;
+  const int64_t stage = 130 + 21 * n / 10;
+  return time(Cfg<true>::kRows, 256, sms / 2, stage < 410 ? 410 : stage) <
+         time(Cfg<false>::kRows, 128, sms, 390);
 }
 
 template <bool PAIR>
@@ -563,7 +574,7 @@ moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t row
   p.wait_ns = wait_limit_ns();
   const int sms = num_sms_of_current_device();
   const cudaError_t st =
-      use_pairs(rows, N, E, counts != nullptr, sms)
+      use_pairs(rows, N, E, sms)
           ? run<true>(p, a, a_scales, b, b_scales, K, out_dtype, sms, stream)
           : run<false>(p, a, a_scales, b, b_scales, K, out_dtype, sms, stream);
   return st == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

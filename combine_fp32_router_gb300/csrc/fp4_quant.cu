@@ -82,6 +82,8 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
   float v[4][8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) load8<DT, VEC>(xr, c0 + i * 256 + lane * 8, cols, v[i]);
+  uint8_t* qo = q + row * static_cast<int64_t>(kp / 2) + (c0 + lane * 8) / 2;
+  uint8_t* so = scales + mx_scale_at(row, (c0 + lane * 8) / 32, kp / 128);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int c = c0 + i * 256 + lane * 8;
@@ -93,16 +95,15 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
     const uint32_t s = mx_scale_byte(amax);
     const float inv = mx_inverse_scale(s);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] = s == 255u ? 0.0f : v[i][j] * inv;
-    const uint32_t code = e2m1x8(v[i]);
+    for (int j = 0; j < 8; ++j) v[i][j] *= inv;
+    const uint32_t code = s == 255u ? 0u : e2m1x8(v[i]);
     // the four scale bytes of sixteen lanes in one word
     uint32_t sw = s << (8 * ((lane >> 2) & 3));
     sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 4);
     sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 8);
     if (c < kp) {
-      *reinterpret_cast<uint32_t*>(q + row * static_cast<int64_t>(kp / 2) + c / 2) = code;
-      if ((lane & 15) == 0)
-        *reinterpret_cast<uint32_t*>(scales + mx_scale_at(row, c / 32, kp / 128)) = sw;
+      *reinterpret_cast<uint32_t*>(qo + i * 128) = code;
+      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(so + i * 2 * kMxTileBytes) = sw;
     }
   }
   // the rows that the last scale tile has and the matrix has not: scale bytes of zero, from
@@ -135,15 +136,16 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
   const uint8_t* qr = q + row_all * static_cast<int64_t>(kp / 2);
   const uint8_t* sg = scales + g * mx_scale_bytes(rows, cols);
   T* o = out + row_all * static_cast<int64_t>(cols);
+  const uint8_t* qi = qr + (c0 + lane * 8) / 2;
+  const uint8_t* si = sg + mx_scale_at(row, (c0 + lane * 8) / 32, kp / 128);
   uint32_t code[4], s[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int c = c0 + i * 256 + lane * 8;
     code[i] = 0;
     s[i] = 0;
-    if (c < cols) {
-      code[i] = __ldg(reinterpret_cast<const uint32_t*>(qr + c / 2));
-      s[i] = __ldg(sg + mx_scale_at(row, c / 32, kp / 128));
+    if (c0 + i * 256 + lane * 8 < cols) {
+      code[i] = __ldg(reinterpret_cast<const uint32_t*>(qi + i * 128));
+      s[i] = __ldg(si + i * 2 * kMxTileBytes);
     }
   }
 #pragma unroll
@@ -163,7 +165,9 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
     if (VEC && c + 8 <= cols) {
 #pragma unroll
       for (int j = 0; j < static_cast<int>(sizeof(t) / 16); ++j)
-        st_v4(reinterpret_cast<char*>(o + c) + 16 * j, reinterpret_cast<const uint4*>(t)[j]);
+        // written once and larger than the codes: not kept in L2 in their place
+        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<char*>(o + c) + 16 * j),
+               reinterpret_cast<const uint4*>(t)[j]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
