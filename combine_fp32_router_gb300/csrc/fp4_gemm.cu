@@ -559,7 +559,7 @@ moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t row
       (reinterpret_cast<uintptr_t>(counts) & 3) != 0)
     return MOE_ERR_INVALID_ARG;
   if (E > kMaxE || N > kMaxFp4Cols || K > kMaxFp4Cols || rows > INT32_MAX - 256 ||
-      static_cast<int64_t>(E) * N > INT32_MAX)
+      static_cast<int64_t>(E) * N > INT32_MAX - 256)  // rows of a tile past the last expert count too
     return MOE_ERR_UNSUPPORTED;
   Params p = {};
   p.counts = counts;

@@ -343,7 +343,7 @@ moe_status_t moe_quantize_weights_fp4(const moe_bf16_t* W, int E, int K, int N, 
  *   counts      : NULL (E = 1: every row), or a DEVICE array [E]: expert e's counts[e] rows
  *                 start at row sum_{j<e} round_up(counts[j], 128) (the layout of
  *                 moe_expert_forward); rows between the segments are left as they were.
- * Any rows, N, K >= 1 (rows = 0 writes nothing); E <= 1024, E * N < 2^31, K <= 2^20.  Counts
+ * Any rows, N, K >= 1 (rows = 0 writes nothing); E <= 1024, E * N < 2^31 - 256, N and K <= 2^20.  Counts
  * that are negative or do not fit `rows` record MOE_ERR_DEVICE_BOUNDS and nothing is written;
  * device-side problems are read with moe_gemm_fp4_get_error, which synchronises `stream`,
  * returns the first one recorded on the current device since the last call, and clears it.
@@ -358,10 +358,10 @@ moe_status_t moe_gemm_fp4_get_error(cudaStream_t stream);
  * chosen expert's weights once:
  *   logits = x router^T (fp32 products and sums), or given; top-k and gate as moe_forward;
  *   out_t = bf16( sum_j gate[t,j] * (h_tj W2[e_j]) ),  h_tj = silu(x_t W1[e_j]) * (x_t W3[e_j])
- * The weights enter as the values that their codes stand for; x and h are not quantised: they
- * enter the products as fp16 with a power of two per token (x) or per 16 values (h), i.e. with
- * 11 significant bits wherever they are above 2^-28 of that group's largest; every sum is fp32,
- * and the expert outputs are combined in fp32 in slot order and rounded once.
+ * The weights enter as the values that their codes stand for.  x and h enter as sums of six
+ * MXFP4 numbers each, which leaves at most 2^-13.9 (usually 2^-19) of the largest value of a block
+ * of 32; every sum is fp32, and the expert outputs are combined in fp32 in slot order and rounded
+ * once.  A value of x that is not finite, or an h, makes its token's output NaN.
  *   x [T,d] bf16; router [E,d] fp32, or NULL; logits [T,E] fp32: written when router is given,
  *   read when it is NULL; W1q, W3q: E matrices of d_ff x d, W2q: of d x d_ff, with their scales
  *   (moe_quantize_weights_fp4 of the bf16 weights of moe_forward); out [T,d] bf16.

@@ -59,7 +59,7 @@ def within(got, want, u):
 
 def few(x, logits, W1, W3, W2, k):
     """The layer in float64 on weight values W1, W3 [E, dff, d], W2 [E, d, dff]: the output, and
-    a bound on the fp32 and fp16 rounding errors before its last rounding."""
+    a bound on the rounding errors before its last rounding."""
     T, d = x.shape
     x = x.double()
     out = torch.zeros(T, d, dtype=torch.float64, device=x.device)
@@ -79,11 +79,12 @@ def few(x, logits, W1, W3, W2, k):
             sg = torch.sigmoid(a)
             h = a * sg * b
             # fp32 sums of d terms (relative to the sum of magnitudes, and every partial sum),
-            # silu' is at most 1.1, fp16 keeps 11 bits of each h
+            # silu' is at most 1.1; h with 11 significant bits (the six 4-bit terms that carry it
+            # keep more than that of all but the smallest values of a block)
             ua = (d + 16) * eps * (W1[e].abs() @ x[t].abs())
             ub = (d + 16) * eps * (W3[e].abs() @ x[t].abs())
             uh = 1.1 * ua * b.abs() + (a * sg).abs() * ub + 16 * eps * h.abs() + 2.0 ** -11 * h.abs()
-            # below 2^-28 of its group's largest a value has fp16's subnormal spacing
+            # and an absolute floor under the largest
             uh = uh + 2.0 ** -38 * h.abs().amax()
             n = h.numel()
             m = W2[e].abs() @ h.abs()
