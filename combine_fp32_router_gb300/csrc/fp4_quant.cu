@@ -39,108 +39,263 @@ struct In<MOE_DTYPE_F32> {
   static __device__ __forceinline__ T of(float v) { return v; }
 };
 
-// Eight values from column c on of a row of `cols` (zeros past its end).  VEC: the row's first
-// value and the row stride are multiples of 16 bytes, and so is c's byte offset (c is a
-// multiple of 8).
-template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const typename In<DT>::T* row, int c, int cols,
-                                      float (&v)[8]) {
-  using T = typename In<DT>::T;
-  if (VEC && c + 8 <= cols) {
-    constexpr int NV = sizeof(T) * 8 / 16;
-    uint4 u[NV];
+constexpr int kQuantWarps = 8;
+
+// ---- rows that start on 16 bytes.  The matrix is cut into tiles of 128 values of a row, rows x kt
+// of them in row-major order, and each warp takes eight that follow one another: half a warp every
+// second one, lane l of it the values 8 l .. 8 l + 7.  Four lanes then hold a block and sixteen
+// the four blocks of a scale word, whatever the width: no lane idles on narrow rows (25894 rows of
+// 328 bf16 values: 7.2 us to quantise, 10.1 us with whole rows per warp).
+constexpr int kHalfTiles = 4;  // tiles per half warp, all loaded before the first is used
+
+// A half warp's walk over its tiles: row and tile, the tile's first value in a matrix with rows
+// `stride` apart, and its place among the scales.  A step inside a row is three additions.
+template <typename T>
+struct Walk {
+  uint32_t row;
+  int t;
+  T* value;
+  int64_t scale;
+  __device__ __forceinline__ Walk(uint32_t tile, int kt, T* base, int64_t stride)
+      : row(tile / static_cast<uint32_t>(kt)), t(static_cast<int>(tile % static_cast<uint32_t>(kt))) {
+    value = base + row * stride + t * 128;
+    scale = mx_scale_at(row, 4 * t, kt);
+  }
+  __device__ __forceinline__ void step(int kt, T* base, int64_t stride) {
+    t += 2;
+    value += 256;
+    scale += 2 * kMxTileBytes;
+    if (t >= kt) {
+      for (; t >= kt; t -= kt) ++row;
+      value = base + row * stride + t * 128;
+      scale = mx_scale_at(row, 4 * t, kt);
+    }
+  }
+};
+
+// Values 8 l .. 8 l + 7 of a tile that has n of its 128 (zeros past them), raw: converting waits
+// for the loads, so it is left for later.
+template <typename T>
+struct alignas(16) Raw8 {
+  T v[8];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* tile, int n, int l) {
+  Raw8<T> r;
+  const int c = 8 * l;
+  if (c + 8 <= n) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) u[i] = ld_nc_v4(reinterpret_cast<const char*>(row + c) + 16 * i);
-    const T* t = reinterpret_cast<const T*>(u);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = In<DT>::f32(t[i]);
+    for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i)
+      reinterpret_cast<uint4*>(&r)[i] = ld_nc_v4(reinterpret_cast<const char*>(tile + c) + 16 * i);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? In<DT>::f32(__ldg(row + c + i)) : 0.0f;
+    for (int i = 0; i < 8; ++i) r.v[i] = c + i < n ? __ldg(tile + c + i) : T(0);
+  }
+  return r;
+}
+
+// Codes and scale byte of a lane's eight values (four lanes hold a block); `sw`: the scale bytes
+// of the sixteen lanes' four blocks.
+__device__ __forceinline__ uint32_t quantize8(float (&v)[8], int l, uint32_t* sw) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+  const uint32_t s = mx_scale_byte(amax);
+  const float inv = mx_inverse_scale(s);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= inv;
+  *sw = s << (8 * ((l >> 2) & 3));
+  *sw |= __shfl_xor_sync(0xFFFFFFFFu, *sw, 4);
+  *sw |= __shfl_xor_sync(0xFFFFFFFFu, *sw, 8);
+  return s == 255u ? 0u : e2m1x8(v);
+}
+// The rows that the last scale tile has and the matrix has not: scale bytes of zero, by the
+// sixteen lanes of the last row's tile.
+__device__ __forceinline__ void pad_tile(uint8_t* scales, int64_t place, uint32_t row, int l) {
+  uint8_t* tile0 = scales + place / kMxTileBytes * kMxTileBytes;
+  for (int r = static_cast<int>(row % 128) + 1 + l; r < 128; r += 16)
+    *reinterpret_cast<uint32_t*>(tile0 + mx_scale_at(r, 0, 1)) = 0u;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(32 * kQuantWarps)
+    quantize_rows_kernel(const typename In<DT>::T* __restrict__ x, int64_t rows, int cols,
+                         int64_t stride, uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
+  using T = typename In<DT>::T;
+  griddep_wait();
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const int kt = static_cast<int>(mx_cols(cols) / 128);
+  const uint32_t w = blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
+  const uint32_t tile = w * 2 * kHalfTiles + (lane >> 4);
+  Walk<const T> at(tile, kt, x, stride);
+  Raw8<T> raw[kHalfTiles];
+  uint32_t row[kHalfTiles];
+  int64_t so[kHalfTiles];
+#pragma unroll
+  for (int i = 0; i < kHalfTiles; ++i) {
+    row[i] = at.row;
+    so[i] = at.scale;
+    // lanes past the last row stay in step and load nothing
+    raw[i] = load8(at.value, at.row < rows ? cols - at.t * 128 : 0, l);
+    at.step(kt, x, stride);
+  }
+  uint8_t* qo = q + static_cast<int64_t>(tile) * 64 + 4 * l;
+#pragma unroll
+  for (int i = 0; i < kHalfTiles; ++i) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = In<DT>::f32(raw[i].v[j]);
+    uint32_t sw;
+    const uint32_t code = quantize8(v, l, &sw);
+    if (row[i] < rows) {
+      *reinterpret_cast<uint32_t*>(qo + i * 128) = code;
+      if (l == 0) *reinterpret_cast<uint32_t*>(scales + so[i]) = sw;
+      if (row[i] == rows - 1) pad_tile(scales, so[i], row[i], l);
+    }
   }
 }
 
-constexpr int kQuantWarps = 8;
-constexpr int kQuantSeg = 1024;  // values of a row per warp: 4 x 32 lanes x 8
+// The inverse: value = code * 2^(s - 127), rounded once to the output type (exact in bf16 and
+// fp32 wherever the type reaches).
+template <int DT>
+__device__ __forceinline__ Raw8<typename In<DT>::T> dequantize8(uint32_t code, uint32_t s) {
+  uint32_t h[4];
+  e2m1x8_to_half(code, h);
+  const float f = mx_scale(s);
+  Raw8<typename In<DT>::T> t;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+    t.v[2 * j] = In<DT>::of(p.x * f);
+    t.v[2 * j + 1] = In<DT>::of(p.y * f);
+  }
+  return t;
+}
 
-// A warp quantises 1024 consecutive values of one row: lane l takes values 8 l .. 8 l + 7 of
-// each 256, so four lanes hold a block and sixteen the four blocks of a scale tile's word.
-// All four loads of a lane are in flight before the first is used.
-template <int DT, bool VEC>
+template <int DT>
 __global__ void __launch_bounds__(32 * kQuantWarps)
-    quantize_rows_kernel(const typename In<DT>::T* __restrict__ x, int64_t rows, int cols,
-                         int64_t stride, uint32_t segs, uint8_t* __restrict__ q,
-                         uint8_t* __restrict__ scales) {
+    dequantize_rows_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales,
+                           int64_t rows, int64_t rows_all, int cols,
+                           typename In<DT>::T* __restrict__ out) {
+  using T = typename In<DT>::T;
+  griddep_wait();
+  const int lane = threadIdx.x & 31, l = lane & 15;
+  const int kt = static_cast<int>(mx_cols(cols) / 128);
+  const uint32_t w = blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
+  const int64_t per = mx_scale_bytes(rows, cols);
+  const uint32_t tile = w * 2 * kHalfTiles + (lane >> 4);
+  Walk<T> at(tile, kt, out, cols);
+  uint32_t code[kHalfTiles], s[kHalfTiles];
+  T* to[kHalfTiles];
+  int n[kHalfTiles];
+  const uint8_t* qi = q + static_cast<int64_t>(tile) * 64 + 4 * l;
+#pragma unroll
+  for (int i = 0; i < kHalfTiles; ++i) {
+    code[i] = 0;
+    s[i] = 0;
+    to[i] = at.value;
+    n[i] = at.row < rows_all ? cols - at.t * 128 : 0;
+    if (8 * l < n[i]) {
+      code[i] = __ldg(reinterpret_cast<const uint32_t*>(qi + i * 128));
+      int64_t so = at.scale;
+      if (rows != rows_all) {  // a group's scales start at a tile of their own
+        const uint32_t g = at.row / static_cast<uint32_t>(rows);
+        so = g * per + mx_scale_at(at.row - g * rows, 4 * at.t, kt);
+      }
+      s[i] = __ldg(scales + so + (l >> 2));
+    }
+    at.step(kt, out, cols);
+  }
+#pragma unroll
+  for (int i = 0; i < kHalfTiles; ++i) {
+    const Raw8<T> t = dequantize8<DT>(code[i], s[i]);
+    T* o = to[i] + 8 * l;
+    if (8 * l + 8 <= n[i]) {
+#pragma unroll
+      for (int j = 0; j < static_cast<int>(sizeof(t) / 16); ++j)
+        // written once and larger than the codes: not kept in L2 in their place
+        __stcs(reinterpret_cast<uint4*>(o) + j, reinterpret_cast<const uint4*>(&t)[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (8 * l + j < n[i]) o[j] = t.v[j];
+    }
+  }
+}
+
+// ---- other rows.  A warp takes U x 256 values of one row; its lanes read or store neighbouring
+// values, 32 at a time, and pass them on through shared memory (5000 rows of 3001 bf16 values:
+// 12 and 8 us; with eight strided accesses per lane 12 and 43; as whole vectors between their
+// 16-byte boundaries 16 and 12).
+template <int DT, int U>
+__global__ void __launch_bounds__(32 * kQuantWarps)
+    quantize_rows_any_kernel(const typename In<DT>::T* __restrict__ x, int64_t rows, int cols,
+                             int64_t stride, uint32_t segs, uint8_t* __restrict__ q,
+                             uint8_t* __restrict__ scales) {
+  __shared__ float4 shared[kQuantWarps * 64];
   griddep_wait();
   const uint32_t w = blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const uint32_t row = w / segs;
   if (row >= rows) return;
-  const int c0 = static_cast<int>(w % segs) * kQuantSeg;
+  const int c0 = static_cast<int>(w % segs) * (U * 256);
   const int kp = static_cast<int>(mx_cols(cols));
   const typename In<DT>::T* xr = x + row * stride;
-  float v[4][8];
+  float* buf = reinterpret_cast<float*>(shared + (threadIdx.x >> 5) * 64);
+  float v[U][8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) load8<DT, VEC>(xr, c0 + i * 256 + lane * 8, cols, v[i]);
-  uint8_t* qo = q + row * static_cast<int64_t>(kp / 2) + (c0 + lane * 8) / 2;
-  uint8_t* so = scales + mx_scale_at(row, (c0 + lane * 8) / 32, kp / 128);
+  for (int i = 0; i < U; ++i)
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = c0 + i * 256 + lane * 8;
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-    const uint32_t s = mx_scale_byte(amax);
-    const float inv = mx_inverse_scale(s);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[i][j] *= inv;
-    const uint32_t code = s == 255u ? 0u : e2m1x8(v[i]);
-    // the four scale bytes of sixteen lanes in one word
-    uint32_t sw = s << (8 * ((lane >> 2) & 3));
-    sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 4);
-    sw |= __shfl_xor_sync(0xFFFFFFFFu, sw, 8);
-    if (c < kp) {
-      *reinterpret_cast<uint32_t*>(qo + i * 128) = code;
-      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(so + i * 2 * kMxTileBytes) = sw;
+    for (int j = 0; j < 8; ++j) {
+      const int k = c0 + i * 256 + 32 * j + lane;
+      v[i][j] = k < cols ? In<DT>::f32(__ldg(xr + k)) : 0.0f;
     }
-  }
-  // the rows that the last scale tile has and the matrix has not: scale bytes of zero, from
-  // the last row's warps (1024 values are 8 words of each)
-  if (row == rows - 1) {
-    const int missing = static_cast<int>(127 - row % 128), kt = kp / 128, t0 = c0 / 128;
-    for (int i = lane; i < missing * 8; i += 32)
-      if (t0 + i % 8 < kt)
-        *reinterpret_cast<uint32_t*>(scales + mx_scale_at(row + 1 + i / 8, 4 * (t0 + i % 8), kt)) =
-            0u;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) buf[32 * j + lane] = v[i][j];
+    __syncwarp();
+    const float4 a = *reinterpret_cast<const float4*>(buf + 8 * lane);
+    const float4 b = *reinterpret_cast<const float4*>(buf + 8 * lane + 4);
+    float t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t sw;
+    const uint32_t code = quantize8(t, lane, &sw);
+    const int c = c0 + i * 256 + lane * 8;
+    if (c < kp) {
+      *reinterpret_cast<uint32_t*>(q + row * static_cast<int64_t>(kp / 2) + c / 2) = code;
+      const int64_t so = mx_scale_at(row, c / 128 * 4, kp / 128);
+      if ((lane & 15) == 0) *reinterpret_cast<uint32_t*>(scales + so) = sw;
+      if (row == rows - 1) pad_tile(scales, so, row, lane & 15);
+    }
   }
 }
 
-// The inverse: value = code * 2^(s - 127), rounded once to the output type (exact in bf16 and
-// fp32 wherever the type reaches).  Eight values per lane as above.
-template <int DT, bool VEC>
+template <int DT, int U>
 __global__ void __launch_bounds__(32 * kQuantWarps)
-    dequantize_rows_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales,
-                           int64_t rows, int64_t rows_all, int cols, uint32_t segs,
-                           typename In<DT>::T* __restrict__ out) {
+    dequantize_rows_any_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scales,
+                               int64_t rows, int64_t rows_all, int cols, uint32_t segs,
+                               typename In<DT>::T* __restrict__ out) {
   using T = typename In<DT>::T;
+  __shared__ Raw8<T> shared[kQuantWarps * 32];
   griddep_wait();
   const uint32_t w = blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const uint32_t row_all = w / segs;
   if (row_all >= rows_all) return;
   const int64_t g = row_all / rows, row = row_all % rows;
-  const int c0 = static_cast<int>(w % segs) * kQuantSeg;
+  const int c0 = static_cast<int>(w % segs) * (U * 256);
   const int kp = static_cast<int>(mx_cols(cols));
-  const uint8_t* qr = q + row_all * static_cast<int64_t>(kp / 2);
-  const uint8_t* sg = scales + g * mx_scale_bytes(rows, cols);
+  const uint8_t* qi = q + row_all * static_cast<int64_t>(kp / 2) + (c0 + lane * 8) / 2;
+  const uint8_t* si = scales + g * mx_scale_bytes(rows, cols) +
+                      mx_scale_at(row, (c0 + lane * 8) / 32, kp / 128);
   T* o = out + row_all * static_cast<int64_t>(cols);
-  const uint8_t* qi = qr + (c0 + lane * 8) / 2;
-  const uint8_t* si = sg + mx_scale_at(row, (c0 + lane * 8) / 32, kp / 128);
-  uint32_t code[4], s[4];
+  Raw8<T>* mine = shared + (threadIdx.x >> 5) * 32;
+  uint32_t code[U], s[U];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < U; ++i) {
     code[i] = 0;
     s[i] = 0;
     if (c0 + i * 256 + lane * 8 < cols) {
@@ -149,29 +304,14 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int c = c0 + i * 256 + lane * 8;
-    if (c >= cols) continue;
-    uint32_t h[4];
-    e2m1x8_to_half(code[i], h);
-    const float f = mx_scale(s[i]);
-    alignas(16) T t[8];
+  for (int i = 0; i < U; ++i) {
+    __syncwarp();
+    mine[lane] = dequantize8<DT>(code[i], s[i]);
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-      t[2 * j] = In<DT>::of(p.x * f);
-      t[2 * j + 1] = In<DT>::of(p.y * f);
-    }
-    if (VEC && c + 8 <= cols) {
-#pragma unroll
-      for (int j = 0; j < static_cast<int>(sizeof(t) / 16); ++j)
-        // written once and larger than the codes: not kept in L2 in their place
-        __stcs(reinterpret_cast<uint4*>(reinterpret_cast<char*>(o + c) + 16 * j),
-               reinterpret_cast<const uint4*>(t)[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c + j < cols) o[c + j] = t[j];
+    for (int j = 0; j < 8; ++j) {
+      const int k = c0 + i * 256 + 32 * j + lane;
+      if (k < cols) o[k] = reinterpret_cast<const T*>(mine)[32 * j + lane];
     }
   }
 }
@@ -264,35 +404,54 @@ __global__ void __launch_bounds__(256)
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Warps of a launch over `rows` rows of `cols` values; 0 when they pass what a grid's 32-bit
-// warp index holds.
-uint32_t quant_segs(int64_t rows, int cols, uint32_t* blocks) {
-  const int64_t segs = (mx_cols(cols) + kQuantSeg - 1) / kQuantSeg;
-  const int64_t warps = rows * segs;
-  if (rows > INT32_MAX || warps > INT32_MAX) return 0;
-  *blocks = static_cast<uint32_t>((warps + kQuantWarps - 1) / kQuantWarps);
-  return static_cast<uint32_t>(segs);
+// Blocks of a launch over `rows` rows that start on 16 bytes (u = 0), or warps of u x 256 values
+// of a row, `segs` per row, for other rows: the most of 4, 2 and 1 that leaves at most an eighth
+// of the lanes without work.  False when a 32-bit index does not hold them.
+struct Cut {
+  int u;
+  uint32_t segs, blocks;
+};
+bool cut_rows(int64_t rows, int cols, bool vec, Cut* c) {
+  const int64_t kp = mx_cols(cols);
+  if (rows > (INT32_MAX - 64) / (kp / 128)) return false;
+  *c = Cut{0, 0, 0};
+  int64_t warps = (rows * (kp / 128) + 2 * kHalfTiles - 1) / (2 * kHalfTiles);
+  if (!vec) {
+    c->u = 4;
+    while (c->u > 1 && (kp + 256 * c->u - 1) / (256 * c->u) * (256 * c->u) * 7 > kp * 8) c->u /= 2;
+    c->segs = static_cast<uint32_t>((kp + 256 * c->u - 1) / (256 * c->u));
+    warps = rows * c->segs;
+  }
+  c->blocks = static_cast<uint32_t>((warps + kQuantWarps - 1) / kQuantWarps);
+  return true;
 }
 
 template <int DT>
-cudaError_t launch_quantize(const void* x, int64_t rows, int cols, int64_t stride, uint32_t segs,
-                            uint32_t blocks, uint8_t* q, uint8_t* scales, cudaStream_t s) {
-  using T = typename In<DT>::T;
-  const bool vec = aligned16(x) && stride * sizeof(T) % 16 == 0;
-  return launch_pdl(vec ? quantize_rows_kernel<DT, true> : quantize_rows_kernel<DT, false>,
-                    dim3(blocks), dim3(32 * kQuantWarps), 0, s, static_cast<const T*>(x), rows,
-                    cols, stride, segs, q, scales);
+cudaError_t launch_quantize(const void* x, int64_t rows, int cols, int64_t stride, const Cut& c,
+                            uint8_t* q, uint8_t* scales, cudaStream_t s) {
+  const auto* xt = static_cast<const typename In<DT>::T*>(x);
+  const dim3 grid(c.blocks), block(32 * kQuantWarps);
+  if (c.u == 0)
+    return launch_pdl(quantize_rows_kernel<DT>, grid, block, 0, s, xt, rows, cols, stride, q, scales);
+  const auto kern = c.u == 4   ? quantize_rows_any_kernel<DT, 4>
+                    : c.u == 2 ? quantize_rows_any_kernel<DT, 2>
+                               : quantize_rows_any_kernel<DT, 1>;
+  return launch_pdl(kern, grid, block, 0, s, xt, rows, cols, stride, c.segs, q, scales);
 }
 template <int DT>
 cudaError_t launch_dequantize(const uint8_t* q, const uint8_t* scales, int64_t rows,
-                              int64_t rows_all, int cols, uint32_t segs, uint32_t blocks,
-                              void* out, cudaStream_t s) {
-  using T = typename In<DT>::T;
-  const bool vec = cols * sizeof(T) % 16 == 0;  // `out` itself is 16-byte aligned
-  return launch_pdl(vec ? dequantize_rows_kernel<DT, true> : dequantize_rows_kernel<DT, false>,
-                    dim3(blocks), dim3(32 * kQuantWarps), 0, s, q, scales, rows, rows_all, cols,
-                    segs, static_cast<T*>(out));
+                              int64_t rows_all, int cols, const Cut& c, void* out, cudaStream_t s) {
+  auto* ot = static_cast<typename In<DT>::T*>(out);
+  const dim3 grid(c.blocks), block(32 * kQuantWarps);
+  if (c.u == 0)
+    return launch_pdl(dequantize_rows_kernel<DT>, grid, block, 0, s, q, scales, rows, rows_all, cols, ot);
+  const auto kern = c.u == 4   ? dequantize_rows_any_kernel<DT, 4>
+                    : c.u == 2 ? dequantize_rows_any_kernel<DT, 2>
+                               : dequantize_rows_any_kernel<DT, 1>;
+  return launch_pdl(kern, grid, block, 0, s, q, scales, rows, rows_all, cols, c.segs, ot);
 }
+
+int64_t dtype_bytes(int dt) { return dt == MOE_DTYPE_F32 ? 4 : 2; }
 
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
@@ -321,19 +480,14 @@ moe_status_t moe_quantize_rows_fp4(const void* x, int dtype, int64_t rows, int c
   if (rows == 0) return MOE_OK;
   if (!x || !q || !scales || !aligned16(q) || !aligned16(scales)) return MOE_ERR_INVALID_ARG;
   if (rows > 1 && row_stride < cols) return MOE_ERR_INVALID_ARG;
-  const uintptr_t unit = dtype == MOE_DTYPE_F32 ? 4 : 2;
-  if (reinterpret_cast<uintptr_t>(x) % unit != 0) return MOE_ERR_INVALID_ARG;
-  uint32_t blocks = 0;
-  if (cols > kMaxFp4Cols) return MOE_ERR_UNSUPPORTED;
-  const uint32_t segs = quant_segs(rows, cols, &blocks);
-  if (segs == 0) return MOE_ERR_UNSUPPORTED;
-  const cudaError_t e =
-      dtype == MOE_DTYPE_BF16
-          ? launch_quantize<MOE_DTYPE_BF16>(x, rows, cols, row_stride, segs, blocks, q, scales, stream)
-      : dtype == MOE_DTYPE_F16
-          ? launch_quantize<MOE_DTYPE_F16>(x, rows, cols, row_stride, segs, blocks, q, scales, stream)
-          : launch_quantize<MOE_DTYPE_F32>(x, rows, cols, row_stride, segs, blocks, q, scales, stream);
-  return cuda_status(e);
+  if (reinterpret_cast<uintptr_t>(x) % dtype_bytes(dtype) != 0) return MOE_ERR_INVALID_ARG;
+  Cut cut;
+  const bool vec = aligned16(x) && row_stride * dtype_bytes(dtype) % 16 == 0;
+  if (cols > kMaxFp4Cols || !cut_rows(rows, cols, vec, &cut)) return MOE_ERR_UNSUPPORTED;
+  const auto run = dtype == MOE_DTYPE_BF16  ? launch_quantize<MOE_DTYPE_BF16>
+                   : dtype == MOE_DTYPE_F16 ? launch_quantize<MOE_DTYPE_F16>
+                                            : launch_quantize<MOE_DTYPE_F32>;
+  return cuda_status(run(x, rows, cols, row_stride, cut, q, scales, stream));
 }
 
 moe_status_t moe_dequantize_rows_fp4(const uint8_t* q, const uint8_t* scales, int groups,
@@ -343,17 +497,14 @@ moe_status_t moe_dequantize_rows_fp4(const uint8_t* q, const uint8_t* scales, in
   if (groups == 0 || rows == 0) return MOE_OK;
   if (!q || !scales || !out || !aligned16(q) || !aligned16(scales) || !aligned16(out))
     return MOE_ERR_INVALID_ARG;
-  if (cols > kMaxFp4Cols || rows > INT32_MAX / groups) return MOE_ERR_UNSUPPORTED;
-  uint32_t blocks = 0;
-  const uint32_t segs = quant_segs(rows * groups, cols, &blocks);
-  if (segs == 0) return MOE_ERR_UNSUPPORTED;
-  const int64_t all = rows * groups;
-  return cuda_status(
-      dtype == MOE_DTYPE_BF16
-          ? launch_dequantize<MOE_DTYPE_BF16>(q, scales, rows, all, cols, segs, blocks, out, stream)
-      : dtype == MOE_DTYPE_F16
-          ? launch_dequantize<MOE_DTYPE_F16>(q, scales, rows, all, cols, segs, blocks, out, stream)
-          : launch_dequantize<MOE_DTYPE_F32>(q, scales, rows, all, cols, segs, blocks, out, stream));
+  Cut cut;
+  const bool vec = cols * dtype_bytes(dtype) % 16 == 0;  // `out` itself is aligned
+  if (cols > kMaxFp4Cols || rows > INT32_MAX / groups || !cut_rows(rows * groups, cols, vec, &cut))
+    return MOE_ERR_UNSUPPORTED;
+  const auto run = dtype == MOE_DTYPE_BF16  ? launch_dequantize<MOE_DTYPE_BF16>
+                   : dtype == MOE_DTYPE_F16 ? launch_dequantize<MOE_DTYPE_F16>
+                                            : launch_dequantize<MOE_DTYPE_F32>;
+  return cuda_status(run(q, scales, rows, rows * groups, cols, cut, out, stream));
 }
 
 moe_status_t moe_quantize_weights_fp4(const moe_bf16_t* W, int E, int K, int N, uint8_t* Wq,

@@ -316,8 +316,8 @@ int64_t moe_fp4_row_bytes(int cols);
 size_t moe_fp4_scale_bytes(int64_t rows, int cols);
 
 /* x [rows, cols] (device, MOE_DTYPE_*, row r at x + r * row_stride elements, aligned to its
- * element) -> q, scales.  Reads each value once.  cols <= 2^20 and rows * ceil(cols / 1024)
- * < 2^31, else MOE_ERR_UNSUPPORTED.  rows = 0 writes nothing.  Asynchronous on `stream`, as
+ * element) -> q, scales.  Reads each value once.  cols <= 2^20 and rows * ceil(cols / 128)
+ * < 2^31 - 64, else MOE_ERR_UNSUPPORTED.  rows = 0 writes nothing.  Asynchronous on `stream`, as
  * every entry point here. */
 moe_status_t moe_quantize_rows_fp4(const void* x, int dtype, int64_t rows, int cols,
                                    int64_t row_stride, uint8_t* q, uint8_t* scales,
