@@ -38,7 +38,7 @@ struct Cfg {
   static constexpr int kRows = PAIR ? 192 : 64;  // N of a tile
   static constexpr int kLocal = PAIR ? kRows / 2 : kRows;  // rows a CTA loads
   static constexpr int kCtas = PAIR ? 2 : 1;
-  static constexpr int kStages = PAIR ? 5 : 8;
+  static constexpr int kStages = PAIR ? 5 : 7;
   static constexpr int kSfTiles = PAIR ? 2 : 1;  // 128-row scale tiles a block can touch
   static constexpr uint32_t kABytes = 128 * 128;
   static constexpr uint32_t kBBytes = kLocal * 128;
@@ -77,7 +77,7 @@ struct Shared {
   int32_t abort_flag;
   uint32_t consumed, peer_issued;          // fills used by MMAs, fills issued by the peer
   uint32_t tx[kMaxStages], peer_tx[kMaxStages];  // bytes of the fill in a stage
-  int32_t first_block[kMaxE + 1], first_row[kMaxE + 1];
+  int32_t first_block[kMaxE + 1], first_row[kMaxE + 1], count[kMaxE];
   alignas(16) uint32_t transpose[4 * 16 * kTrRow];
 };
 template <bool PAIR>
@@ -111,9 +111,10 @@ struct Tile {
 
 // first_block[e], first_row[e]: blocks and rows before expert e (E + 1 entries each)
 template <bool PAIR>
-__device__ __forceinline__ Tile decode(const Params& p, const Shared& sh, int64_t tile) {
+__device__ __forceinline__ Tile decode(const Params& p, const Shared& sh, uint32_t tile) {
   constexpr int R = Cfg<PAIR>::kRows;
-  const int b = static_cast<int>(tile / p.nt);
+  const uint32_t nt = static_cast<uint32_t>(p.nt);
+  const int b = static_cast<int>(tile / nt);
   int lo = 0, hi = p.E;  // the last expert with first_block[e] <= b
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -124,9 +125,8 @@ __device__ __forceinline__ Tile decode(const Params& p, const Shared& sh, int64_
   t.e = lo;
   const int i = b - sh.first_block[lo];
   t.row0 = sh.first_row[lo] + i * R;
-  const int cnt = p.counts ? p.counts[lo] : static_cast<int>(p.rows);
-  t.nvalid = min(cnt - i * R, R);
-  t.n0 = static_cast<int>(tile % p.nt) * (PAIR ? 256 : p.mt);
+  t.nvalid = min(sh.count[lo] - i * R, R);
+  t.n0 = static_cast<int>(tile - b * nt) * (PAIR ? 256 : p.mt);
   const int half = PAIR ? (t.nvalid + 1) / 2 : t.nvalid;
   t.box = half <= 16 ? 0 : (half <= 32 ? 1 : (half <= 64 ? 2 : 3));
   t.local = t.box == 3 ? 96 : 16 << t.box;
@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       if (e < p.E) {
         sh.first_block[e] = nb + b - b_own;
         sh.first_row[e] = (nr + r - r_own) * 128;
+        sh.count[e] = c;
         // the last row that is read has to exist (the padding after it need not)
         bad |= static_cast<int64_t>(nr + r - r_own) * 128 + c > p.rows;
       }
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   if constexpr (PAIR) cluster_sync_all();  // the peer's barriers are initialised
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int64_t tiles = static_cast<int64_t>(sh.first_block[p.E]) * p.nt;
+  const uint32_t tiles = static_cast<uint32_t>(sh.first_block[p.E]) * p.nt;
   const int nks = (p.kt + 1) / 2;
   uint32_t issued = 0;  // fills that this CTA's producer issued
 
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, x, y);
       else tma_load_2d(dst, m, bar, x, y);
     };
-    for (int64_t tile = unit; ok && tile < tiles; tile += units) {
+    for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
       const Tile t = decode<PAIR>(p, sh, tile);
       const CUtensorMap* mb = &p.mapB[t.box];
       const uint32_t bytes = (PAIR ? 128 : p.mt) * 128u + t.local * 128u + C::kSfaBytes + C::kSfbBytes;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   } else if (warp == 1 && rank == 0) {
     uint32_t s = 0, phase = 0, n = 0, used = 0;
     bool ok = true;
-    for (int64_t tile = unit; ok && tile < tiles; tile += units, ++n) {
+    for (uint32_t tile = unit; ok && tile < tiles; tile += units, ++n) {
       const Tile t = decode<PAIR>(p, sh, tile);
       const uint32_t acc = n & 1, tacc = tmem + acc * C::kRows;
       if (n >= 2 && !warp_wait(tempty(acc), (n / 2 - 1) & 1, abort_flag, err, 63, p.wait_ns)) break;
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     const int q = warp - 4;
     uint32_t* tr = sh.transpose + q * 16 * kTrRow;
     uint32_t n = 0;
-    for (int64_t tile = unit; tile < tiles; tile += units, ++n) {
+    for (uint32_t tile = unit; tile < tiles; tile += units, ++n) {
       const Tile t = decode<PAIR>(p, sh, tile);
       const uint32_t acc = n & 1;
       if (!mbar_wait(tfull(acc), (n / 2) & 1, abort_flag, err, 66, p.wait_ns)) break;
@@ -533,7 +534,7 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* a_scales, const uint
     if (i == 0 || p.rows > boxes[i - 1])
       p.mapB[i] = code_map(a, inner, static_cast<uint64_t>(p.rows), boxes[i], &st);
   if (st != cudaSuccess) return st;
-  const int64_t tiles = blocks * p.nt;
+  const int64_t tiles = blocks * p.nt;  // checked by the caller to fit 31 bits
   const int units = static_cast<int>(tiles < sms / C::kCtas ? tiles : sms / C::kCtas);
   return out_dtype == MOE_DTYPE_F32 ? launch<true, PAIR>(p, units, stream)
                                     : launch<false, PAIR>(p, units, stream);
@@ -561,6 +562,8 @@ moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t row
   if (E > kMaxE || N > kMaxFp4Cols || K > kMaxFp4Cols || rows > INT32_MAX - 256 ||
       static_cast<int64_t>(E) * N > INT32_MAX - 256)  // rows of a tile past the last expert count too
     return MOE_ERR_UNSUPPORTED;
+  // tiles of 64 x 32 at the least
+  if (((rows + 63) / 64 + E) * ((N + 31) / 32) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   Params p = {};
   p.counts = counts;
   p.rows = rows;
