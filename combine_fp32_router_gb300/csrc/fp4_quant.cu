@@ -94,22 +94,67 @@ __device__ __forceinline__ Raw8<T> load8(const T* tile, int n, int l) {
   return r;
 }
 
-// Codes and scale byte of a lane's eight values (four lanes hold a block); `sw`: the scale bytes
-// of the sixteen lanes' four blocks.
-__device__ __forceinline__ uint32_t quantize8(float (&v)[8], int l, uint32_t* sw) {
+// A lane's part of its block's largest magnitude, as fp32 bits: of eight values, or of eight raw
+// 16-bit ones two at a time (all formats order like their bits).
+__device__ __forceinline__ uint32_t largest(const float (&v)[8]) {
   uint32_t amax = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  return amax;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t largest(const Raw8<uint16_t>& r) {
+  const uint4 u = *reinterpret_cast<const uint4*>(&r);
+  constexpr uint32_t m = 0x7FFF7FFFu;
+  const uint32_t t = __vimax3_u16x2(__vimax3_u16x2(u.x & m, u.y & m, u.z & m), u.w & m, 0u);
+  const uint32_t top = max(t & 0xFFFFu, t >> 16);
+  return DT == MOE_DTYPE_BF16 ? top << 16 : __float_as_uint(In<DT>::f32(static_cast<uint16_t>(top)));
+}
+// The scale byte of the block that four lanes hold; `sw`: those of sixteen lanes' four blocks.
+__device__ __forceinline__ uint32_t block_scale(uint32_t amax, int l, uint32_t* sw) {
   amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
   amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
   const uint32_t s = mx_scale_byte(amax);
-  const float inv = mx_inverse_scale(s);
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= inv;
   *sw = s << (8 * ((l >> 2) & 3));
   *sw |= __shfl_xor_sync(0xFFFFFFFFu, *sw, 4);
   *sw |= __shfl_xor_sync(0xFFFFFFFFu, *sw, 8);
+  return s;
+}
+__device__ __forceinline__ uint32_t codes8(float (&v)[8], uint32_t s) {
+  const float inv = mx_inverse_scale(s);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] *= inv;
   return s == 255u ? 0u : e2m1x8(v);
+}
+// The same from raw values.  A bf16 times a power of two is exact in bf16 (or far below the
+// smallest code), two at a time.
+template <int DT>
+__device__ __forceinline__ uint32_t quantize8(const Raw8<typename In<DT>::T>& r, int l, uint32_t* sw) {
+  float v[8];
+  if constexpr (DT == MOE_DTYPE_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = r.v[j];
+    const uint32_t s = block_scale(largest(v), l, sw);
+    return codes8(v, s);
+  } else {
+    const uint32_t s = block_scale(largest<DT>(r), l, sw);
+    if constexpr (DT == MOE_DTYPE_F16) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = In<DT>::f32(r.v[j]);
+      return codes8(v, s);
+    } else {
+      const uint32_t i2 = (__float_as_uint(mx_inverse_scale(s)) >> 16) * 0x10001u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 t = __hmul2(reinterpret_cast<const __nv_bfloat162*>(&r)[j],
+                                         *reinterpret_cast<const __nv_bfloat162*>(&i2));
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&t);
+        v[2 * j] = bf16lo(w);
+        v[2 * j + 1] = bf16hi(w);
+      }
+      return s == 255u ? 0u : e2m1x8(v);
+    }
+  }
 }
 // The rows that the last scale tile has and the matrix has not: scale bytes of zero, by the
 // sixteen lanes of the last row's tile.
@@ -144,11 +189,8 @@ __global__ void __launch_bounds__(32 * kQuantWarps, DT == MOE_DTYPE_F32 ? 4 : 5)
   uint8_t* qo = q + static_cast<int64_t>(tile) * 64 + 4 * l;
 #pragma unroll
   for (int i = 0; i < kHalfTiles; ++i) {
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = In<DT>::f32(raw[i].v[j]);
     uint32_t sw;
-    const uint32_t code = quantize8(v, l, &sw);
+    const uint32_t code = quantize8<DT>(raw[i], l, &sw);
     if (row[i] < rows) {
       *reinterpret_cast<uint32_t*>(qo + i * 128) = code;
       if (l == 0) *reinterpret_cast<uint32_t*>(scales + so[i]) = sw;
@@ -262,7 +304,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
     const float4 b = *reinterpret_cast<const float4*>(buf + 8 * lane + 4);
     float t[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     uint32_t sw;
-    const uint32_t code = quantize8(t, lane, &sw);
+    const uint32_t code = codes8(t, block_scale(largest(t), lane, &sw));
     const int c = c0 + i * 256 + lane * 8;
     if (c < kp) {
       *reinterpret_cast<uint32_t*>(q + row * static_cast<int64_t>(kp / 2) + c / 2) = code;
@@ -497,6 +539,11 @@ moe_status_t moe_dequantize_rows_fp4(const uint8_t* q, const uint8_t* scales, in
   if (groups == 0 || rows == 0) return MOE_OK;
   if (!q || !scales || !out || !aligned16(q) || !aligned16(scales) || !aligned16(out))
     return MOE_ERR_INVALID_ARG;
+  if (rows % 128 == 0) {  // groups of whole scale tiles are one matrix
+    if (rows > INT32_MAX / groups) return MOE_ERR_UNSUPPORTED;
+    rows *= groups;
+    groups = 1;
+  }
   Cut cut;
   const bool vec = cols * dtype_bytes(dtype) % 16 == 0;  // `out` itself is aligned
   if (cols > kMaxFp4Cols || rows > INT32_MAX / groups || !cut_rows(rows * groups, cols, vec, &cut))
