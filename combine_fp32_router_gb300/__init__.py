@@ -257,6 +257,14 @@ def _raw_stream(stream, t):
     return _current_raw_stream(t.get_device())
 
 
+def _empty(shape, dtype, device, stream):
+    """A new output, from the memory of the stream that will write it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _dtype(dt):
     code = _DTYPES.get(dt)
     if code is None:
@@ -277,18 +285,19 @@ def moe_fp4_scale_bytes(rows, cols):
 def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
     """MXFP4 form of x [rows, cols] (bf16, fp16 or fp32; rows may have a stride): returns
     (q [rows, moe_fp4_row_bytes(cols)] uint8, scales [moe_fp4_scale_bytes(rows, cols)] uint8),
-    written into ``q`` and ``scales`` where they are given (see include/moe.h)."""
+    written into ``q`` and ``scales`` where they are given (see include/moe.h).  New outputs of
+    this and the calls below belong to the stream that writes them."""
     rows, cols = x.shape
     stride, one = x.stride()
     if one != 1 and cols > 1:
         raise ValueError("the values of a row must be contiguous")
     dt, kb, sb = _dtype(x.dtype), moe_fp4_row_bytes(cols), moe_fp4_scale_bytes(rows, cols)
     if q is None:
-        q = torch.empty((rows, kb), dtype=torch.uint8, device=x.device)
+        q = _empty((rows, kb), torch.uint8, x.device, stream)
     elif _nbytes(q) < rows * kb:
         raise ValueError("q too small for %d x %d values" % (rows, cols))
     if scales is None:
-        scales = torch.empty(sb, dtype=torch.uint8, device=x.device)
+        scales = _empty((sb,), torch.uint8, x.device, stream)
     elif _nbytes(scales) < sb:
         raise ValueError("scales too small for %d x %d values" % (rows, cols))
     _check(_lib.moe_quantize_rows_fp4(x.data_ptr(), dt, rows, cols, stride, _addr(q),
@@ -306,7 +315,7 @@ def moe_dequantize_rows_fp4(q, scales, cols, dtype=torch.bfloat16, stream=None):
     if shape[-1] != moe_fp4_row_bytes(cols) or \
             _nbytes(scales) < groups * moe_fp4_scale_bytes(rows, cols):
         raise ValueError("q or scales do not hold rows of %d values" % cols)
-    out = torch.empty((*shape[:-1], cols), dtype=dtype, device=q.device)
+    out = _empty((*shape[:-1], cols), dtype, q.device, stream)
     _check(_lib.moe_dequantize_rows_fp4(_addr(q), _addr(scales), groups, rows, cols, dt,
                                         out.data_ptr(), _raw_stream(stream, q)),
            "moe_dequantize_rows_fp4")
@@ -319,8 +328,8 @@ def moe_quantize_weights_fp4(W, stream=None):
     E, K, N = W.shape
     if W.dtype != torch.bfloat16:
         raise ValueError("W must be bfloat16: got %s" % W.dtype)
-    Wq = torch.empty((E, N, moe_fp4_row_bytes(K)), dtype=torch.uint8, device=W.device)
-    sc = torch.empty((E, moe_fp4_scale_bytes(N, K)), dtype=torch.uint8, device=W.device)
+    Wq = _empty((E, N, moe_fp4_row_bytes(K)), torch.uint8, W.device, stream)
+    sc = _empty((E, moe_fp4_scale_bytes(N, K)), torch.uint8, W.device, stream)
     _check(_lib.moe_quantize_weights_fp4(_addr(W), E, K, N, Wq.data_ptr(), sc.data_ptr(),
                                          _raw_stream(stream, W)),
            "moe_quantize_weights_fp4")

@@ -343,11 +343,12 @@ moe_status_t moe_quantize_weights_fp4(const moe_bf16_t* W, int E, int K, int N, 
  *   counts      : NULL (E = 1: every row), or a DEVICE array [E]: expert e's counts[e] rows
  *                 start at row sum_{j<e} round_up(counts[j], 128) (the layout of
  *                 moe_expert_forward); rows between the segments are left as they were.
- * Any rows, N, K >= 1 (rows = 0 writes nothing); E <= 1024, E * N < 2^31 - 256, N and K <= 2^20,
- * (ceil(rows / 64) + E) * ceil(N / 32) < 2^31.  Counts
- * that are negative or do not fit `rows` record MOE_ERR_DEVICE_BOUNDS and nothing is written;
- * device-side problems are read with moe_gemm_fp4_get_error, which synchronises `stream`,
- * returns the first one recorded on the current device since the last call, and clears it.
+ * Any rows, N, K >= 1 (rows = 0 writes nothing) with E <= 1024, N and K <= 2^20,
+ * E * N < 2^31 - 256 and (ceil(rows / 64) + E) * ceil(N / 32) < 2^31, else MOE_ERR_UNSUPPORTED.
+ * Counts that are negative or do not fit `rows` record MOE_ERR_DEVICE_BOUNDS and nothing is
+ * written; device-side problems are read with moe_gemm_fp4_get_error, which synchronises
+ * `stream`, returns the first one recorded on the current device since the last call, and clears
+ * it.
  */
 moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t rows,
                           const int32_t* counts, const uint8_t* b, const uint8_t* b_scales, int E,

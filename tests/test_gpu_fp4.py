@@ -219,6 +219,22 @@ def test_gemm_on_another_stream(moe):
     assert torch.equal(out, base)
 
 
+def test_new_outputs_on_another_stream(moe):
+    x = torch.randn(300, 700, generator=gen(18), device=DEV)
+    W = torch.randn(2, 300, 96, generator=gen(19), device=DEV).to(torch.bfloat16)
+    q0, s0 = moe.moe_quantize_rows_fp4(x)
+    w0, ws0 = moe.moe_quantize_weights_fp4(W)
+    v0 = moe.moe_dequantize_rows_fp4(q0, s0, 700, torch.float32)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    q1, s1 = moe.moe_quantize_rows_fp4(x, stream=s)
+    w1, ws1 = moe.moe_quantize_weights_fp4(W, stream=s)
+    v1 = moe.moe_dequantize_rows_fp4(q1, s1, 700, torch.float32, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in ((q0, q1), (s0, s1), (w0, w1), (ws0, ws1), (v0, v1)):
+        assert torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------- few tokens
 def layer(moe, T, d, E, k, dff, seed, spread=0):
     x = torch.randn(T, d, generator=gen(seed), device=DEV).to(torch.bfloat16)
