@@ -6,7 +6,8 @@
 // one expert (the N operand, so a block costs MMAs for the rows it has), in one of two shapes:
 //   pairs    256 weight rows x up to 192 rows on a CTA pair (cta_group::2): each CTA loads its
 //            half of both, 31 KB per 256 values of K for 128 x 192 outputs
-//   singles  128 weight rows x up to 64 rows on one CTA, where pairs would leave SMs idle
+//   singles  128 weight rows (or 64 or 32 of them) x up to 128 rows on one CTA, where pairs would
+//            leave SMs idle
 // Both add the same products in the same order: K runs through the tensor cores 64 values at a
 // time, whatever the other rows are.  Warps:
 //   0      producer: codes by TMA (128-byte swizzle), scale tiles by TMA (plain)
@@ -14,9 +15,11 @@
 //          runs in that order
 //   2      TMEM allocator, 3 the experts' first rows and blocks
 //   4..7   epilogue: accumulator column = output row, lane = output column
-// Bound by what an SM can take in (measured: some 100 GB/s) once a block is full: a 128 x 192
-// tile on single CTAs needs 43 KB for the same work and ran the 8192 x 7168 x 7168 product at
-// 4.8 PFLOP/s.
+// Bound, with full blocks of pairs, by the tensor pipe and the thread that feeds it: a stage of
+// 256 values of K takes some 540 cycles, 408 of them MMAs (8192 x 7168 x 7168: 131 us, 6.4
+// PFLOP/s; 128 x 192 tiles on single CTAs, which take in 43 KB for the same work, 175 us); with few
+// rows by the 128 weight rows that an MMA reads whatever it multiplies them with (70 cycles per 64
+// values of K: 3 rows of 4096 x 7168 10 us).
 #include <cuda.h>
 
 #include <atomic>
@@ -35,10 +38,10 @@ __device__ DevErr g_gemm_err;
 
 template <bool PAIR>
 struct Cfg {
-  static constexpr int kRows = PAIR ? 192 : 64;  // N of a tile
+  static constexpr int kRows = PAIR ? 192 : 128;  // N of a tile
   static constexpr int kLocal = PAIR ? kRows / 2 : kRows;  // rows a CTA loads
   static constexpr int kCtas = PAIR ? 2 : 1;
-  static constexpr int kStages = PAIR ? 5 : 7;
+  static constexpr int kStages = 5;
   static constexpr int kSfTiles = PAIR ? 2 : 1;  // 128-row scale tiles a block can touch
   static constexpr uint32_t kABytes = 128 * 128;
   static constexpr uint32_t kBBytes = kLocal * 128;
@@ -47,13 +50,13 @@ struct Cfg {
   static constexpr uint32_t kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
   static constexpr uint32_t kSfCols = 8 + 8 * kSfTiles;  // TMEM columns of a stage's scales
   static constexpr uint32_t kSfCol0 = 2 * kRows;
-  static constexpr uint32_t kTmemCols = PAIR ? 512 : 256;
+  static constexpr uint32_t kTmemCols = 512;
   static_assert(kSfCol0 + kStages * kSfCols <= kTmemCols, "TMEM columns");
   static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
-constexpr int kBoxes = 4;  // box heights of the activation rows: 16, 32, 64, and 96 (pairs)
+constexpr int kBoxes = 4;  // box heights of the activation rows: 16, 32, 64, and 96 (pairs) or 128
 constexpr int kThreads = 256;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 5;
 constexpr int kTrRow = 36;  // words of a transpose row: 32 columns, padded against bank conflicts
 
 struct Params {
@@ -129,7 +132,7 @@ __device__ __forceinline__ Tile decode(const Params& p, const Shared& sh, uint32
   t.n0 = static_cast<int>(tile - b * nt) * (PAIR ? 256 : p.mt);
   const int half = PAIR ? (t.nvalid + 1) / 2 : t.nvalid;
   t.box = half <= 16 ? 0 : (half <= 32 ? 1 : (half <= 64 ? 2 : 3));
-  t.local = t.box == 3 ? 96 : 16 << t.box;
+  t.local = PAIR && t.box == 3 ? 96 : 16 << t.box;
   return t;
 }
 
@@ -497,22 +500,22 @@ CUtensorMap scale_map(const void* base, int kt, uint64_t tiles, uint32_t box_til
   return m;
 }
 
-// Pairs or singles, by the time of the rounds of tiles that each takes: a stage costs a single
-// some 390 cycles (its MMAs read 128 weight rows however few columns they have) and a pair
-// 130 + 2.1 per activation row, at least 410.  Measured on GB300, single and pair: 256 rows of
-// N 4096, K 7168 11.0 and 12.1 us; 384 rows of 4096 x 4096 12.2 and 9.2; 777 of 1545 x 2976 11.3
-// and 12.0; 512 of 7168 x 2048 10.7 and 9.4; over 64 experts of 1024 x 2048 300 rows 11.4 and
-// 12.4, 4000 rows 18.7 and 16.4.  With `counts` the experts are taken to have equal shares.
-bool use_pairs(int64_t rows, int N, int E, int sms) {
+// Pairs or singles, by the rounds of tiles that each takes over the SMs: a full round of pairs
+// costs 9/8 of one of singles (both then take in what an SM can, 955 and 843 cycles a stage over
+// 64 experts).  Measured on GB300, single and pair: 3 rows of N 4096, K 7168 10.0 and 10.6 us; 777
+// of 1545 x 2976 9.6 and 11.8; 1024 of 2048 x 2048 6.0 and 7.1; 4096 of 1024 x 2048 8.8 and 9.7;
+// over 64 experts of 1024 x 2048 300 rows 11.2 and 12.2, 24576 rows 42.6 and 36.2; 8192 of 7168 x
+// 7168 175 (128 x 192 singles) and 131.  With `counts`, which are on the device, the experts are
+// taken to have equal shares of the rows less half a tile of padding each; both shapes give the
+// same bits.
+bool use_pairs(int64_t rows, int N, int E, bool grouped, int sms) {
+  if (grouped) rows = rows > 65 * static_cast<int64_t>(E) ? rows - 64 * static_cast<int64_t>(E) : E;
   const int64_t share = (rows + E - 1) / E;
-  const auto time = [&](int height, int width, int units, int64_t stage) {
+  const auto rounds = [&](int height, int width, int units) {
     const int64_t tiles = E * ((share + height - 1) / height) * ((N + width - 1) / width);
-    return (tiles + units - 1) / units * stage;
+    return (tiles + units - 1) / units;
   };
-  const int64_t n = share < Cfg<true>::kRows ? share : Cfg<true>::kRows;
-  const int64_t stage = 130 + 21 * n / 10;
-  return time(Cfg<true>::kRows, 256, sms / 2, stage < 410 ? 410 : stage) <
-         time(Cfg<false>::kRows, 128, sms, 390);
+  return 9 * rounds(Cfg<true>::kRows, 256, sms / 2) < 8 * rounds(Cfg<false>::kRows, 128, sms);
 }
 
 template <bool PAIR>
@@ -529,8 +532,8 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* a_scales, const uint
   p.mapA = code_map(b, inner, static_cast<uint64_t>(p.E) * p.N, p.mt, &st);
   p.mapSa = scale_map(b_scales, p.kt, static_cast<uint64_t>(p.E) * p.sf_tiles, 1, &st);
   p.mapSb = scale_map(a_scales, p.kt, static_cast<uint64_t>((p.rows + 127) / 128), C::kSfTiles, &st);
-  const int boxes[kBoxes] = {16, 32, 64, 96};
-  for (int i = 0; i < (PAIR ? 4 : 3); ++i)  // no block has more than `rows`
+  const int boxes[kBoxes] = {16, 32, 64, PAIR ? 96 : 128};
+  for (int i = 0; i < kBoxes; ++i)  // no block has more than `rows`
     if (i == 0 || p.rows > boxes[i - 1])
       p.mapB[i] = code_map(a, inner, static_cast<uint64_t>(p.rows), boxes[i], &st);
   if (st != cudaSuccess) return st;
@@ -577,7 +580,7 @@ moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t row
   p.wait_ns = wait_limit_ns();
   const int sms = num_sms_of_current_device();
   const cudaError_t st =
-      use_pairs(rows, N, E, sms)
+      use_pairs(rows, N, E, counts != nullptr, sms)
           ? run<true>(p, a, a_scales, b, b_scales, K, out_dtype, sms, stream)
           : run<false>(p, a, a_scales, b, b_scales, K, out_dtype, sms, stream);
   return st == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

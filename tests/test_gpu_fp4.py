@@ -168,6 +168,45 @@ def test_gemm_rows_do_not_depend_on_the_batch(moe):
     assert torch.equal(product(a.flip(0)).flip(0), whole)
 
 
+def test_gemm_tile_shapes_give_the_same_bits(moe):
+    """Many rows run on CTA pairs, a hundred of them alone on single CTAs, ten on single CTAs with
+    fewer weight rows each."""
+    rows, K, N = 4000, 600, 4096
+    a = torch.randn(rows, K, generator=gen(110), device=DEV)
+    bq, sb = moe.moe_quantize_weights_fp4(
+        torch.randn(1, K, N, generator=gen(111), device=DEV).to(torch.bfloat16))
+
+    def product(x):
+        q, s = moe.moe_quantize_rows_fp4(x)
+        o = torch.empty(x.shape[0], N, device=DEV)
+        moe.moe_gemm_fp4(q, s, bq, sb, o, K)
+        return o
+    whole = product(a)
+    for first, n in ((0, 100), (1234, 100), (3990, 10), (2000, 1)):
+        assert torch.equal(product(a[first:first + n].contiguous()), whole[first:first + n])
+    assert moe.moe_gemm_fp4_get_error() == moe.MOE_OK
+
+
+def test_gemm_grouped_on_pairs(moe):
+    counts, N, K = [2000, 0, 1500, 193, 64, 3000, 1, 700], 2048, 384
+    E, rows = len(counts), sum(ref.up(c, 128) for c in counts)
+    a = torch.randn(rows, K, generator=gen(112), device=DEV)
+    b = torch.randn(E, K, N, generator=gen(113), device=DEV).to(torch.bfloat16)
+    aq, sa = moe.moe_quantize_rows_fp4(a)
+    bq, sb = moe.moe_quantize_weights_fp4(b)
+    out = torch.full((rows, N), 7.0, device=DEV)
+    moe.moe_gemm_fp4(aq, sa, bq, sb, out, K,
+                     counts=torch.tensor(counts, dtype=torch.int32, device=DEV))
+    av = ref.values(aq, sa, rows, K)
+    at = 0
+    for e, c in enumerate(counts):
+        bv = ref.values(bq[e], sb[e], N, K)
+        assert ref.within(out[at:at + c], av[at:at + c] @ bv.t(), gemm_bound(av[at:at + c], bv))
+        assert bool((out[at + c:at + ref.up(c, 128)] == 7.0).all())
+        at += ref.up(c, 128)
+    assert moe.moe_gemm_fp4_get_error() == moe.MOE_OK
+
+
 def test_gemm_nan_scales_reach_their_rows_and_columns_only(moe):
     a = torch.randn(200, 256, generator=gen(12), device=DEV)
     a[150, 70] = float("inf")
