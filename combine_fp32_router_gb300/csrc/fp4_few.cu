@@ -79,7 +79,7 @@ FewLayout few_layout(int64_t T, int d, int E, int k, int dff) {
   L.clear_end = at;
   L.xq = take(T * kTerms * (d / 2));
   // scale tiles [d / 128][512] of up to 8 tokens, or words [d / 128][T kTerms] of more
-  L.xs = take(T <= kTok ? static_cast<size_t>(d / 128) * kMxTileBytes : static_cast<size_t>(d / 128) * T * kTerms * 4);
+  L.xs = take(static_cast<size_t>(d / 128) * (T <= kTok ? kMxTileBytes : T * kTerms * 4));
   L.gq = take(T <= kTok ? 0 : G * rows * (d / 2));
   L.gs = take(T <= kTok ? 0 : G * (d / 128) * kMxTileBytes);
   L.hq = take(G * rows * (dff / 2));
@@ -164,9 +164,10 @@ struct RouterParams {
 constexpr int kRouterExperts = 2;  // per CTA
 constexpr int kRouterThreads = 256;
 
-// Every CTA clears its share of the counters and marks its share of the sums' places; the first `conv` write x in MXFP4 terms; each of
-// the others computes the logits of two experts for up to TB tokens (blockIdx.y: which): warp w
-// sums the 128-value pieces w, w + 8, ... of d, lanes then warps are added in a fixed order.
+// Every CTA clears its share of the counters and marks its share of the sums' places; the first
+// `conv` write x in MXFP4 terms; each of the next computes the logits of two experts for up to TB
+// tokens (blockIdx.y: which): warp w sums the 128-value pieces w, w + 8, ... of d, lanes then warps
+// are added in a fixed order.  Any others only mark.
 template <int TB>
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams p) {
   griddep_wait();
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams
     }
   }
   const int e0 = (static_cast<int>(blockIdx.x) - p.conv) * kRouterExperts;
-  if (e0 < 0 || e0 >= p.E) return;
+  if (!p.router || e0 < 0 || e0 >= p.E) return;
   const int t0 = blockIdx.y * TB, tn = min(TB, p.T - t0);
   const int ne = min(kRouterExperts, p.E - e0);
   const float* r0 = p.router + static_cast<int64_t>(e0) * p.d;
@@ -364,71 +365,17 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, uint3
       : "memory");
 }
 
-// Top-k and gate of one token by one warp, the same selection and arithmetic as topk_token.  A
-// lane sorts its logits first (best one on top, ties by index), so a round is a max-reduction
-// over the lanes' best, a vote, and the winner's step to its next one.
+// Routing of one token by one warp.  (Lists of logits sorted per lane, or every logit's rank counted
+// by a thread, were no faster: each CTA runs this code once per launch.)
 template <int EPL>
 __device__ __forceinline__ void route_token(const ExpertParams& p, Shared& sh, int t, int lane) {
-  uint32_t key[EPL], idx[EPL];
+  float v[EPL];
 #pragma unroll
-  for (int c = 0; c < EPL; ++c) {
-    idx[c] = lane + 32 * c;
-    key[c] = 0u;  // below every logit's key but the NaN with all bits set
-    if (lane + 32 * c < p.E) key[c] = order_key(__ldcg(p.logits + static_cast<int64_t>(t) * p.E + lane + 32 * c));
-    else idx[c] = 0xFFFFu;  // no expert: after every other
-  }
-#pragma unroll
-  for (int a = 1; a < EPL; ++a)  // insertion, as fixed exchanges
-#pragma unroll
-    for (int c = a; c > 0; --c) {
-      const bool swap = key[c] > key[c - 1] || (key[c] == key[c - 1] && idx[c] < idx[c - 1]);
-      const uint32_t k0 = swap ? key[c] : key[c - 1], k1 = swap ? key[c - 1] : key[c];
-      const uint32_t i0 = swap ? idx[c] : idx[c - 1], i1 = swap ? idx[c - 1] : idx[c];
-      key[c - 1] = k0;
-      key[c] = k1;
-      idx[c - 1] = i0;
-      idx[c] = i1;
-    }
-  int sel_e = 0;
-  float sel_v = 0.0f;
-  for (int j = 0; j < p.k; ++j) {
-    const uint32_t bk = __reduce_max_sync(0xFFFFFFFFu, key[0]);
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, key[0] == bk);
-    uint32_t e = __shfl_sync(0xFFFFFFFFu, idx[0], __ffs(who) - 1);
-    if (who & (who - 1u)) e = __reduce_min_sync(0xFFFFFFFFu, key[0] == bk ? idx[0] : 0xFFFFu);  // a tie
-    const bool won = idx[0] == e;
-#pragma unroll
-    for (int c = 0; c < EPL; ++c) {
-      key[c] = won ? (c + 1 < EPL ? key[c + 1 < EPL ? c + 1 : c] : 0u) : key[c];
-      idx[c] = won ? (c + 1 < EPL ? idx[c + 1 < EPL ? c + 1 : c] : 0xFFFFu) : idx[c];
-    }
-    if (lane == j) {
-      sel_e = static_cast<int>(e);
-      sel_v = order_value(bk);
-    }
-  }
-  const float v0 = __shfl_sync(0xFFFFFFFFu, sel_v, 0);
-  const float ex = lane < p.k ? expf(sel_v - v0) : 0.0f;
-  float sum = 0.0f;
-  for (int j = 0; j < p.k; ++j) sum += __shfl_sync(0xFFFFFFFFu, ex, j);
-  const int top = __reduce_max_sync(0xFFFFFFFFu, lane < p.k ? sel_e : 0);
-  if (lane < p.k) {
-    sh.slot_e[t][lane] = static_cast<uint16_t>(sel_e);
-    sh.gate[t][lane] = ex / sum;
-    atomicOr(&sh.mask[sel_e], 1u << t);
-  }
-  if (lane == 0) sh.last_e[t] = top;
-}
-
-// The same for up to 1024 experts, whose sorted lists would not fit the registers.
-__device__ void route_token_any(const ExpertParams& p, Shared& sh, int t, int lane) {
-  float v[kMaxE / 32];
-#pragma unroll
-  for (int c = 0; c < kMaxE / 32; ++c)
+  for (int c = 0; c < EPL; ++c)
     v[c] = lane + 32 * c < p.E ? __ldcg(p.logits + static_cast<int64_t>(t) * p.E + lane + 32 * c) : 0.0f;
   int e;
   float g;
-  topk_token<kMaxE / 32>(v, p.E, p.k, lane, &e, &g);
+  topk_token<EPL>(v, p.E, p.k, lane, &e, &g);
   const int top = __reduce_max_sync(0xFFFFFFFFu, lane < p.k ? e : 0);
   if (lane < p.k) {
     sh.slot_e[t][lane] = static_cast<uint16_t>(e);
@@ -514,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int t = warp; t < p.T; t += kThreads / 32) {
     if (p.E <= 64) route_token<2>(p, sh, t, lane);
     else if (p.E <= 256) route_token<8>(p, sh, t, lane);
-    else route_token_any(p, sh, t, lane);
+    else route_token<kMaxE / 32>(p, sh, t, lane);
   }
   __syncthreads();
   // groups of up to 8 tokens per chosen expert, in expert order; 32 experts per warp at a time
@@ -1020,7 +967,9 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
 
   const int64_t conv = T * ((d + kRouterThreads * 8 - 1) / (kRouterThreads * 8));
   r.conv = static_cast<int>(conv < 152 ? conv : 152);
-  const int rgrid = r.conv + (router ? (E + kRouterExperts - 1) / kRouterExperts : 0);
+  int rgrid = r.conv + (router ? (E + kRouterExperts - 1) / kRouterExperts : 0);
+  const int64_t marking = r.n_places / (4 * kRouterThreads);  // CTAs of four stores a thread
+  if (rgrid < 2 * 152 && rgrid < marking) rgrid = static_cast<int>(marking < 2 * 152 ? marking : 2 * 152);
   st = T <= 1   ? launch_router<1>(r, rgrid, stream)
        : T <= 4 ? launch_router<4>(r, rgrid, stream)
                 : launch_router<8>(r, rgrid, stream);
