@@ -14,8 +14,8 @@
 // d_ff = 2048, where the stream alone takes 225 us.)
 //
 // Units of work are 128 weight rows x a range of K for up to 8 tokens of an expert, first of
-// W1 and W3, then of W2.  CTAs take them from a counter in that order, so whoever waits for an h
-// waits only for units that running CTAs hold.  Every sum's order is fixed by the sizes:
+// W1 and W3, then of W2, at last the tokens' combines.  CTAs take them from a counter in that order, so whoever waits for an h
+// (or a row of y) waits only for units that running CTAs hold.  Every sum's order is fixed by the sizes:
 // results do not depend on the batch or on which CTA did what.
 #include <cuda.h>
 
@@ -323,8 +323,8 @@ struct Group {
   int32_t n;
 };
 struct Unit {
-  int32_t kind;  // 0: no more work, 1: W1 or W3 rows, 2: W2 rows
-  int32_t group, tile, q;  // q: matrix + 2 * K range
+  int32_t kind;  // 0: no more work, 1: W1 or W3 rows, 2: W2 rows, 3: a token's combine
+  int32_t group, tile, q;  // q: matrix + 2 * K range; kind 3: group is the token
 };
 struct StageMeta {
   Unit u;
@@ -337,7 +337,6 @@ struct Shared {
   uint32_t mask[kMaxE];
   int32_t base[kMaxE];  // first row of an expert's tokens
   float gate[kMaxT][kMaxK];
-  int32_t last_e[kMaxT];  // a token's highest expert
   uint16_t slot_e[kMaxT][kMaxK];
   StageMeta meta[kMaxStages];
   Unit acc_unit[kGroups];
@@ -376,13 +375,11 @@ __device__ __forceinline__ void route_token(const ExpertParams& p, Shared& sh, i
   int e;
   float g;
   topk_token<EPL>(v, p.E, p.k, lane, &e, &g);
-  const int top = __reduce_max_sync(0xFFFFFFFFu, lane < p.k ? e : 0);
   if (lane < p.k) {
     sh.slot_e[t][lane] = static_cast<uint16_t>(e);
     sh.gate[t][lane] = g;
     atomicOr(&sh.mask[e], 1u << t);
   }
-  if (lane == 0) sh.last_e[t] = top;
 }
 
 // Row of (token, slot) in h and y: rows by (expert, token)
@@ -516,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool direct = p.T <= kTok;  // column = token; else column = place in the group
   const int groups = sh.groups;
   const int ht = p.dff / 128, yt = p.d / 128, Q = 2 * p.parts;
-  const int n0 = direct ? 0 : groups, n1 = n0 + groups * ht * Q, n_units = n1 + groups * yt;
+  const int n0 = direct ? 0 : groups, n1 = n0 + groups * ht * Q, n2 = n1 + groups * yt;
+  const int n_units = n2 + p.T * yt;
   const int kt1 = p.d / 128, kt2 = p.dff / 128;
   if (!direct) {  // the first units: gathering
     while (true) {
@@ -524,12 +522,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncthreads();
       const int u = sh.ticket;
       if (u >= n0) break;
+      if (threadIdx.x == 0) next = atomicAdd(p.ticket, 1);
       gather_group(p, sh, u);
       __syncthreads();
-      if (threadIdx.x == 0) {
-        red_release_add(p.xdone + u, 1);
-        next = atomicAdd(p.ticket, 1);
-      }
+      if (threadIdx.x == 0) red_release_add(p.xdone + u, 1);
     }
   }
   const int st1 = (kt1 + kStageKt - 1) / kStageKt, st2 = (kt2 + kStageKt - 1) / kStageKt;
@@ -549,11 +545,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         un = Unit{1, v / (ht * Q), w / Q, w % Q};
         ks0 = st1 * (un.q >> 1) / p.parts;
         ks1 = st1 * ((un.q >> 1) + 1) / p.parts;
-      } else if (work) {
+      } else if (work && u < n2) {
         un = Unit{2, (u - n1) / yt, (u - n1) % yt, 0};
         ks1 = st2;
+      } else if (work) {
+        un = Unit{3, (u - n2) / yt, (u - n2) % yt, 0};
       }
-      const int e = sh.group[un.group].e;
+      const bool loads = work && u < n2;
+      const int e = loads ? sh.group[un.group].e : 0;
       const bool first = un.kind == 1;
       const bool wide = first ? p.wide1 : p.wide2;
       const int kt = first ? kt1 : kt2;
@@ -570,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
           sh.meta[s] = StageMeta{un, ks, nkt, (ks == ks0 ? 1 : 0) | (ks == ks1 - 1 ? 2 : 0)};
           mbar_arrive(told(s));
-          if (!work) {
+          if (!loads) {
             mbar_arrive(full(s));
           } else if (wide) {
             mbar_arrive_expect_tx(full(s), kABytes + nkt * kMxTileBytes);
@@ -581,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < pieces; ++c)
               tma_load_2d(st + c * (kABytes / 2), mw, full(s), (2 * ks + c) * 128, wrow);
           }
-          if (work)
+          if (loads)
             bulk_load(st + kABytes + 2 * p.n * 128u, sfa + static_cast<int64_t>(ks) * kSfBytes,
                       nkt * kMxTileBytes, full(s));
         }
@@ -605,9 +604,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t bbytes = p.n * 128u;
     while (warp_wait(told(s), phase, abort_flag, p.err, 77, p.wait_ns)) {
       const StageMeta m = sh.meta[s];
-      if (m.u.kind == 0) {
+      if (m.u.kind == 0 || m.u.kind == 3) {  // nothing to load
         if (elect_one()) mbar_arrive(full(s));
-        break;
+        __syncwarp();
+        if (m.u.kind == 0) break;
+        if (++s == S) {
+          s = 0;
+          phase ^= 1;
+        }
+        continue;
       }
       const bool first = m.u.kind == 1;
       const bool wide = first ? p.wide1 : p.wide2;
@@ -675,7 +680,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t st = base + s * p.stage_bytes, stb = st + kABytes;
       const uint32_t ssa = stb + 2 * bbytes, ssb = ssa + kSfBytes;
       const uint32_t tsf = tmem + kSfCol0 + s * kSfCols;
-      if (elect_one()) {
+      if (m.u.kind == 3) {  // handed on without MMAs
+        if (elect_one()) {
+          mbar_arrive(empty(s));
+          sh.acc_unit[acc] = m.u;
+          mbar_arrive(tfull(acc));
+          mbar_arrive(tfull(acc));
+        }
+      } else if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < kStageKt; ++i) {
           if (i < m.nkt) {
@@ -719,6 +731,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(tfull(acc), i & 1, abort_flag, p.err, 76, p.wait_ns)) break;
       const Unit un = sh.acc_unit[acc];
       if (un.kind == 0) break;
+      if (un.kind == 3) {
+        // 32 columns of a token, in slot order; the units of its experts are all older.  (Combining a
+        // token in the unit of its last expert left most of them to the last few units: a tail of 5 us
+        // at 32 tokens over 64 experts.)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty(acc));
+        const int t = un.group, col = 128 * un.tile + 32 * qd + lane;
+        float o = 0.0f;
+        bool ok = true;
+#pragma unroll 1
+        for (int jb = 0; ok && jb < p.k; jb += 8) {
+          float v[8];
+          ok = get_sums([&](int i) { return p.y + static_cast<int64_t>(row_of(sh, t, jb + i)) * p.d + col; },
+                        min(8, p.k - jb), v, abort_flag, p.err, 79, p.wait_ns);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (jb + j < p.k) o = fmaf(sh.gate[t][jb + j], v[j], o);
+        }
+        if (!ok) break;
+        p.out[static_cast<int64_t>(t) * p.d + col] = bf16_bits(o);
+        continue;
+      }
       tc_fence_after();
       const uint32_t tacc = tmem + acc * kAccCols + (static_cast<uint32_t>(32 * qd) << 16);
       float v[kMaxN];
@@ -798,29 +832,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_global();
         __syncwarp();
         if (lane == 0) red_release_add(p.done1 + un.group, 1);
-      } else {
-        // the tokens whose last expert this is are combined here, in slot order; the units of
-        // their other experts are older
-        const float* y = p.y + 128 * un.tile + 32 * qd + lane;
-        uint32_t left = gr.tokens;
-        bool ok = true;
-#pragma unroll 1
-        for (; ok && left; left &= left - 1u) {
-          const int t = __ffs(left) - 1;
-          if (sh.last_e[t] != gr.e) continue;
-          float o = 0.0f;
-#pragma unroll 1
-          for (int jb = 0; ok && jb < p.k; jb += 8) {
-            float v[8];
-            ok = get_sums([&](int i) { return y + static_cast<int64_t>(row_of(sh, t, jb + i)) * p.d; },
-                          min(8, p.k - jb), v, abort_flag, p.err, 79, p.wait_ns);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              if (jb + j < p.k) o = fmaf(sh.gate[t][jb + j], v[j], o);
-          }
-          p.out[static_cast<int64_t>(t) * p.d + 128 * un.tile + 32 * qd + lane] = bf16_bits(o);
-        }
-        if (!ok) break;
       }
     }
   }
@@ -986,7 +997,7 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
     attr_set_mask.fetch_or(bit, std::memory_order_release);
   }
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + sizeof(Shared);
-  const int64_t units = T * k * (d_ff / 128 * 2 * L.parts + d / 128);
+  const int64_t units = T * k * (d_ff / 128 * 2 * L.parts + d / 128) + T * (d / 128);
   const int sms = num_sms_of_current_device();
   st = launch_pdl(few_experts_kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)),
                   dim3(kThreads), smem, stream, p);
