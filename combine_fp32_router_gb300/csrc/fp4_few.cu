@@ -9,14 +9,14 @@
 // residual of each being quantised again: a term leaves at most 1/5 of its block's largest
 // value, six at most 2^-13.9 of it (2^-19 is usual), which is below what rounding to bf16
 // would cost.  A token's terms are six columns of the N operand, the partial products are
-// added in fp32.  (Converting the weights to fp16 for mma.sync instead kept the integer pipe
-// busy for longer than the memory: 502 us for 16 tokens over 64 experts of d = 7168,
-// d_ff = 2048, where the stream alone takes 225 us.)
+// added in fp32.  (Converting the weights to fp16 for mma.sync took 502 us for 16 tokens over 64
+// experts of d = 7168, d_ff = 2048; this takes 218 us, 6.9 TB/s.)
 //
 // Units of work are 128 weight rows x a range of K for up to 8 tokens of an expert, first of
-// W1 and W3, then of W2, at last the tokens' combines.  CTAs take them from a counter in that order, so whoever waits for an h
-// (or a row of y) waits only for units that running CTAs hold.  Every sum's order is fixed by the sizes:
-// results do not depend on the batch or on which CTA did what.
+// W1 and W3, then of W2, at last the tokens' combines.  CTAs take them from a counter in that
+// order, so whoever waits for an h (or a row of y) waits only for units that running CTAs hold.
+// Every sum's order is fixed by the sizes: results do not depend on the batch or on which CTA did
+// what.
 #include <cuda.h>
 
 #include <atomic>
@@ -39,15 +39,16 @@ constexpr int kPartStages = 4;           // stages of a K range of W1 and W3 (at
 constexpr uint32_t kABytes = 128 * kStageKt * 64;
 constexpr uint32_t kSfBytes = kStageKt * kMxTileBytes;
 constexpr int kMaxStages = 4;  // 160 KB in flight per SM; more only lengthens every other round trip
-// Four groups of four warps finish units in turn, each with an accumulator of its own: publishing
-// a unit's sums (store, fence, counter) and, for the last of a tile, SwiGLU and the terms of h
-// take 2 to 4 us, about as long as streaming the next unit's weights.  With one group the stream
-// waited for it: 320 us instead of 255 us for 16 tokens over 64 experts.
+// Four groups of four warps finish units in turn, each with an accumulator of its own: waiting
+// for a tile's other sums, SwiGLU and the terms of h take longer than streaming the next unit's
+// weights (round trips take 2 to 4 us beside a full ring).  With one group the stream waited for
+// it: 320 us instead of 253 us for 16 tokens over 64 experts, the rest being equal.
 constexpr int kGroups = 4;
 constexpr uint32_t kAccCols = 64;        // TMEM: the accumulators, then the stages' scales
 constexpr uint32_t kSfCol0 = kGroups * kAccCols;
 constexpr uint32_t kSfCols = 8 * kStageKt;
-static_assert(kSfCol0 + kMaxStages * kSfCols <= 512 && kMaxN <= static_cast<int>(kAccCols), "TMEM columns");
+static_assert(kSfCol0 + kMaxStages * kSfCols <= 512 && kMaxN <= static_cast<int>(kAccCols),
+              "TMEM columns");
 // warps 0 and 3 load weights and activations, 1 issues MMAs, 2 owns TMEM, 4 on finish units
 constexpr int kThreads = 128 + 128 * kGroups;
 

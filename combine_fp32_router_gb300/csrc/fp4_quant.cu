@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
 // columns; codes and scale words leave through shared memory in 16-byte and 4-byte pieces of
 // whole rows.
 constexpr int kWtK = 256, kWtN = 64;
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 5)
     quantize_weights_fp4_kernel(const uint16_t* __restrict__ W, int K, int N, int n_tiles,
                                 uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   griddep_wait();
@@ -403,27 +403,29 @@ __global__ void __launch_bounds__(256)
   }
   __syncthreads();
   const int np = tid & 31, b = tid >> 5;
-  uint32_t a0 = 0, a1 = 0;
+  // both columns at a time: magnitudes order like their bits, and a bf16 times a power of two is
+  // exact in bf16 (or far below the smallest code)
+  uint32_t top = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const uint32_t t = tile[32 * b + i][np];
-    a0 = max(a0, (t << 16) & 0x7FFFFFFFu);
-    a1 = max(a1, t & 0x7FFF0000u);
-  }
-  const uint32_t s0 = mx_scale_byte(a0), s1 = mx_scale_byte(a1);
-  const float i0 = mx_inverse_scale(s0), i1 = mx_inverse_scale(s1);
+  for (int i = 0; i < 32; ++i) top = __vmaxu2(top, tile[32 * b + i][np] & 0x7FFF7FFFu);
+  const uint32_t s0 = mx_scale_byte(top << 16), s1 = mx_scale_byte(top & 0xFFFF0000u);
+  const uint32_t inv = (__float_as_uint(mx_inverse_scale(s0)) >> 16) |
+                       (__float_as_uint(mx_inverse_scale(s1)) & 0xFFFF0000u);
   uint32_t w0[4], w1[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float v0[8], v1[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t t = tile[32 * b + 8 * i + j][np];
-      v0[j] = s0 == 255u ? 0.0f : bf16lo(t) * i0;
-      v1[j] = s1 == 255u ? 0.0f : bf16hi(t) * i1;
+      const __nv_bfloat162 t =
+          __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&tile[32 * b + 8 * i + j][np]),
+                  *reinterpret_cast<const __nv_bfloat162*>(&inv));
+      const uint32_t u = *reinterpret_cast<const uint32_t*>(&t);
+      v0[j] = bf16lo(u);
+      v1[j] = bf16hi(u);
     }
-    w0[i] = e2m1x8(v0);
-    w1[i] = e2m1x8(v1);
+    w0[i] = s0 == 255u ? 0u : e2m1x8(v0);
+    w1[i] = s1 == 255u ? 0u : e2m1x8(v1);
   }
   codes[2 * np][b] = make_uint4(w0[0], w0[1], w0[2], w0[3]);
   codes[2 * np + 1][b] = make_uint4(w1[0], w1[1], w1[2], w1[3]);
