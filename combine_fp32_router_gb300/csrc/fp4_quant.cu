@@ -165,7 +165,7 @@ __device__ __forceinline__ void pad_tile(uint8_t* scales, int64_t place, uint32_
 }
 
 template <int DT>
-__global__ void __launch_bounds__(32 * kQuantWarps, DT == MOE_DTYPE_F32 ? 4 : 5)
+__global__ void __launch_bounds__(32 * kQuantWarps, DT == MOE_DTYPE_F32 ? 4 : 6)
     quantize_rows_kernel(const typename In<DT>::T* __restrict__ x, int64_t rows, int cols,
                          int64_t stride, uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   using T = typename In<DT>::T;
