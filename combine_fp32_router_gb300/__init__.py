@@ -291,18 +291,21 @@ def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
     stride, one = x.stride()
     if one != 1 and cols > 1:
         raise ValueError("the values of a row must be contiguous")
-    dt, kb, sb = _dtype(x.dtype), moe_fp4_row_bytes(cols), moe_fp4_scale_bytes(rows, cols)
+    dt = _dtype(x.dtype)
+    kt = (cols + 127) // 128
+    sb = (rows + 127) // 128 * kt * 512
     if q is None:
-        q = _empty((rows, kb), torch.uint8, x.device, stream)
-    elif _nbytes(q) < rows * kb:
-        raise ValueError("q too small for %d x %d values" % (rows, cols))
+        q = _empty((rows, kt * 64), torch.uint8, x.device, stream)
+    elif _nbytes(q) < rows * kt * 64 or not q.is_contiguous():
+        raise ValueError("q too small for %d x %d values, or not contiguous" % (rows, cols))
     if scales is None:
         scales = _empty((sb,), torch.uint8, x.device, stream)
-    elif _nbytes(scales) < sb:
-        raise ValueError("scales too small for %d x %d values" % (rows, cols))
-    _check(_lib.moe_quantize_rows_fp4(x.data_ptr(), dt, rows, cols, stride, _addr(q),
-                                      _addr(scales), _raw_stream(stream, x)),
-           "moe_quantize_rows_fp4")
+    elif _nbytes(scales) < sb or not scales.is_contiguous():
+        raise ValueError("scales too small for %d x %d values, or not contiguous" % (rows, cols))
+    st = _lib.moe_quantize_rows_fp4(x.data_ptr(), dt, rows, cols, stride, q.data_ptr(),
+                                    scales.data_ptr(), _raw_stream(stream, x))
+    if st:
+        raise MoeError(st, "moe_quantize_rows_fp4")
     return q, scales
 
 
@@ -312,13 +315,14 @@ def moe_dequantize_rows_fp4(q, scales, cols, dtype=torch.bfloat16, stream=None):
     shape = q.shape
     groups, rows = (shape[0], shape[1]) if len(shape) == 3 else (1, shape[0])
     dt = _dtype(dtype)
-    if shape[-1] != moe_fp4_row_bytes(cols) or \
-            _nbytes(scales) < groups * moe_fp4_scale_bytes(rows, cols):
+    kt = (cols + 127) // 128
+    if shape[-1] != kt * 64 or _nbytes(scales) < groups * ((rows + 127) // 128) * kt * 512:
         raise ValueError("q or scales do not hold rows of %d values" % cols)
     out = _empty((*shape[:-1], cols), dtype, q.device, stream)
-    _check(_lib.moe_dequantize_rows_fp4(_addr(q), _addr(scales), groups, rows, cols, dt,
-                                        out.data_ptr(), _raw_stream(stream, q)),
-           "moe_dequantize_rows_fp4")
+    st = _lib.moe_dequantize_rows_fp4(_addr(q), _addr(scales), groups, rows, cols, dt,
+                                      out.data_ptr(), _raw_stream(stream, q))
+    if st:
+        raise MoeError(st, "moe_dequantize_rows_fp4")
     return out
 
 
