@@ -39,13 +39,15 @@ struct In<MOE_DTYPE_F32> {
   static __device__ __forceinline__ T of(float v) { return v; }
 };
 
-constexpr int kQuantWarps = 8;
+// Warps of a CTA.  Four leave an SM's places sooner than eight: 16384 x 7168 bf16 values 50.9 and
+// 45.3 us (quantise and back) against 51.4 and 46.0; two are no faster.
+constexpr int kQuantWarps = 4;
 
 // ---- rows that start on 16 bytes.  The matrix is cut into tiles of 128 values of a row, rows x kt
 // of them in row-major order, and each warp takes eight that follow one another: half a warp every
 // second one, lane l of it the values 8 l .. 8 l + 7.  Four lanes then hold a block and sixteen
 // the four blocks of a scale word, whatever the width: no lane idles on narrow rows (25894 rows of
-// 328 bf16 values: 7.2 us to quantise, 10.1 us with whole rows per warp).
+// 328 bf16 values: 7.4 us to quantise, 10.1 us with whole rows per warp).
 constexpr int kHalfTiles = 4;  // tiles per half warp, all loaded before the first is used
 
 // A half warp's walk over its tiles: row and tile, the tile's first value in a matrix with rows
@@ -165,7 +167,7 @@ __device__ __forceinline__ void pad_tile(uint8_t* scales, int64_t place, uint32_
 }
 
 template <int DT>
-__global__ void __launch_bounds__(32 * kQuantWarps, DT == MOE_DTYPE_F32 ? 4 : 6)
+__global__ void __launch_bounds__(32 * kQuantWarps, DT == MOE_DTYPE_F32 ? 8 : 12)
     quantize_rows_kernel(const typename In<DT>::T* __restrict__ x, int64_t rows, int cols,
                          int64_t stride, uint8_t* __restrict__ q, uint8_t* __restrict__ scales) {
   using T = typename In<DT>::T;
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
 
 // ---- other rows.  A warp takes U x 256 values of one row; its lanes read or store neighbouring
 // values, 32 at a time, and pass them on through shared memory (5000 rows of 3001 bf16 values:
-// 12 and 8 us; with eight strided accesses per lane 12 and 43; as whole vectors between their
+// 11 and 8 us; with eight strided accesses per lane 12 and 43; as whole vectors between their
 // 16-byte boundaries 16 and 12).
 template <int DT, int U>
 __global__ void __launch_bounds__(32 * kQuantWarps)
