@@ -272,6 +272,12 @@ def _dtype(dt):
     return code
 
 
+def _check_codes(q, dims, name):
+    if q.dtype != torch.uint8 or q.dim() not in dims:
+        raise ValueError("%s must hold uint8 codes in %s dimensions: got %s %s" %
+                         (name, " or ".join(map(str, dims)), q.dtype, tuple(q.shape)))
+
+
 def moe_fp4_row_bytes(cols):
     """Bytes of the codes of one MXFP4 row of ``cols`` values."""
     return (cols + 127) // 128 * 64 if cols > 0 else 0
@@ -312,6 +318,7 @@ def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
 def moe_dequantize_rows_fp4(q, scales, cols, dtype=torch.bfloat16, stream=None):
     """The values of one MXFP4 matrix (q [rows, bytes]) or of a group of them
     (q [E, rows, bytes], scales [E, ...]) as a new tensor [..., rows, cols] of ``dtype``."""
+    _check_codes(q, (2, 3), "q")
     shape = q.shape
     groups, rows = (shape[0], shape[1]) if len(shape) == 3 else (1, shape[0])
     dt = _dtype(dtype)
@@ -345,6 +352,8 @@ def moe_gemm_fp4(aq, a_scales, bq, b_scales, out, K, counts=None, stream=None):
     bq [E, N, bytes] (or [N, bytes]).  ``counts`` (int32 device tensor [E]): expert e's rows
     start on a 128-row boundary after expert e - 1's; without it E is 1 (see include/moe.h)."""
     rows, N = out.shape
+    _check_codes(aq, (2,), "aq")
+    _check_codes(bq, (2, 3), "bq")
     ash, bsh = aq.shape, bq.shape
     E = bsh[0] if len(bsh) == 3 else 1
     kb = moe_fp4_row_bytes(K)
@@ -382,6 +391,8 @@ def moe_forward_few_fp4(x, logits, router, W1q, W3q, W2q, w1_scales, w3_scales, 
             W2q.shape != (E, d, moe_fp4_row_bytes(d_ff)) or logits.shape != (T, E) or \
             out.shape != (T, d) or (router is not None and router.shape != (E, d)):
         raise ValueError("the arguments' shapes do not fit one layer")
+    for w in (W1q, W3q, W2q):
+        _check_codes(w, (3,), "a weight")
     if x.dtype != torch.bfloat16 or out.dtype != torch.bfloat16 or \
             logits.dtype != torch.float32 or \
             (router is not None and router.dtype != torch.float32):

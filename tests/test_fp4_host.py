@@ -127,3 +127,42 @@ def test_python_refusals(lib):
         lib.moe_forward_few_fp4(b, torch.zeros(1, 3), None, w, w, w, s, s, s, 1, b, s)
     with pytest.raises(ValueError):
         lib.moe_forward_few_fp4(b.float(), torch.zeros(1, 2), None, w, w, w, s, s, s, 1, b, s)
+
+
+@pytest.fixture
+def calls(lib, monkeypatch):
+    """The library calls that a wrapper makes, none of which runs."""
+    made = []
+
+    class Recorder:
+        def __getattr__(self, name):
+            return lambda *a: made.append(name) or 0
+    monkeypatch.setattr(lib, "_lib", Recorder())
+    return made
+
+
+def test_codes_of_other_dimensions_or_types_are_refused(lib, calls):
+    """A row of codes taken for a matrix would have its bytes counted as rows: 3584 of them written
+    to an output of one."""
+    def u8(*shape):
+        return torch.zeros(shape, dtype=torch.uint8)
+    s, out = u8(1 << 18), torch.zeros(64, 4)
+    for q in (u8(3584), u8(1, 2, 2, 3584), u8(4, 3584).to(torch.int32), torch.zeros(4, 3584)):
+        with pytest.raises(ValueError, match="q must hold uint8 codes"):
+            lib.moe_dequantize_rows_fp4(q, s, 7168)
+    with pytest.raises(ValueError, match="q must hold uint8 codes"):
+        lib.moe_dequantize_rows_fp4(u8(64), u8(512), 128)
+    for a in (u8(64), u8(64, 1, 64), u8(64, 64).to(torch.int16)):
+        with pytest.raises(ValueError, match="aq must hold uint8 codes"):
+            lib.moe_gemm_fp4(a, s, u8(4, 64), s, out, 128)
+    for b in (u8(64), u8(2, 2, 4, 64), torch.zeros(4, 64)):
+        with pytest.raises(ValueError, match="bq must hold uint8 codes"):
+            lib.moe_gemm_fp4(u8(64, 64), s, b, s, out, 128)
+    x = torch.zeros(1, 128, dtype=torch.bfloat16)
+    w = u8(2, 128, 64)
+    for i in range(3):
+        ws = [w, w, w]
+        ws[i] = w.to(torch.float32)
+        with pytest.raises(ValueError, match="a weight must hold uint8 codes"):
+            lib.moe_forward_few_fp4(x, torch.zeros(1, 2), None, *ws, s, s, s, 1, x, s)
+    assert not calls
