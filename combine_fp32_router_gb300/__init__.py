@@ -243,8 +243,10 @@ _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _addr(t):
-    if not t.is_contiguous():
+def _addr(t, contiguous=True):
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    if contiguous and not t.is_contiguous():
         raise ValueError("tensor arguments must be contiguous")
     return t.data_ptr()
 
@@ -252,8 +254,6 @@ def _addr(t):
 def _raw_stream(stream, t):
     if stream is not None:
         return stream.cuda_stream
-    if not t.is_cuda:
-        raise ValueError("tensor arguments must be CUDA tensors")
     return _current_raw_stream(t.get_device())
 
 
@@ -308,8 +308,8 @@ def moe_quantize_rows_fp4(x, q=None, scales=None, stream=None):
         scales = _empty((sb,), torch.uint8, x.device, stream)
     elif _nbytes(scales) < sb or not scales.is_contiguous():
         raise ValueError("scales too small for %d x %d values, or not contiguous" % (rows, cols))
-    st = _lib.moe_quantize_rows_fp4(x.data_ptr(), dt, rows, cols, stride, q.data_ptr(),
-                                    scales.data_ptr(), _raw_stream(stream, x))
+    st = _lib.moe_quantize_rows_fp4(_addr(x, False), dt, rows, cols, stride, _addr(q, False),
+                                    _addr(scales, False), _raw_stream(stream, x))
     if st:
         raise MoeError(st, "moe_quantize_rows_fp4")
     return q, scales

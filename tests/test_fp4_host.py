@@ -166,3 +166,41 @@ def test_codes_of_other_dimensions_or_types_are_refused(lib, calls):
         with pytest.raises(ValueError, match="a weight must hold uint8 codes"):
             lib.moe_forward_few_fp4(x, torch.zeros(1, 2), None, *ws, s, s, s, 1, x, s)
     assert not calls
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_host_tensors_are_refused(lib, calls, monkeypatch, given):
+    """A host address never reaches a kernel, whichever argument it comes in and whether or not a
+    stream is given.  (Here the other arguments are host tensors that pass for device ones.)"""
+    class Stream:
+        cuda_stream = 0
+
+    class Device(torch.Tensor):
+        is_cuda = True
+    kw = dict(stream=Stream()) if given else {}
+    monkeypatch.setattr(lib, "_raw_stream", lambda stream, t: 0)
+    monkeypatch.setattr(lib, "_empty", lambda shape, dtype, device, stream: dev(shape, dtype))
+
+    def dev(shape, dtype=torch.uint8):
+        return torch.zeros(shape, dtype=dtype).as_subclass(Device)
+    bf, f32 = torch.bfloat16, torch.float32
+    w, s = ((2, 128, 64), torch.uint8), ((2048,), torch.uint8)
+    for f, args in (
+            (lambda x, q, s: lib.moe_quantize_rows_fp4(x, q, s, **kw),
+             [((4, 128), bf), ((4, 64), torch.uint8), s]),
+            (lambda q, s: lib.moe_dequantize_rows_fp4(q, s, 128, **kw), [((4, 64), torch.uint8), s]),
+            (lambda W: lib.moe_quantize_weights_fp4(W, **kw), [((2, 32, 32), bf)]),
+            (lambda a, sa, b, sb, o, c: lib.moe_gemm_fp4(a, sa, b, sb, o, 128, counts=c, **kw),
+             [((4, 64), torch.uint8), s, w, s, ((4, 128), f32), ((2,), torch.int32)]),
+            (lambda x, lg, r, a, b, c, sa, sb, sc, o, ws:
+             lib.moe_forward_few_fp4(x, lg, r, a, b, c, sa, sb, sc, 1, o, ws, **kw),
+             [((1, 128), bf), ((1, 2), f32), ((2, 128), f32), w, w, w, s, s, s, ((1, 128), bf),
+              ((1 << 20,), torch.uint8)])):
+        f(*(dev(*a) for a in args))
+        assert len(calls) == 1          # as it is: accepted
+        calls.clear()
+        for i in range(len(args)):
+            mixed = [torch.zeros(a[0], dtype=a[1]) if j == i else dev(*a) for j, a in enumerate(args)]
+            with pytest.raises(ValueError, match="must be CUDA tensors"):
+                f(*mixed)
+        assert not calls
