@@ -154,6 +154,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
   const int unit = blockIdx.x / C::kCtas, units = gridDim.x / C::kCtas;
   DevErr* err = &g_gemm_err;
+  // the peer arrives on a pair's barriers too: those waits acquire at cluster scope
+  const auto wait = [&](uint32_t bar, uint32_t parity, volatile int* ab, int site) {
+    if constexpr (PAIR) return mbar_wait_cluster(bar, parity, ab, err, site, p.wait_ns);
+    else return mbar_wait(bar, parity, ab, err, site, p.wait_ns);
+  };
+  const auto warp_wait = [&](uint32_t bar, uint32_t parity, int site) {
+    return __all_sync(0xFFFFFFFFu, wait(bar, parity, abort_flag, site)) != 0;
+  };
 
   if (threadIdx.x == 0) {
     for (uint32_t s = 0; s < S; ++s) {
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       // around them meets outputs that are not stored)
       const uint32_t aplace = (t.n0 % 128) * 128u;
       for (int ks = 0; ks < nks; ++ks) {
-        if (issued >= S) ok = warp_wait(empty(s), phase, abort_flag, err, 61, p.wait_ns);
+        if (issued >= S) ok = warp_wait(empty(s), phase, 61);
         if (!ok) break;
         const uint32_t st = base + s * C::kStageBytes, ssf = st + C::kABytes + C::kBBytes;
         const uint32_t bar = PAIR ? mapa_shared(full(s), 0) : full(s);
@@ -264,13 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     for (uint32_t tile = unit; ok && tile < tiles; tile += units, ++n) {
       const Tile t = decode<PAIR>(p, sh, tile);
       const uint32_t acc = n & 1, tacc = tmem + acc * C::kRows;
-      if (n >= 2 && !warp_wait(tempty(acc), (n / 2 - 1) & 1, abort_flag, err, 63, p.wait_ns)) break;
+      if (n >= 2 && !warp_wait(tempty(acc), (n / 2 - 1) & 1, 63)) break;
       tc_fence_after();
       // the block may start inside a scale tile (row 64 of it: column 2)
       const uint32_t sf_shift = (t.row0 % 128) / 32;
       const uint32_t idesc = idesc_mxf4(128 * C::kCtas, t.local * C::kCtas);
       for (int ks = 0; ks < nks; ++ks) {
-        ok = warp_wait(full(s), phase, abort_flag, err, 64, p.wait_ns);
+        ok = warp_wait(full(s), phase, 64);
         if (!ok) break;
         tc_fence_after();
         const uint32_t st = base + s * C::kStageBytes;
@@ -333,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     for (uint32_t tile = unit; tile < tiles; tile += units, ++n) {
       const Tile t = decode<PAIR>(p, sh, tile);
       const uint32_t acc = n & 1;
-      if (!mbar_wait(tfull(acc), (n / 2) & 1, abort_flag, err, 66, p.wait_ns)) break;
+      if (!wait(tfull(acc), (n / 2) & 1, abort_flag, 66)) break;
       tc_fence_after();
       const uint32_t tacc = tmem + acc * C::kRows + (static_cast<uint32_t>(32 * q) << 16);
       const int col0 = t.n0 / 128 * 128 + 128 * rank + 32 * q;  // this warp's 32 output columns
@@ -414,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
       const uint32_t s = f % S;
       if (f >= issued) mbar_arrive_expect_tx(full(s), sh.peer_tx[s]);
       else if (f >= peer) mbar_complete_tx(full(s), sh.tx[s]);
-      mbar_wait(full(s), (f / S) & 1, nullptr, err, 62, p.wait_ns);
+      wait(full(s), (f / S) & 1, nullptr, 62);
     }
   }
   if constexpr (PAIR) {

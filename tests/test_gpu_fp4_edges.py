@@ -1,0 +1,38 @@
+"""The 4-bit operators at their edges on the GPU: repeated runs, values that are not finite, wide
+layers, matrices of more than 2^31 values, and what the few-token layer keeps of its activations."""
+import pytest
+import torch
+
+import fp4_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import combine_fp32_router_gb300 as m
+    return m
+
+
+def gen(seed):
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+# ------------------------------------------------------------------------- product
+@pytest.mark.parametrize("rows,N,K", [(4000, 4096, 640), (2049, 2048, 3000)])
+def test_pairs_repeat_bit_for_bit(moe, rows, N, K):
+    """Products on CTA pairs, whose waits see the peer's arrivals: twenty runs, one after the other,
+    give the bits of the first."""
+    aq, sa = moe.moe_quantize_rows_fp4(torch.randn(rows, K, generator=gen(1), device=DEV))
+    bq, sb = moe.moe_quantize_weights_fp4(
+        torch.randn(1, K, N, generator=gen(2), device=DEV).to(torch.bfloat16))
+    outs = [torch.empty(rows, N, device=DEV) for _ in range(20)]
+    for o in outs:
+        moe.moe_gemm_fp4(aq, sa, bq, sb, o, K)
+    assert moe.moe_gemm_fp4_get_error() == moe.MOE_OK
+    av, bv = ref.values(aq, sa, rows, K), ref.values(bq[0], sb[0], N, K)
+    bound = (K + 8) * 2.0 ** -23 * (av.abs() @ bv.abs().t())
+    assert ref.within(outs[0], av @ bv.t(), bound)
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
