@@ -69,6 +69,7 @@ struct Params {
   int vec;  // output rows start on 16 bytes
   void* out;
   uint64_t wait_ns;
+  uint32_t withhold;  // test hook: bit 0, 1: CTA 0, 1 loads nothing
   CUtensorMap mapA, mapSa;          // weight codes (boxes of 128 rows) and scale tiles
   CUtensorMap mapB[kBoxes], mapSb;  // activation codes and scale tiles
 };
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
 
   if (warp == 0) {
     uint32_t s = 0, phase = 1;
-    bool ok = true;
+    bool ok = blockIdx.x > 1 || ((p.withhold >> blockIdx.x) & 1u) == 0u;
     const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
       if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, x, y);
       else tma_load_2d(dst, m, bar, x, y);
@@ -341,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
     for (uint32_t tile = unit; tile < tiles; tile += units, ++n) {
       const Tile t = decode<PAIR>(p, sh, tile);
       const uint32_t acc = n & 1;
-      if (!wait(tfull(acc), (n / 2) & 1, abort_flag, 66)) break;
+      // one answer for the warp: the tcgen05.ld below is .sync.aligned
+      if (!warp_wait(tfull(acc), (n / 2) & 1, 66)) break;
       tc_fence_after();
       const uint32_t tacc = tmem + acc * C::kRows + (static_cast<uint32_t>(32 * q) << 16);
       const int col0 = t.n0 / 128 * 128 + 128 * rank + 32 * q;  // this warp's 32 output columns
@@ -586,6 +588,7 @@ moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t row
   p.vec = N % 8 == 0;
   p.out = out;
   p.wait_ns = wait_limit_ns();
+  p.withhold = withheld_loaders();
   const int sms = num_sms_of_current_device();
   const cudaError_t st =
       use_pairs(rows, N, E, counts != nullptr, sms)

@@ -33,9 +33,11 @@ struct WsLayout {
 };
 
 // SM count of the current device (152 if it cannot be read), and the limit of device-side
-// waits that moe_set_wait_timeout_ns set.
+// waits that moe_set_wait_timeout_ns set, and the loaders that moe_debug_set_flags stops in the
+// 4-bit kernels (flag bits 0 and 2 as bits 0 and 1).
 int num_sms_of_current_device();
 uint64_t wait_limit_ns();
+uint32_t withheld_loaders();
 
 WsLayout make_layout(int64_t T, int d, int E, int k, int dff);
 

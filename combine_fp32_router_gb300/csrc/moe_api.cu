@@ -177,6 +177,11 @@ int num_sms_of_current_device() {
 
 uint64_t wait_limit_ns() { return g_wait_ns.load(); }
 
+uint32_t withheld_loaders() {
+  const uint32_t f = static_cast<uint32_t>(g_debug_flags.load());
+  return (f & 1u) | ((f >> 1) & 2u);
+}
+
 namespace {
 
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
