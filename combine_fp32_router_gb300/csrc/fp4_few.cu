@@ -729,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qd = warp & 3;             // rows 32 qd .. of the tile
     const uint32_t acc = (warp >> 2) - 1;  // this group's accumulator
     for (uint32_t i = 0;; ++i) {
-      if (!mbar_wait(tfull(acc), i & 1, abort_flag, p.err, 76, p.wait_ns)) break;
+      // one answer for the warp: the tcgen05.ld below is .sync.aligned
+      if (!warp_wait(tfull(acc), i & 1, abort_flag, p.err, 76, p.wait_ns)) break;
       const Unit un = sh.acc_unit[acc];
       if (un.kind == 0) break;
       if (un.kind == 3) {
