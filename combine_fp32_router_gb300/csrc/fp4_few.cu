@@ -310,6 +310,7 @@ struct ExpertParams {
   int32_t *ticket, *done1, *xdone;
   DevErr* err;
   uint64_t wait_ns;
+  uint32_t withhold;  // test hook, CTA 0: bit 0 no weights are loaded, bit 1 no activations
   // codes of W1, W3, W2 (boxes of 128 rows) and of x and h terms (boxes of n rows), 128 bytes
   // wide; where rows are whole numbers of 128-byte pieces (wide) a box holds two of them
   CUtensorMap map1, map3, map2, mapx, maph;
@@ -346,6 +347,9 @@ struct Shared {
   int32_t groups, ticket;
   int32_t abort_flag;
   uint32_t tmem;
+  // fills of the ring: given out by the weights' loader, joined by the activations', and landed
+  // before their MMAs
+  uint32_t given, joined, landed;
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
@@ -444,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(drain, 1);
     fence_mbar_init();
     sh.abort_flag = 0;
+    sh.given = sh.joined = sh.landed = 0u;
     tma_prefetch_desc(&p.map1);
     tma_prefetch_desc(&p.map3);
     tma_prefetch_desc(&p.map2);
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
     uint32_t it = 0, s = 0, phase = 1;
-    bool ok = true;
+    bool ok = !(blockIdx.x == 0 && (p.withhold & 1u));
     while (ok) {
       const int u = __shfl_sync(0xFFFFFFFFu, next, 0);
       const bool work = u < n_units;
@@ -594,20 +599,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!work) break;
     }
-    // copies still in flight land before the CTA ends
-    if (*abort_flag)
-      for (uint32_t i = it > S ? it - S : 0; i < it; ++i)
-        mbar_wait(full(i % S), (i / S) & 1, nullptr, p.err, 72, p.wait_ns);
+    if (lane == 0) sh.given = it;
   } else if (warp == 3) {
     // ---------------------------------------------------------------- loads of activations
     // apart from the weights' so that those run ahead while an h is not there yet
-    uint32_t s = 0, phase = 0;
+    uint32_t it = 0, s = 0, phase = 0;
     const uint32_t bbytes = p.n * 128u;
-    while (warp_wait(told(s), phase, abort_flag, p.err, 77, p.wait_ns)) {
+    const bool stop = blockIdx.x == 0 && (p.withhold & 2u);
+    while (!stop && warp_wait(told(s), phase, abort_flag, p.err, 77, p.wait_ns)) {
       const StageMeta m = sh.meta[s];
       if (m.u.kind == 0 || m.u.kind == 3) {  // nothing to load
         if (elect_one()) mbar_arrive(full(s));
         __syncwarp();
+        ++it;
         if (m.u.kind == 0) break;
         if (++s == S) {
           s = 0;
@@ -645,17 +649,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_load(ssb, sfb, m.nkt * kMxTileBytes, full(s));
       }
       __syncwarp();
+      ++it;
       if (++s == S) {
         s = 0;
         phase ^= 1;
       }
     }
+    if (lane == 0) sh.joined = it;
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
-    uint32_t s = 0, phase = 0, units = 0;
+    uint32_t it = 0, s = 0, phase = 0, units = 0;
     const uint32_t idesc = idesc_mxf4(128, p.n);
     const uint32_t bbytes = p.n * 128u;
     while (warp_wait(full(s), phase, abort_flag, p.err, 73, p.wait_ns)) {
+      ++it;
       tc_fence_after();
       const StageMeta m = sh.meta[s];
       if (m.u.kind == 0) {  // no more work: every group gets that as its next unit
@@ -722,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+    if (lane == 0) sh.landed = it;
     if (elect_one()) umma_commit(drain);  // every MMA issued is complete before TMEM is freed
     mbar_wait(drain, 0, nullptr, p.err, 75, p.wait_ns);
   } else if (warp >= 4) {
@@ -839,6 +847,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  // After an abort copies may still be in flight: they land before the CTA ends.  At most a ring of
+  // fills (a slot is given out again only after its fill landed); where the activations' loader
+  // left before it joined one, its arrival is made up for.
+  if (threadIdx.x == 0)
+    for (uint32_t f = sh.landed; f < sh.given; ++f) {
+      if (f >= sh.joined) mbar_arrive(full(f % S));
+      mbar_wait(full(f % S), (f / S) & 1, nullptr, p.err, 72, p.wait_ns);
+    }
   if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -967,6 +983,7 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   p.xdone = ints(L.xdone);
   p.err = r.err;
   p.wait_ns = wait_limit_ns();
+  p.withhold = withheld_loaders();
   p.wide1 = d % 256 == 0;
   p.wide2 = d_ff % 256 == 0;
   const uint64_t rows = static_cast<uint64_t>(L.cols) * kTerms, groups = static_cast<uint64_t>(L.groups);

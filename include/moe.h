@@ -504,7 +504,8 @@ void moe_set_wait_timeout_ns(uint64_t ns);
  * the timeout path on a tiny problem with a short timeout).  Bit 1: moe_forward dispatches
  * batches of T <= 128 with the multi-kernel sequence of larger batches instead of its
  * single launch (both give bitwise the same workspace contents and output).  Bits 0 and 2: the
- * first and the second CTA of moe_gemm_fp4 load nothing, so that its waits run out. */
+ * first and the second CTA of moe_gemm_fp4 load nothing; the first of moe_forward_few_fp4 loads no
+ * weights and no activations, so that their waits run out. */
 void moe_debug_set_flags(int flags);
 
 /* Short English description of a status code. */

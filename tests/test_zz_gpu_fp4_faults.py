@@ -51,3 +51,32 @@ def test_product_times_out_and_recovers(moe, rows, N, K, out_dtype, flags):
     moe.moe_gemm_fp4(aq, sa, bq, sb, out, K)
     assert moe.moe_gemm_fp4_get_error() == moe.MOE_OK
     assert torch.equal(out, want)
+
+
+# tokens as columns, gathered tokens, rows that are odd numbers of 128-byte pieces; more stages than
+# the ring has, one stage
+@pytest.mark.parametrize("T,d,E,k,dff", [(1, 4096, 8, 4, 512), (4, 384, 16, 3, 128),
+                                         (16, 2048, 8, 3, 1024), (32, 128, 4, 2, 128)])
+@pytest.mark.parametrize("router", [False, True])
+@pytest.mark.parametrize("flags", [1, 4, 5])
+def test_few_tokens_time_out_and_recover(moe, T, d, E, k, dff, router, flags):
+    x = torch.randn(T, d, generator=gen(3), device=DEV).to(torch.bfloat16)
+    W = [moe.moe_quantize_weights_fp4((torch.randn(E, a, b, generator=gen(4 + i), device=DEV) /
+                                       a ** 0.5).to(torch.bfloat16))
+         for i, (a, b) in enumerate([(d, dff), (d, dff), (dff, d)])]
+    logits = torch.randn(T, E, generator=gen(7), device=DEV)
+    R = torch.randn(E, d, generator=gen(8), device=DEV) / d ** 0.5 if router else None
+    ws = torch.empty(moe.moe_few_workspace_bytes(T, d, E, k, dff), dtype=torch.uint8, device=DEV)
+    want, out = torch.empty_like(x), torch.empty_like(x)
+
+    def run(o):
+        moe.moe_forward_few_fp4(x, logits, R, W[0][0], W[1][0], W[2][0], W[0][1], W[1][1], W[2][1],
+                                k, o, ws)
+    run(want)
+    assert moe.moe_get_error(ws) == moe.MOE_OK
+    with stopped(moe, flags):
+        run(out)
+    assert moe.moe_get_error(ws) == moe.MOE_ERR_TIMEOUT
+    run(out)
+    assert moe.moe_get_error(ws) == moe.MOE_OK
+    assert torch.equal(out, want)
