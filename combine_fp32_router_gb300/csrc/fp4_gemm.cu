@@ -36,6 +36,10 @@ namespace {
 // fit the rows): first error since moe_gemm_fp4_get_error last read it.
 __device__ DevErr g_gemm_err;
 
+// Reads and clears it in one step: an error that comes between the two would be lost.
+__device__ int g_taken_status;
+__global__ void take_error_kernel() { g_taken_status = atomicExch(&g_gemm_err.status, 0); }
+
 template <bool PAIR>
 struct Cfg {
   static constexpr int kRows = PAIR ? 192 : 128;  // N of a tile
@@ -599,11 +603,16 @@ moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t row
 
 moe_status_t moe_gemm_fp4_get_error(cudaStream_t stream) {
   if (cudaStreamSynchronize(stream) != cudaSuccess) return MOE_ERR_CUDA;
-  DevErr e = {}, none = {};
-  if (cudaMemcpyFromSymbol(&e, g_gemm_err, sizeof(e)) != cudaSuccess) return MOE_ERR_CUDA;
-  if (e.status != 0 && cudaMemcpyToSymbol(g_gemm_err, &none, sizeof(none)) != cudaSuccess)
+  static std::mutex m;  // g_taken_status is one caller's at a time
+  const std::lock_guard<std::mutex> lock(m);
+  int status = 0;
+  if (cudaLaunchKernel(reinterpret_cast<const void*>(take_error_kernel), dim3(1), dim3(1), nullptr, 0,
+                       stream) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&status, g_taken_status, sizeof(status), 0, cudaMemcpyDeviceToHost,
+                                stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
     return MOE_ERR_CUDA;
-  return static_cast<moe_status_t>(e.status);
+  return static_cast<moe_status_t>(status);
 }
 
 }  // extern "C"

@@ -348,7 +348,8 @@ moe_status_t moe_quantize_weights_fp4(const moe_bf16_t* W, int E, int K, int N, 
  * Counts that are negative or do not fit `rows` record MOE_ERR_DEVICE_BOUNDS and nothing is
  * written; device-side problems are read with moe_gemm_fp4_get_error, which synchronises
  * `stream`, returns the first one recorded on the current device since the last call, and clears
- * it.
+ * it in the same step.  The record is the device's: products on other streams share it, and of
+ * several callers one gets an error.
  */
 moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t rows,
                           const int32_t* counts, const uint8_t* b, const uint8_t* b_scales, int E,

@@ -36,3 +36,37 @@ def test_pairs_repeat_bit_for_bit(moe, rows, N, K):
     assert ref.within(outs[0], av @ bv.t(), bound)
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+def test_an_error_is_taken_by_one_caller(moe):
+    """Callers that read the record at once: one of them gets the error, the record is clear then."""
+    import threading
+    aq, sa = moe.moe_quantize_rows_fp4(torch.randn(128, 128, generator=gen(3), device=DEV))
+    bq, sb = moe.moe_quantize_weights_fp4(
+        torch.randn(2, 128, 128, generator=gen(4), device=DEV).to(torch.bfloat16))
+    out = torch.empty(128, 128, device=DEV)
+    bad = torch.tensor([128, 1], dtype=torch.int32, device=DEV)
+    n, rounds = 8, 40
+    streams = [torch.cuda.Stream() for _ in range(n)]
+    barrier = threading.Barrier(n + 1)
+    got = [[] for _ in range(n)]
+
+    def reader(i):
+        for _ in range(rounds):
+            barrier.wait()
+            got[i].append(moe.moe_gemm_fp4_get_error(streams[i]))
+            barrier.wait()
+    threads = [threading.Thread(target=reader, args=(i,), daemon=True) for i in range(n)]
+    for t in threads:
+        t.start()
+    for _ in range(rounds):
+        moe.moe_gemm_fp4(aq, sa, bq, sb, out, 128, counts=bad)
+        torch.cuda.synchronize()
+        barrier.wait(60)
+        barrier.wait(60)
+    for t in threads:
+        t.join(60)
+    for r in range(rounds):
+        statuses = sorted(g[r] for g in got)
+        assert statuses == [moe.MOE_OK] * (n - 1) + [moe.MOE_ERR_DEVICE_BOUNDS], r
+    assert moe.moe_gemm_fp4_get_error() == moe.MOE_OK
