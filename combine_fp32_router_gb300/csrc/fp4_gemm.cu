@@ -213,8 +213,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp4_kernel(const __grid_cons
         sh.first_block[e] = nb + b - b_own;
         sh.first_row[e] = (nr + r - r_own) * 128;
         sh.count[e] = c;
-        // the last row that is read has to exist (the padding after it need not)
-        bad |= static_cast<int64_t>(nr + r - r_own) * 128 + c > p.rows;
+        // the last row that is read has to exist (the padding after it need not, nor the place
+        // where an expert without rows would start)
+        bad |= c > 0 && static_cast<int64_t>(nr + r - r_own) * 128 + c > p.rows;
       }
       nb += __shfl_sync(0xFFFFFFFFu, b, 31);
       nr += __shfl_sync(0xFFFFFFFFu, r, 31);

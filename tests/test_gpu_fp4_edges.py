@@ -70,3 +70,32 @@ def test_an_error_is_taken_by_one_caller(moe):
         statuses = sorted(g[r] for g in got)
         assert statuses == [moe.MOE_OK] * (n - 1) + [moe.MOE_ERR_DEVICE_BOUNDS], r
     assert moe.moe_gemm_fp4_get_error() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("counts", [[133], [133, 0, 0], [0, 133, 0], [128, 5] + [0] * 40, [5, 200, 0],
+                                    [3000, 1500, 0, 0]])
+def test_rows_may_end_with_the_last_segment(moe, counts):
+    """Rows that stop where the last expert's do, with no padding for the experts after it that have
+    none; one row fewer does not hold the segments."""
+    E, N, K = len(counts), 1024, 256
+    last = max(e for e in range(E) if counts[e])
+    rows = sum(ref.up(c, 128) for c in counts[:last]) + counts[last]
+    aq, sa = moe.moe_quantize_rows_fp4(torch.randn(rows, K, generator=gen(60), device=DEV))
+    bq, sb = moe.moe_quantize_weights_fp4(
+        torch.randn(E, K, N, generator=gen(61), device=DEV).to(torch.bfloat16))
+    on_device = torch.tensor(counts, dtype=torch.int32, device=DEV)
+    out = torch.full((rows, N), 7.0, device=DEV)
+    moe.moe_gemm_fp4(aq, sa, bq, sb, out, K, counts=on_device)
+    assert moe.moe_gemm_fp4_get_error() == moe.MOE_OK
+    at = 0
+    for e, c in enumerate(counts):
+        if c:
+            alone = torch.empty(c, N, device=DEV)
+            q, s = moe.moe_quantize_rows_fp4(
+                moe.moe_dequantize_rows_fp4(aq, sa, K, torch.float32)[at:at + c])
+            moe.moe_gemm_fp4(q, s, bq[e], sb[e], alone, K)
+            assert torch.equal(out[at:at + c], alone)
+            assert bool((out[at + c:at + ref.up(c, 128)] == 7.0).all())
+        at += ref.up(c, 128)
+    moe.moe_gemm_fp4(aq, sa, bq, sb, out[:rows - 1], K, counts=on_device)
+    assert moe.moe_gemm_fp4_get_error() == moe.MOE_ERR_DEVICE_BOUNDS
