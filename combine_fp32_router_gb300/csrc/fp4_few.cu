@@ -168,8 +168,8 @@ constexpr int kRouterThreads = 256;
 // Every CTA clears its share of the counters and marks its share of the sums' places; the first
 // `conv` write x in MXFP4 terms; each of the next computes the logits of two experts for up to TB
 // tokens (blockIdx.y: which): warp w sums the 128-value pieces w, w + 8, ... of d, lanes then warps
-// are added in a fixed order.  Any others only mark.
-template <int TB>
+// are added in a fixed order, the same for every U.  Any others only mark.
+template <int TB, int U>
 __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams p) {
   griddep_wait();
   // the experts' kernel may take its places now; it waits for this one's results itself
@@ -244,7 +244,6 @@ __global__ void __launch_bounds__(kRouterThreads) few_router_kernel(RouterParams
   float acc[TB][kRouterExperts];
 #pragma unroll
   for (int t = 0; t < TB; ++t) acc[t][0] = acc[t][1] = 0.0f;
-  constexpr int U = 7;  // pieces of the router in flight
   for (int c0 = warp * 128; c0 < p.d; c0 += U * 1024) {
     float4 a[U], b[U];
 #pragma unroll
@@ -897,10 +896,15 @@ CUtensorMap make_piece_map(const void* base, uint64_t inner, uint64_t rows, uint
   return m;
 }
 
+// U pieces of 1024 values in flight: 4 for narrow routers, which would load tokens for pieces that
+// they do not have, 8 for wide ones, which would wait for a second round of loads.  A whole call with
+// U = 4 and 8, 256 experts of d_ff = 128, routers out of HBM: 8 tokens of d = 1024 14.07 and 14.26 us, of
+// 2560 15.97 and 16.25; one token of 4096 15.35 and 14.48, of 7168 17.50 and 16.08, of 12288 21.02 and
+// 18.62.
 template <int TB>
 cudaError_t launch_router(const RouterParams& p, int grid, cudaStream_t s) {
-  return launch_pdl(few_router_kernel<TB>, dim3(grid, p.router ? (p.T + TB - 1) / TB : 1),
-                    dim3(kRouterThreads), 0, s, p);
+  const auto kern = p.d < 4096 ? few_router_kernel<TB, 4> : few_router_kernel<TB, 8>;
+  return launch_pdl(kern, dim3(grid, p.router ? (p.T + TB - 1) / TB : 1), dim3(kRouterThreads), 0, s, p);
 }
 
 }  // namespace
@@ -995,11 +999,12 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   p.maph = make_piece_map(p.hq, d_ff / 2, groups * rows, p.n, p.wide2, &st);
   if (st != cudaSuccess) return MOE_ERR_CUDA;
 
+  const int sms = num_sms_of_current_device();
   const int64_t conv = T * ((d + kRouterThreads * 8 - 1) / (kRouterThreads * 8));
-  r.conv = static_cast<int>(conv < 152 ? conv : 152);
+  r.conv = static_cast<int>(conv < sms ? conv : sms);
   int rgrid = r.conv + (router ? (E + kRouterExperts - 1) / kRouterExperts : 0);
   const int64_t marking = r.n_places / (4 * kRouterThreads);  // CTAs of four stores a thread
-  if (rgrid < 2 * 152 && rgrid < marking) rgrid = static_cast<int>(marking < 2 * 152 ? marking : 2 * 152);
+  if (rgrid < 2 * sms && rgrid < marking) rgrid = static_cast<int>(marking < 2 * sms ? marking : 2 * sms);
   st = T <= 1   ? launch_router<1>(r, rgrid, stream)
        : T <= 4 ? launch_router<4>(r, rgrid, stream)
                 : launch_router<8>(r, rgrid, stream);
@@ -1017,7 +1022,6 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
   }
   const size_t smem = 1024 + static_cast<size_t>(p.stages) * p.stage_bytes + sizeof(Shared);
   const int64_t units = T * k * (d_ff / 128 * 2 * L.parts + d / 128) + T * (d / 128);
-  const int sms = num_sms_of_current_device();
   st = launch_pdl(few_experts_kernel, dim3(static_cast<unsigned>(units < sms ? units : sms)),
                   dim3(kThreads), smem, stream, p);
   return st == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

@@ -92,3 +92,60 @@ def few(x, logits, W1, W3, W2, k):
             mag[t] += g[j] * m
             err[t] += g[j] * (W2[e].abs() @ uh + (n + 16) * eps * m)
     return out, err + (k + 32) * eps * mag
+
+
+TERMS = 6                      # MXFP4 numbers that carry an activation of the few-token layer
+LEFT = 5.0 ** -TERMS           # of a block's largest value, at most, is what they leave
+
+
+def block_max(v):
+    """Largest magnitude of each value's block of 32 along the last dimension (whole blocks)."""
+    return v.abs().view(*v.shape[:-1], -1, 32).amax(-1, keepdim=True).expand(
+        *v.shape[:-1], -1, 32).reshape(v.shape)
+
+
+def in_terms(x, n=TERMS):
+    """What n MXFP4 numbers keep of x [.., multiples of 32] (float64): each the nearest to what the
+    ones before left, on the smallest power-of-two scale on which none exceeds 6."""
+    grid = torch.tensor(GRID, dtype=torch.float64, device=x.device)
+    left = x.double().clone()
+    for _ in range(n):
+        top = block_max(left).clamp(min=2.0 ** -120)
+        m, e = torch.frexp(top)                       # top = m 2^e, m in [.5, 1)
+        scale = torch.exp2((e - 3 + (m > 0.75)).double())
+        w = left.abs() / scale
+        k = torch.zeros_like(w, dtype=torch.int64)
+        for i, mid in enumerate((0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0)):
+            k += (w >= mid) if i % 2 else (w > mid)
+        left = left - grid[k] * scale * torch.sign(left)
+    return x.double() - left
+
+
+def few_in_terms(x, logits, W1, W3, W2, k):
+    """few(), with a bound that holds for activations carried as terms: what they leave of x and of
+    h is at most LEFT of a block's largest value."""
+    T, d = x.shape
+    x = x.double()
+    out, err = (torch.zeros(T, d, dtype=torch.float64, device=x.device) for _ in range(2))
+    eps = 2.0 ** -23
+    for t in range(T):
+        top, sel = torch.sort(logits[t].double(), descending=True, stable=True)
+        g = torch.softmax(top[:k], dim=0)
+        ux = LEFT * block_max(x[t])
+        mag = torch.zeros_like(out[t])
+        for j, e in enumerate(sel[:k].tolist()):
+            w1, w3, w2 = W1[e].abs(), W3[e].abs(), W2[e].abs()
+            a, b = W1[e] @ x[t], W3[e] @ x[t]
+            sg = torch.sigmoid(a)
+            h = a * sg * b
+            # fp32 sums of TERMS d products, in any order; silu' is at most 1.1
+            ua = (TERMS * d + 16) * eps * (w1 @ (x[t].abs() + ux)) + w1 @ ux
+            ub = (TERMS * d + 16) * eps * (w3 @ (x[t].abs() + ux)) + w3 @ ux
+            uh = 1.1 * ua * (b.abs() + ub) + (a * sg).abs() * ub + 16 * eps * h.abs()
+            uh = uh + LEFT * block_max(h.abs() + uh)
+            m = w2 @ (h.abs() + uh)
+            out[t] += g[j] * (W2[e] @ h)
+            err[t] += g[j] * (w2 @ uh + (TERMS * h.numel() + 16) * eps * m)
+            mag += g[j] * m
+        err[t] += (k + 32) * eps * mag
+    return out, err

@@ -99,3 +99,45 @@ def test_rows_may_end_with_the_last_segment(moe, counts):
         at += ref.up(c, 128)
     moe.moe_gemm_fp4(aq, sa, bq, sb, out[:rows - 1], K, counts=on_device)
     assert moe.moe_gemm_fp4_get_error() == moe.MOE_ERR_DEVICE_BOUNDS
+
+
+# ------------------------------------------------------------------------- few tokens
+def weights(moe, d, E, dff, seed):
+    return [moe.moe_quantize_weights_fp4((torch.randn(E, a, b, generator=gen(seed + i), device=DEV) /
+                                          a ** 0.5).to(torch.bfloat16))
+            for i, (a, b) in enumerate([(d, dff), (d, dff), (dff, d)])]
+
+
+def run_few(moe, x, logits, router, W, k):
+    T, d = x.shape
+    E, dff = W[0][0].shape[:2]
+    ws = torch.full((moe.moe_few_workspace_bytes(T, d, E, k, dff),), 255, dtype=torch.uint8,
+                    device=DEV)
+    out = torch.full((T, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    moe.moe_forward_few_fp4(x, logits, router, W[0][0], W[1][0], W[2][0], W[0][1], W[1][1],
+                            W[2][1], k, out, ws)
+    assert moe.moe_get_error(ws) == moe.MOE_OK
+    return out
+
+
+def dense(W, rows, cols):
+    return torch.stack([ref.values(q, s, rows, cols) for q, s in zip(*W)])
+
+
+# the widths of large layers, up to the largest; sums of more than eight K ranges (d > 8192); experts
+# with more than eight tokens
+@pytest.mark.parametrize("T,d,E,k,dff", [
+    (1, 7168, 4, 2, 256), (8, 4096, 5, 3, 384), (32, 7168, 8, 2, 128), (5, 8320, 2, 2, 128),
+    (16, 16384, 3, 2, 128), (2, 65536, 2, 1, 128), (3, 128, 2, 1, 65536), (9, 384, 3, 2, 8320)])
+def test_few_wide_layers(moe, T, d, E, k, dff):
+    x = torch.randn(T, d, generator=gen(20), device=DEV).to(torch.bfloat16)
+    W = weights(moe, d, E, dff, 21)
+    router = torch.randn(E, d, generator=gen(25), device=DEV) / d ** 0.5
+    logits = torch.full((T, E), float("nan"), device=DEV)
+    out = run_few(moe, x, logits, router, W, k)
+    want = x.double() @ router.double().t()
+    u = (d + 8) * 2.0 ** -24 * (x.double().abs() @ router.double().abs().t())
+    assert bool(((logits.double() - want).abs() <= u).all())
+    want, bound = ref.few_in_terms(x, logits, dense(W[0], dff, d), dense(W[1], dff, d),
+                                   dense(W[2], d, dff), k)
+    assert ref.within(out, want, bound)
