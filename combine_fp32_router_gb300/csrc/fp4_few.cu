@@ -3,7 +3,9 @@
 //                      counters cleared
 //   few_experts_kernel top-k and gates, both expert products with SwiGLU between, the combine
 //
-// Bound by reading the chosen experts' weights once, 17/32 byte a value.  The block-scaled
+// Bound by reading the chosen experts' weights, 17/32 byte a value, once for up to 8 tokens that
+// chose an expert (9 to 16 tokens read it twice, and so on: 32 tokens over 8 experts of d = 7168,
+// d_ff = 2048, top-2, met in 11.2 groups, 83.8 us; one reading each would be 27.7).  The block-scaled
 // tensor cores (tcgen05 kind::mxf4) take the weights as they lie in memory; the activations
 // have to be 4-bit operands too, so each is written as a sum of kTerms = 6 MXFP4 numbers, the
 // residual of each being quantised again: a term leaves at most 1/5 of its block's largest

@@ -16,10 +16,12 @@
 //   2      TMEM allocator, 3 the experts' first rows and blocks
 //   4..7   epilogue: accumulator column = output row, lane = output column
 // Bound, with full blocks of pairs, by the tensor pipe and the thread that feeds it: a stage of
-// 256 values of K takes some 540 cycles, 408 of them MMAs (8192 x 7168 x 7168: 131 us, 6.4
-// PFLOP/s; 128 x 192 tiles on single CTAs, which take in 43 KB for the same work, 175 us); with few
-// rows by the 128 weight rows that an MMA reads whatever it multiplies them with (70 cycles per 64
-// values of K: 3 rows of 4096 x 7168 10 us).
+// 256 values of K takes some 540 cycles, 408 of them MMAs (8192 x 7168 x 7168: 131 to 141 us by box
+// and clocks, 6.0 to 6.4 PFLOP/s; 128 x 192 tiles on single CTAs, which take in 43 KB for the same
+// work, 175 us); with few rows by the issuing thread: 3 rows of 4096 x 7168, 10.1 us, spend 16.8
+// thousand cycles in its loop, 3.6 of them waiting for loads, the others some 470 for each of 28
+// stages, of which 280 are MMAs (70 per 64 values of K, since an MMA reads 128 weight rows whatever
+// part of them is real).
 #include <cuda.h>
 
 #include <atomic>

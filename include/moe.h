@@ -357,8 +357,8 @@ moe_status_t moe_gemm_fp4(const uint8_t* a, const uint8_t* a_scales, int64_t row
 moe_status_t moe_gemm_fp4_get_error(cudaStream_t stream);
 
 /*
- * The whole layer for a few tokens (T <= 32) on 4-bit experts, in two launches, reading each
- * chosen expert's weights once:
+ * The whole layer for a few tokens (T <= 32) on 4-bit experts, in two launches, reading a chosen
+ * expert's weights once for every eight of its tokens (rounded up):
  *   logits = x router^T (fp32 products and sums), or given; top-k and gate as moe_forward;
  *   out_t = bf16( sum_j gate[t,j] * (h_tj W2[e_j]) ),  h_tj = silu(x_t W1[e_j]) * (x_t W3[e_j])
  * The weights enter as the values that their codes stand for.  x and h enter as sums of six
@@ -367,7 +367,8 @@ moe_status_t moe_gemm_fp4_get_error(cudaStream_t stream);
  * once.  A value of x that is not finite, or an h, makes its token's output NaN.
  *   x [T,d] bf16; router [E,d] fp32, or NULL; logits [T,E] fp32: written when router is given,
  *   read when it is NULL; W1q, W3q: E matrices of d_ff x d, W2q: of d x d_ff, with their scales
- *   (moe_quantize_weights_fp4 of the bf16 weights of moe_forward); out [T,d] bf16.
+ *   (moe_quantize_weights_fp4 of the bf16 weights of moe_forward); out [T,d] bf16.  W3q is
+ *   needed: there is no form for experts without the gate projection (moe_forward's W3 = NULL).
  *   ws: moe_few_workspace_bytes(T, d, E, k, d_ff) bytes (0 for unsupported sizes), 256-byte
  *   aligned, ordered between calls as for moe_forward; its error word is read with moe_get_error.
  * Sizes as moe_forward, with T <= 32, E * d < 2^31 and E * d_ff < 2^31.  T = 0 writes nothing.
