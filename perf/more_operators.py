@@ -51,7 +51,7 @@ def listed():
         # one token through a projection of the large layer: weight streaming
         dict(name="gemm_token", op="gemm", rows=1, N=4096, K=7168, E=1, out="bf16"),
         # ragged in every size, fp32 out
-        dict(name="gemm_ragged", op="gemm", rows=777, N=1545, K=2976, E=1, out="f32"),
+        dict(name="gemm_ragged", op="gemm", rows=777, N=1545, K=2700, E=1, out="f32"),
         # gate and up projections of the mid layer's experts, 24576 pairs over 64 experts with
         # unequal shares (some empty)
         dict(name="gemm_experts", op="gemm", rows=24576, N=2048, K=2048, E=64, out="bf16"),
