@@ -44,6 +44,11 @@ EXPORTS = ("moe_route_workspace_bytes", "moe_workspace_bytes", "moe_route_dispat
            "moe_fp4_row_bytes", "moe_fp4_scale_bytes", "moe_quantize_rows_fp4",
            "moe_dequantize_rows_fp4", "moe_quantize_weights_fp4", "moe_gemm_fp4",
            "moe_gemm_fp4_get_error", "moe_few_workspace_bytes", "moe_forward_few_fp4",
+           "moe_fp8_row_bytes", "moe_quantize_rows_fp8", "moe_dequantize_rows_fp8",
+           "moe_quantize_blocks_fp8", "moe_gemm_fp8", "moe_gemm_fp8_get_error", "moe_rmsnorm",
+           "moe_rmsnorm_workspace_bytes", "moe_rmsnorm_backward", "moe_sort_rows_bound",
+           "moe_sort_workspace_bytes", "moe_sort_tokens", "moe_sort_tokens_backward",
+           "moe_unsort_tokens", "moe_unsort_tokens_backward",
            "moe_ep_first_expert", "moe_ep_plan", "moe_ep_return_plan", "moe_ep_copy_rows",
            "moe_expert_workspace_bytes", "moe_expert_forward", "moe_combine",
            "moe_probe_dram_read", "moe_get_error", "moe_set_wait_timeout_ns",
@@ -111,6 +116,36 @@ def _load():
     lib.moe_few_workspace_bytes.restype = sz
     lib.moe_forward_few_fp4.argtypes = [p] * 9 + [i64, i, i, i, i, p, p, sz, p]
     lib.moe_forward_few_fp4.restype = i
+    lib.moe_fp8_row_bytes.argtypes = [i]
+    lib.moe_fp8_row_bytes.restype = i64
+    lib.moe_quantize_rows_fp8.argtypes = [p, i, i64, i, i64, i, p, p, p, p]
+    lib.moe_quantize_rows_fp8.restype = i
+    lib.moe_dequantize_rows_fp8.argtypes = [p, p, i64, i, i, p, p]
+    lib.moe_dequantize_rows_fp8.restype = i
+    lib.moe_quantize_blocks_fp8.argtypes = [p, i, i, i, i, p, p, p]
+    lib.moe_quantize_blocks_fp8.restype = i
+    lib.moe_gemm_fp8.argtypes = [p, p, i64, p, p, p, i, i, i, p, i, p]
+    lib.moe_gemm_fp8.restype = i
+    lib.moe_gemm_fp8_get_error.argtypes = [p]
+    lib.moe_gemm_fp8_get_error.restype = i
+    lib.moe_rmsnorm.argtypes = [p, i64, p, p, i, i, i64, i, ctypes.c_float, p, p, p, p, p, p]
+    lib.moe_rmsnorm.restype = i
+    lib.moe_rmsnorm_workspace_bytes.argtypes = [i64, i]
+    lib.moe_rmsnorm_workspace_bytes.restype = sz
+    lib.moe_rmsnorm_backward.argtypes = [p, p, p, p, p, i, i, i64, i, p, p, p, sz, p]
+    lib.moe_rmsnorm_backward.restype = i
+    lib.moe_sort_rows_bound.argtypes = [i64, i, i]
+    lib.moe_sort_rows_bound.restype = i64
+    lib.moe_sort_workspace_bytes.argtypes = [i64, i, i]
+    lib.moe_sort_workspace_bytes.restype = sz
+    lib.moe_sort_tokens.argtypes = [p, i64, p, i, p, i64, i, i, p, i64, p, p, p, p, p, sz, p]
+    lib.moe_sort_tokens.restype = i
+    lib.moe_sort_tokens_backward.argtypes = [p, i, i64, p, i64, i, i, p, p, p]
+    lib.moe_sort_tokens_backward.restype = i
+    lib.moe_unsort_tokens.argtypes = [p, i, i64, p, p, i64, i, i, p, p, p]
+    lib.moe_unsort_tokens.restype = i
+    lib.moe_unsort_tokens_backward.argtypes = [p, p, i, i64, p, p, i64, i, i, p, p, p, p]
+    lib.moe_unsort_tokens_backward.restype = i
     lib.moe_ep_first_expert.argtypes = [i, i, i]
     lib.moe_ep_first_expert.restype = i
     lib.moe_ep_plan.argtypes = [p, i, i, i, i, i, p, p, p, p, p]
@@ -406,6 +441,297 @@ def moe_forward_few_fp4(x, logits, router, W1q, W3q, W2q, w1_scales, w3_scales, 
                                     _addr(w2_scales), T, d, E, k, d_ff, _addr(out), _addr(ws),
                                     _nbytes(ws), _raw_stream(stream, x)),
            "moe_forward_few_fp4")
+
+
+# ---- 8-bit rows and weights with a scale per 128 values, the norm before the layer, tokens sorted
+# by expert and back.  These, too, run in a few microseconds.
+_F32, _I32 = torch.float32, torch.int32
+_CODES8 = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _device_of(t):
+    """The index of the tensor's device, which has to be the current one: the launches go there."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensor arguments must be CUDA tensors")
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors are on cuda:%d, which is not the current device" % dev)
+    return dev
+
+
+def _arg(t, dev, name, dtype, numel):
+    """Address of a contiguous tensor of `numel` values of `dtype` (a type or a tuple of types) on
+    device `dev`; None passes through."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
+    dt = t.dtype
+    if dt is not dtype and not (type(dtype) is tuple and dt in dtype):
+        raise ValueError("%s must hold %s: got %s" % (name, dtype, dt))
+    if t.numel() != numel or not t.is_contiguous():
+        raise ValueError("%s must hold %d values and be contiguous: got %s with strides %s" %
+                         (name, numel, tuple(t.shape), t.stride()))
+    return t.data_ptr()
+
+
+def _rows_of(x, name):
+    """(rows, cols, distance of rows) of a matrix whose rows may have a stride."""
+    if x.dim() != 2:
+        raise ValueError("%s must have two dimensions: got %s" % (name, tuple(x.shape)))
+    rows, cols = x.shape
+    stride, one = x.stride()
+    if one != 1 and cols > 1:
+        raise ValueError("the values of a row of %s must be contiguous" % name)
+    return rows, cols, (stride if rows > 1 else cols)
+
+
+def moe_fp8_row_bytes(cols):
+    """Bytes of the codes of one 8-bit row of ``cols`` values."""
+    return (cols + 127) // 128 * 128 if cols > 0 else 0
+
+
+def moe_quantize_rows_fp8(x, q=None, scales=None, swiglu=False, perm=None, stream=None):
+    """8-bit form of x [rows, cols] (bf16, fp16 or fp32; rows may have a stride): returns
+    (q [rows, moe_fp8_row_bytes(cols)] E4M3 codes as uint8, scales [rows, ceil(cols / 128)] fp32),
+    written into ``q`` (uint8 or float8_e4m3fn) and ``scales`` where they are given.  ``swiglu``:
+    x is [rows, 2 cols] = [a | b], and silu(a) * b is quantised.  ``perm`` (int32 [rows], as
+    moe_sort_tokens writes it): rows with perm < 0 are left as they were.  New outputs of this and
+    the calls below belong to the stream that writes them."""
+    rows, cols, stride = _rows_of(x, "x")
+    if swiglu:
+        if cols % 2:
+            raise ValueError("x must hold an even number of columns, a and b")
+        cols //= 2
+    dt = _dtype(x.dtype)
+    dev = _device_of(x)
+    kp = (cols + 127) // 128 * 128
+    if perm is not None and (q is None or scales is None):
+        raise ValueError("perm leaves rows as they were: q and scales must be given")
+    if q is None:
+        q = _empty((rows, kp), torch.uint8, x.device, stream)
+    if scales is None:
+        scales = _empty((rows, kp // 128), _F32, x.device, stream)
+    st = _lib.moe_quantize_rows_fp8(x.data_ptr(), dt, rows, cols, stride, 1 if swiglu else 0,
+                                    _arg(perm, dev, "perm", _I32, rows),
+                                    _arg(q, dev, "q", _CODES8, rows * kp),
+                                    _arg(scales, dev, "scales", _F32, rows * (kp // 128)),
+                                    _raw_stream(stream, x))
+    if st:
+        raise MoeError(st, "moe_quantize_rows_fp8")
+    return q, scales
+
+
+def moe_dequantize_rows_fp8(q, scales, cols, dtype=torch.bfloat16, stream=None):
+    """The values of 8-bit rows (q [rows, bytes], scales [rows, ceil(cols / 128)]) as a new tensor
+    [rows, cols] of ``dtype``."""
+    if q.dim() != 2 or cols < 1 or q.shape[1] != moe_fp8_row_bytes(cols):
+        raise ValueError("q does not hold rows of %d values" % cols)
+    rows = q.shape[0]
+    dt = _dtype(dtype)
+    dev = _device_of(q)
+    kp = q.shape[1]
+    qa = _arg(q, dev, "q", _CODES8, rows * kp)
+    sa = _arg(scales, dev, "scales", _F32, rows * (kp // 128))
+    out = _empty((rows, cols), dtype, q.device, stream)
+    st = _lib.moe_dequantize_rows_fp8(qa, sa, rows, cols, dt, out.data_ptr(),
+                                      _raw_stream(stream, q))
+    if st:
+        raise MoeError(st, "moe_dequantize_rows_fp8")
+    return out
+
+
+def moe_quantize_blocks_fp8(W, transpose=True, stream=None):
+    """8-bit form of expert weights W [E, K, N] bf16 in 128 x 128 blocks: returns
+    (Wq [E, N, moe_fp8_row_bytes(K)] uint8, scales [E, ceil(N / 128), ceil(K / 128)] fp32) for
+    products over K.  ``transpose=False``: (Wq [E, K, moe_fp8_row_bytes(N)], scales
+    [E, ceil(K / 128), ceil(N / 128)]), the same values for products over N (the gradient of a
+    product's rows)."""
+    if W.dim() != 3 or W.dtype != torch.bfloat16:
+        raise ValueError("W must be bfloat16 [E, K, N]: got %s %s" % (W.dtype, tuple(W.shape)))
+    E, K, N = W.shape
+    dev = _device_of(W)
+    a, b = (N, K) if transpose else (K, N)
+    w = _arg(W, dev, "W", torch.bfloat16, E * K * N)
+    Wq = _empty((E, a, moe_fp8_row_bytes(b)), torch.uint8, W.device, stream)
+    sc = _empty((E, (a + 127) // 128, (b + 127) // 128), _F32, W.device, stream)
+    _check(_lib.moe_quantize_blocks_fp8(w, E, K, N, 1 if transpose else 0, Wq.data_ptr(),
+                                        sc.data_ptr(), _raw_stream(stream, W)),
+           "moe_quantize_blocks_fp8")
+    return Wq, sc
+
+
+def moe_gemm_fp8(aq, a_scales, bq, b_scales, out, K, counts=None, stream=None):
+    """out [rows, N] (bf16 or fp32) = the product over K of 8-bit rows aq (at least ``rows`` of
+    them) and weights bq [E, N, bytes] (or [N, bytes]) with a scale per 128 x 128 block.
+    ``counts`` (int32 device tensor [E]): expert e's rows start on a 128-row boundary after expert
+    e - 1's; without it E is 1 (see include/moe.h)."""
+    if out.dim() != 2 or aq.dim() != 2 or bq.dim() not in (2, 3) or K < 1:
+        raise ValueError("aq and out have two dimensions, bq two or three")
+    rows, N = out.shape
+    ash, bsh = aq.shape, bq.shape
+    E = bsh[0] if len(bsh) == 3 else 1
+    kb = (K + 127) // 128 * 128
+    if ash[1] != kb or bsh[-1] != kb or ash[0] < rows or bsh[-2] != N:
+        raise ValueError("aq, bq and out do not fit one product over %d values" % K)
+    dt = _dtype(out.dtype)
+    dev = _device_of(out)
+    st = _lib.moe_gemm_fp8(_arg(aq, dev, "aq", _CODES8, ash[0] * kb),
+                           _arg(a_scales, dev, "a_scales", _F32, ash[0] * (kb // 128)), rows,
+                           _arg(counts, dev, "counts", _I32, E),
+                           _arg(bq, dev, "bq", _CODES8, E * N * kb),
+                           _arg(b_scales, dev, "b_scales", _F32, E * ((N + 127) // 128) * (kb // 128)),
+                           E, N, K, _arg(out, dev, "out", out.dtype, rows * N), dt,
+                           _raw_stream(stream, out))
+    if st:
+        raise MoeError(st, "moe_gemm_fp8")
+
+
+def moe_gemm_fp8_get_error(stream=None):
+    """Synchronise the stream; the first device-side problem that moe_gemm_fp8 recorded on the
+    current device since the last call (cleared by it)."""
+    return int(_lib.moe_gemm_fp8_get_error(_stream(stream)))
+
+
+def moe_rmsnorm(x, weight, eps, residual=None, sum_out=None, out=None, q=None, scales=None,
+                rstd=None, stream=None):
+    """Root-mean-square norm of the rows of x [rows, cols] (bf16, fp16 or fp32; rows may have a
+    stride) times weight [cols] (x's type or fp32), into ``out`` [rows, cols] of x's type and / or
+    ``q`` and ``scales`` (as moe_quantize_rows_fp8).  ``residual`` [rows, cols]: x + residual is
+    normalised and written to ``sum_out`` (which may be ``residual`` itself).  ``rstd`` [rows]
+    fp32: kept for moe_rmsnorm_backward."""
+    rows, cols, stride = _rows_of(x, "x")
+    xt, n, dev = x.dtype, rows * cols, _device_of(x)
+    dt = _dtype(xt)
+    kp = (cols + 127) // 128 * 128
+    wt = weight.dtype
+    st = _lib.moe_rmsnorm(x.data_ptr(), stride, _arg(residual, dev, "residual", xt, n),
+                          _arg(weight, dev, "weight", (xt, _F32), cols), dt,
+                          2 if wt is _F32 else dt, rows, cols, eps,
+                          _arg(sum_out, dev, "sum_out", xt, n), _arg(out, dev, "out", xt, n),
+                          _arg(q, dev, "q", _CODES8, rows * kp),
+                          _arg(scales, dev, "scales", _F32, rows * (kp // 128)),
+                          _arg(rstd, dev, "rstd", _F32, rows), _raw_stream(stream, x))
+    if st:
+        raise MoeError(st, "moe_rmsnorm")
+
+
+def moe_rmsnorm_workspace_bytes(rows, cols):
+    return int(_lib.moe_rmsnorm_workspace_bytes(rows, cols))
+
+
+def moe_rmsnorm_backward(dy, s, weight, rstd, dx, dweight, ws, dsum=None, stream=None):
+    """Gradient of moe_rmsnorm: dx [rows, cols] (of x and of residual alike) and dweight [cols]
+    fp32 (or None) for dy [rows, cols], with s the normalised rows (sum_out, or x without a
+    residual) and rstd from the forward.  ``dsum``: a gradient that arrives at sum_out, added to
+    dx.  ``ws``: moe_rmsnorm_workspace_bytes(rows, cols) bytes."""
+    if dy.dim() != 2:
+        raise ValueError("dy must have two dimensions: got %s" % (tuple(dy.shape),))
+    rows, cols = dy.shape
+    t, n, dev = dy.dtype, rows * cols, _device_of(dy)
+    dt = _dtype(t)
+    wt = weight.dtype
+    wsa, wsb = (None, 0) if ws is None else (_addr(ws), _nbytes(ws))
+    st = _lib.moe_rmsnorm_backward(_arg(dy, dev, "dy", t, n), _arg(s, dev, "s", t, n),
+                                   _arg(weight, dev, "weight", (t, _F32), cols),
+                                   _arg(rstd, dev, "rstd", _F32, rows),
+                                   _arg(dsum, dev, "dsum", t, n), dt, 2 if wt is _F32 else dt,
+                                   rows, cols, _arg(dx, dev, "dx", t, n),
+                                   _arg(dweight, dev, "dweight", _F32, cols), wsa, wsb,
+                                   _raw_stream(stream, dy))
+    if st:
+        raise MoeError(st, "moe_rmsnorm_backward")
+
+
+def moe_sort_rows_bound(T, k, E):
+    """Rows that T * k pairs can take in 128-row segments of E experts."""
+    return int(_lib.moe_sort_rows_bound(T, k, E))
+
+
+def moe_sort_workspace_bytes(T, E, k):
+    return int(_lib.moe_sort_workspace_bytes(T, E, k))
+
+
+def moe_sort_tokens(x, topk_idx, rows, counts, perm, pos, ws, x_scales=None, rows_scales=None,
+                    stream=None):
+    """The rows of x [T, d] (any type; 8-bit rows with x_scales [T, n] fp32) by expert: pair (t, j)
+    with topk_idx[t, j] = e (int32 [T, k]; -1: no expert) goes to row pos[t, j] of ``rows``
+    [n_rows, d], n_rows >= moe_sort_rows_bound(T, k, E), its scales to ``rows_scales``; counts [E],
+    perm [n_rows] (the pair of a row, -1 for none) and pos [T, k] are int32.  Rows without a pair
+    are left as they were."""
+    if x.dim() != 2 or topk_idx.dim() != 2 or rows.dim() != 2 or rows.shape[1] != x.shape[1] or \
+            topk_idx.shape[0] != x.shape[0]:
+        raise ValueError("x [T, d], topk_idx [T, k] and rows [n_rows, d] do not fit each other")
+    T, d = x.shape
+    k, E, n_rows = topk_idx.shape[1], counts.numel(), rows.shape[0]
+    xt, dev = x.dtype, _device_of(x)
+    ns = 0
+    if x_scales is not None:
+        if x_scales.dim() != 2:
+            raise ValueError("x_scales must have two dimensions")
+        ns = x_scales.shape[1]
+    st = _lib.moe_sort_tokens(_arg(x, dev, "x", xt, T * d), d * x.element_size(),
+                              _arg(x_scales, dev, "x_scales", _F32, T * ns), ns,
+                              _arg(topk_idx, dev, "topk_idx", _I32, T * k), T, k, E,
+                              _arg(rows, dev, "rows", xt, n_rows * d), n_rows,
+                              _arg(rows_scales, dev, "rows_scales", _F32, n_rows * ns),
+                              _arg(counts, dev, "counts", _I32, E),
+                              _arg(perm, dev, "perm", _I32, n_rows),
+                              _arg(pos, dev, "pos", _I32, T * k), _addr(ws), _nbytes(ws),
+                              _raw_stream(stream, x))
+    if st:
+        raise MoeError(st, "moe_sort_tokens")
+
+
+def _pairs(rows, pos, name):
+    if rows.dim() != 2 or pos.dim() != 2:
+        raise ValueError("%s and pos must have two dimensions" % name)
+    return rows.shape[0], rows.shape[1], pos.shape[0], pos.shape[1]
+
+
+def moe_sort_tokens_backward(drows, pos, dx, err_word, stream=None):
+    """Gradient of moe_sort_tokens: dx [T, d] = sum over the pairs of a token of drows[pos]."""
+    n_rows, d, T, k = _pairs(drows, pos, "drows")
+    t, dev = drows.dtype, _device_of(drows)
+    st = _lib.moe_sort_tokens_backward(_arg(drows, dev, "drows", t, n_rows * d), _dtype(t), n_rows,
+                                       _arg(pos, dev, "pos", _I32, T * k), T, k, d,
+                                       _arg(dx, dev, "dx", t, T * d), _addr(err_word),
+                                       _raw_stream(stream, drows))
+    if st:
+        raise MoeError(st, "moe_sort_tokens_backward")
+
+
+def moe_unsort_tokens(rows, gate, pos, out, err_word, stream=None):
+    """out [T, d] = sum over j of gate[t, j] (fp32 [T, k], or None for ones) times
+    rows[pos[t, j]], in the type of ``rows`` (bf16, fp16 or fp32); a pair with pos -1 adds nothing.
+    ``err_word``: 16 bytes or more of device memory that starts as a workspace of
+    moe_sort_tokens does (see include/moe.h)."""
+    n_rows, d, T, k = _pairs(rows, pos, "rows")
+    t, dev = rows.dtype, _device_of(rows)
+    st = _lib.moe_unsort_tokens(_arg(rows, dev, "rows", t, n_rows * d), _dtype(t), n_rows,
+                                _arg(gate, dev, "gate", _F32, T * k),
+                                _arg(pos, dev, "pos", _I32, T * k), T, k, d,
+                                _arg(out, dev, "out", t, T * d), _addr(err_word),
+                                _raw_stream(stream, rows))
+    if st:
+        raise MoeError(st, "moe_unsort_tokens")
+
+
+def moe_unsort_tokens_backward(dout, rows, gate, pos, drows, dgate, err_word, stream=None):
+    """Gradient of moe_unsort_tokens: drows[pos[t, j]] = gate[t, j] * dout[t] (rows without a pair
+    are left as they were) and dgate [T, k] fp32 = <rows[pos[t, j]], dout[t]> (0 for pairs without
+    a row; None, with ``rows`` None, to leave it out)."""
+    n_rows, d, T, k = _pairs(drows, pos, "drows")
+    t, dev = dout.dtype, _device_of(dout)
+    st = _lib.moe_unsort_tokens_backward(_arg(dout, dev, "dout", t, T * d),
+                                         _arg(rows, dev, "rows", t, n_rows * d), _dtype(t), n_rows,
+                                         _arg(gate, dev, "gate", _F32, T * k),
+                                         _arg(pos, dev, "pos", _I32, T * k), T, k, d,
+                                         _arg(drows, dev, "drows", t, n_rows * d),
+                                         _arg(dgate, dev, "dgate", _F32, T * k), _addr(err_word),
+                                         _raw_stream(stream, dout))
+    if st:
+        raise MoeError(st, "moe_unsort_tokens_backward")
 
 
 class ForwardGraph:

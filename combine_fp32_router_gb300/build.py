@@ -16,7 +16,8 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 
 SOURCES = ["route.cu", "gemm_fwd.cu", "gemm_bwd.cu", "moe_api.cu", "route_noalloc.cu", "ep.cu", "probe.cu",
-           "fp4_quant.cu", "fp4_gemm.cu", "fp4_few.cu"]
+           "fp4_quant.cu", "fp4_gemm.cu", "fp4_few.cu",
+           "norm.cu", "fp8_quant.cu", "fp8_gemm.cu", "sort.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
          "-I", os.path.join(ROOT, "include"), "-I", CSRC]

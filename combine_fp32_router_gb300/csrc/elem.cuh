@@ -1,0 +1,57 @@
+// Element types of the row kernels (MOE_DTYPE_*), and eight values of a row at a time.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace moe {
+
+// A value in fp32 and back (rounded to nearest, ties to even).
+template <int DT>
+struct In;
+template <>
+struct In<MOE_DTYPE_BF16> {
+  using T = uint16_t;
+  static __device__ __forceinline__ float f32(T v) {
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
+  }
+  static __device__ __forceinline__ T of(float v) { return bf16_bits(v); }
+};
+template <>
+struct In<MOE_DTYPE_F16> {
+  using T = uint16_t;
+  static __device__ __forceinline__ float f32(T v) { return __half2float(__ushort_as_half(v)); }
+  static __device__ __forceinline__ T of(float v) {
+    return __half_as_ushort(__float2half_rn(v));
+  }
+};
+template <>
+struct In<MOE_DTYPE_F32> {
+  using T = float;
+  static __device__ __forceinline__ float f32(T v) { return v; }
+  static __device__ __forceinline__ T of(float v) { return v; }
+};
+
+// Values 8 l .. 8 l + 7 of a tile that has n of its 128 (zeros past them), raw: converting waits
+// for the loads, so it is left for later.
+template <typename T>
+struct alignas(16) Raw8 {
+  T v[8];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* tile, int n, int l) {
+  Raw8<T> r;
+  const int c = 8 * l;
+  if (c + 8 <= n) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i)
+      reinterpret_cast<uint4*>(&r)[i] = ld_nc_v4(reinterpret_cast<const char*>(tile + c) + 16 * i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r.v[i] = c + i < n ? __ldg(tile + c + i) : T(0);
+  }
+  return r;
+}
+
+}  // namespace moe

@@ -113,19 +113,6 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int M, int N) {
          (static_cast<uint32_t>(M >> 7) << 27);
 }
 
-// One lane of a converged warp.  The warps that issue copies and MMAs run their loops as whole
-// warps and elect a lane only around the issue itself: the operands then stay in uniform
-// registers.  With the loops inside `if (lane == 0)` every tcgen05 or TMA instruction cost its
-// thread 100 to 170 cycles.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xFFFFFFFF;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r));
-  return r != 0;
-}
 // mbar_wait by a whole warp, with one answer for all of it
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           DevErr* err, int site, uint64_t limit_ns) {

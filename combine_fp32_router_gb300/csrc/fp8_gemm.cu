@@ -1,0 +1,618 @@
+// Product of 8-bit rows and 8-bit expert weights with a scale per 128 values (format: fp8.cuh):
+//   out[r, n] = sum_kb sa[r, kb] sb[e(r)][n / 128, kb] sum_{k in kb} A[r, k] B[e(r)][n, k],
+// rows grouped by expert in 128-row segments, or one matrix.
+//
+// One persistent launch.  A tile is 256 x 256 on a CTA pair (cta_group::2: each CTA holds 128 rows
+// and half of the weights) or 128 rows x 128, 64 or 32 weight rows on one CTA.  The tensor cores
+// (tcgen05.mma kind::f8f6f4) sum the 128 values of a block of K into TMEM; scales differ from block
+// to block, so the sum of each block is taken out of TMEM, scaled and added to the tile's sums, which
+// stay in registers:  acc = fma(sum, sa sb, acc), two values an instruction.  Every shape adds the
+// same products in the same order, so a row's results do not depend on the other rows.  Warps:
+//   0..7  sums: lanes 32 (w % 4) .. of TMEM, half w / 4 of the columns; then the output
+//   8     producer: codes by TMA (128-byte swizzle)
+//   9     MMAs, TMEM allocation
+// Ten warps leave 200 registers to a thread: 128 sums, 32 values in flight.
+#include <cuda.h>
+
+#include <atomic>
+#include <cstdlib>
+#include <mutex>
+
+#include "fp8.cuh"
+#include "internal.h"
+
+namespace moe {
+
+namespace {
+
+// Device-side problems of the 8-bit product (a bounded wait that ran out, counts that do not fit
+// the rows): first error since moe_gemm_fp8_get_error last read it.
+__device__ DevErr g_gemm8_err;
+
+// Reads and clears it in one step: an error that comes between the two would be lost.
+__device__ int g_taken8_status;
+__global__ void take_error_kernel() { g_taken8_status = atomicExch(&g_gemm8_err.status, 0); }
+
+constexpr int kThreads = 320;
+constexpr int kSumWarps = 8;
+constexpr int kMaxStages = 32;
+constexpr int kMaxBufs = 8;
+constexpr int kBoxes = 5;  // box heights of the rows: 8, 16, 32, 64, 128
+constexpr uint32_t kRingBytes = 192 * 1024;
+
+template <int NT, bool PAIR>
+struct Cfg {
+  static constexpr int kCtas = PAIR ? 2 : 1;
+  static constexpr int kRows = 128 * kCtas;       // rows of a tile
+  static constexpr int kLocalN = NT / kCtas;      // weight rows that a CTA loads
+  static constexpr int kCols = NT / 2;            // columns of a warp's sums
+  static constexpr int kBufs = 512 / NT < kMaxBufs ? 512 / NT : kMaxBufs;  // of block sums in TMEM
+  static constexpr uint32_t kTmemCols = kBufs * NT;
+};
+
+struct Params {
+  const int32_t* counts;
+  const float *sa, *sb;
+  int64_t rows;
+  int N, kt, E, nt, nb;  // outputs, blocks of K, experts, weight tiles and scale blocks per expert
+  int stages;
+  uint32_t abytes;       // a stage's place for rows
+  int vec;               // output rows start on 32 (2), 16 (1) bytes or neither (0)
+  int f32;
+  void* out;
+  uint64_t wait_ns;
+  uint32_t withhold;     // test hook: bit 0, 1: CTA 0, 1 loads nothing
+  CUtensorMap mapB, mapA[kBoxes];
+};
+
+// behind the stages, and behind the 16 KB past the last one that an MMA of fewer than 128 rows reads
+struct Shared {
+  uint64_t bars[2 * kMaxStages + 2 * kMaxBufs + 1];
+  uint32_t tmem;
+  int32_t abort_flag;
+  uint32_t consumed, peer_issued;                // fills used by MMAs, fills issued by the peer
+  uint32_t tx[kMaxStages], peer_tx[kMaxStages];  // bytes of the fill in a stage
+  int32_t first_block[kMaxE + 1], first_row[kMaxE + 1], count[kMaxE];
+};
+constexpr size_t kSmemBytes = kRingBytes + 16384 + 1024 + sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "fits the opt-in shared memory of a CTA (227 KB)");
+
+struct Tile {
+  int e, row0, nvalid, n0;
+  int box;  // index of the box height, the same on both CTAs of a pair
+};
+
+template <int NT, bool PAIR>
+__device__ __forceinline__ Tile decode(const Params& p, const Shared& sh, uint32_t tile) {
+  constexpr int R = Cfg<NT, PAIR>::kRows;
+  const uint32_t nt = static_cast<uint32_t>(p.nt);
+  const int b = static_cast<int>(tile / nt);
+  int lo = 0, hi = p.E;  // the last expert with first_block[e] <= b
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (sh.first_block[mid] <= b) lo = mid;
+    else hi = mid;
+  }
+  Tile t;
+  t.e = lo;
+  const int i = b - sh.first_block[lo];
+  t.row0 = sh.first_row[lo] + i * R;
+  t.nvalid = min(sh.count[lo] - i * R, R);
+  t.n0 = static_cast<int>(tile - b * nt) * NT;
+  t.box = t.nvalid <= 8 ? 0 : t.nvalid <= 16 ? 1 : t.nvalid <= 32 ? 2 : t.nvalid <= 64 ? 3 : 4;
+  return t;
+}
+
+// 16 columns of this thread's lane, not waited for; and the wait, after which they may be used.
+__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16_done(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+// Two fp32 sums += two values * a scale
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
+  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
+      : "+l"(acc)
+      : "r"(lo), "r"(hi), "l"(s2));
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+
+__device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+// Eight words to a place of its alignment (vec as in Params)
+__device__ __forceinline__ void store8(uint32_t* o, int vec, const uint32_t (&w)[8]) {
+  if (vec == 2) {
+    st_v8(o, w);
+  } else {
+    st_v4(o, make_uint4(w[0], w[1], w[2], w[3]));
+    st_v4(o + 4, make_uint4(w[4], w[5], w[6], w[7]));
+  }
+}
+
+// 16 sums of a row to its columns col .. col + 15 (those below N).
+__device__ __forceinline__ void store16(const Params& p, int64_t row, int col, const uint64_t* acc) {
+  const int64_t at = row * p.N + col;
+  if (p.vec && col + 16 <= p.N) {
+    uint32_t w[8];
+    if (p.f32) {
+      uint32_t* o = static_cast<uint32_t*>(p.out) + at;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          w[2 * i] = static_cast<uint32_t>(acc[4 * h + i]);
+          w[2 * i + 1] = static_cast<uint32_t>(acc[4 * h + i] >> 32);
+        }
+        store8(o + 8 * h, p.vec, w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(lo_of(acc[i]), hi_of(acc[i]));
+      store8(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at), p.vec, w);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float v = i & 1 ? hi_of(acc[i / 2]) : lo_of(acc[i / 2]);
+    if (col + i < p.N) {
+      if (p.f32) static_cast<float*>(p.out)[at + i] = v;
+      else static_cast<uint16_t*>(p.out)[at + i] = bf16_bits(v);
+    }
+  }
+}
+
+template <int NT, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_constant__ Params p) {
+  using C = Cfg<NT, PAIR>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (base - raw) + kRingBytes + 16384);
+  const uint32_t S = static_cast<uint32_t>(p.stages);
+  const uint32_t stage_bytes = p.abytes + C::kLocalN * 128;
+  const auto full = [&](uint32_t s) { return smem_u32(&sh.bars[s]); };
+  const auto empty = [&](uint32_t s) { return smem_u32(&sh.bars[kMaxStages + s]); };
+  const auto tfull = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + a]); };
+  const auto tempty = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + kMaxBufs + a]); };
+  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs]);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(&sh.abort_flag);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+  const int unit = blockIdx.x / C::kCtas, units = gridDim.x / C::kCtas;
+  DevErr* err = &g_gemm8_err;
+  // the peer arrives on a pair's barriers too: those waits acquire at cluster scope
+  const auto wait = [&](uint32_t bar, uint32_t parity, volatile int* ab, int site) {
+    if constexpr (PAIR) return mbar_wait_cluster(bar, parity, ab, err, site, p.wait_ns);
+    else return mbar_wait(bar, parity, ab, err, site, p.wait_ns);
+  };
+  const auto warp_wait = [&](uint32_t bar, uint32_t parity, int site) {
+    return __all_sync(0xFFFFFFFFu, wait(bar, parity, abort_flag, site)) != 0;
+  };
+
+  if (threadIdx.x == 0) {
+    for (uint32_t s = 0; s < S; ++s) {
+      mbar_init(full(s), 1);  // rank 0's: its arming arrival and both CTAs' bytes
+      mbar_init(empty(s), 1);
+    }
+    for (int a = 0; a < C::kBufs; ++a) {
+      mbar_init(tfull(a), 1);
+      mbar_init(tempty(a), kSumWarps * C::kCtas);  // rank 0's: an arrival of every summing warp
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+    sh.abort_flag = 0;
+    sh.consumed = sh.peer_issued = 0u;
+    tma_prefetch_desc(&p.mapB);
+  }
+  if (warp == 9) {
+    if constexpr (PAIR) tmem_alloc_pair(smem_u32(&sh.tmem), C::kTmemCols);
+    else tmem_alloc(smem_u32(&sh.tmem), C::kTmemCols);
+  }
+  griddep_wait();
+  if (warp == 8) {  // the experts' first blocks and rows
+    int nb = 0, nr = 0;
+    bool bad = false;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      int c = 0;
+      if (e < p.E) c = p.counts ? p.counts[e] : static_cast<int>(p.rows);
+      bad |= c < 0 || c > p.rows;
+      if (bad) c = 0;
+      int b = (c + C::kRows - 1) / C::kRows, r = p.counts ? (c + 127) / 128 : 0;
+      const int b_own = b, r_own = r;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int ub = __shfl_up_sync(0xFFFFFFFFu, b, o), ur = __shfl_up_sync(0xFFFFFFFFu, r, o);
+        if (lane >= o) {
+          b += ub;
+          r += ur;
+        }
+      }
+      if (e < p.E) {
+        sh.first_block[e] = nb + b - b_own;
+        sh.first_row[e] = (nr + r - r_own) * 128;
+        sh.count[e] = c;
+        // the last row that is read has to exist (the padding after it need not, nor the place
+        // where an expert without rows would start)
+        bad |= c > 0 && static_cast<int64_t>(nr + r - r_own) * 128 + c > p.rows;
+      }
+      nb += __shfl_sync(0xFFFFFFFFu, b, 31);
+      nr += __shfl_sync(0xFFFFFFFFu, r, 31);
+    }
+    bad = __any_sync(0xFFFFFFFFu, bad);
+    if (lane == 0) {
+      sh.first_block[p.E] = bad ? 0 : nb;  // no block at all when the counts do not fit
+      if (bad && rank == 0) set_error(err, MOE_ERR_DEVICE_BOUNDS, 80);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // the peer's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t tiles = static_cast<uint32_t>(sh.first_block[p.E]) * p.nt;
+  uint32_t issued = 0;  // fills that this CTA's producer issued
+
+  if (warp == 8) {
+    uint32_t s = 0, phase = 1;
+    bool ok = blockIdx.x > 1 || ((p.withhold >> blockIdx.x) & 1u) == 0u;
+    const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
+      if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, x, y);
+      else tma_load_2d(dst, m, bar, x, y);
+    };
+    for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
+      const Tile t = decode<NT, PAIR>(p, sh, tile);
+      const CUtensorMap* ma = &p.mapA[t.box];
+      const uint32_t bytes = (8u << t.box) * 128u + C::kLocalN * 128u;
+      const int wrow = t.e * p.N + t.n0 + C::kLocalN * rank, arow = t.row0 + 128 * rank;
+      for (int kb = 0; kb < p.kt; ++kb) {
+        if (issued >= S) ok = warp_wait(empty(s), phase, 81);
+        if (!ok) break;
+        const uint32_t st = base + s * stage_bytes;
+        const uint32_t bar = PAIR ? mapa_shared(full(s), 0) : full(s);
+        if (elect_one()) {
+          sh.tx[s] = bytes;
+          if (rank == 0) mbar_arrive_expect_tx(full(s), bytes * C::kCtas);
+          load(st, ma, bar, kb * 128, arow);
+          load(st + p.abytes, &p.mapB, bar, kb * 128, wrow);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == S) {
+          s = 0;
+          phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 9 && rank == 0) {
+    constexpr uint32_t idesc = idesc_e4m3_f32(C::kRows, NT);
+    uint32_t s = 0, phase = 0, a = 0, aphase = 1, used = 0;
+    bool ok = true;
+    for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
+      for (int kb = 0; kb < p.kt; ++kb) {
+        if (used >= C::kBufs) ok = warp_wait(tempty(a), aphase, 83);
+        if (ok) ok = warp_wait(full(s), phase, 84);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t st = base + s * stage_bytes, d = tmem + a * NT;
+        if (elect_one()) {
+          const uint64_t da = smem_desc_sw128(st, 16, 1024);
+          const uint64_t db = smem_desc_sw128(st + p.abytes, 16, 1024);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // 32 values of K each
+            if constexpr (PAIR) umma_f8_pair(d, da + 2 * j, db + 2 * j, idesc, j > 0);
+            else umma_f8(d, da + 2 * j, db + 2 * j, idesc, j > 0);
+          }
+          if constexpr (PAIR) {
+            umma_commit_pair(empty(s), 3);
+            umma_commit_pair(tfull(a), 3);
+          } else {
+            umma_commit(empty(s));
+            umma_commit(tfull(a));
+          }
+        }
+        __syncwarp();
+        ++used;
+        if (++s == S) {
+          s = 0;
+          phase ^= 1;
+        }
+        if (++a == C::kBufs) {
+          a = 0;
+          aphase ^= 1;
+        }
+      }
+    }
+    __syncwarp();
+    if (elect_one()) {  // every MMA issued is complete before TMEM is freed
+      sh.consumed = used;
+      if constexpr (PAIR) umma_commit_pair(drain, 1);
+      else umma_commit(drain);
+    }
+    mbar_wait(drain, 0, nullptr, err, 85, p.wait_ns);
+  } else if (warp < kSumWarps) {
+    const int q = warp & 3, half = warp >> 2;
+    constexpr int kCols = C::kCols, kChunks = kCols / 16;
+    const uint32_t lane0 = static_cast<uint32_t>(32 * q) << 16;
+    uint32_t a = 0, aphase = 0;
+    bool ok = true;
+    for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
+      const Tile t = decode<NT, PAIR>(p, sh, tile);
+      const int r0 = 128 * rank + 32 * q, col0 = t.n0 + half * kCols;
+      const bool live = r0 < t.nvalid && col0 < p.N;  // else nothing of it is stored
+      // rows past the last valid one take its scale (it exists), columns past N the last block's
+      const float* sa = p.sa + static_cast<int64_t>(t.row0 + min(r0 + lane, t.nvalid - 1)) * p.kt;
+      const float* sb = p.sb + (static_cast<int64_t>(t.e) * p.nb + min(col0 / 128, p.nb - 1)) * p.kt;
+      uint64_t acc[kCols / 2];
+#pragma unroll
+      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
+      float a0 = 0, a1 = 0, b0 = 0, b1 = 0;  // scales of this block and the next
+      if (live) {
+        a0 = __ldg(sa);
+        b0 = __ldg(sb);
+        a1 = __ldg(sa + min(1, p.kt - 1));
+        b1 = __ldg(sb + min(1, p.kt - 1));
+      }
+      for (int kb = 0; kb < p.kt; ++kb) {
+        const float scale = a0 * b0;
+        if (live) {
+          const int next = min(kb + 2, p.kt - 1);
+          a0 = a1;
+          b0 = b1;
+          a1 = __ldg(sa + next);
+          b1 = __ldg(sb + next);
+        }
+        // one answer for the warp: the tcgen05.ld below is .sync.aligned
+        ok = warp_wait(tfull(a), aphase, 86);
+        if (!ok) break;
+        tc_fence_after();
+        if (live) {
+          uint64_t s2;
+          asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "r"(__float_as_uint(scale)));
+          const uint32_t ta = tmem + a * NT + half * kCols + lane0;
+          uint32_t v[2][16];
+          tmem_ld16_start(ta, v[0]);
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            tmem_ld16_done(v[c & 1]);
+            if (c + 1 < kChunks) tmem_ld16_start(ta + 16 * (c + 1), v[(c + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], s2);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR) mbar_arrive_cluster_relaxed(mapa_shared(tempty(a), 0));
+          else mbar_arrive(tempty(a));
+        }
+        if (++a == C::kBufs) {
+          a = 0;
+          aphase ^= 1;
+        }
+      }
+      if (ok && live && r0 + lane < t.nvalid) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) store16(p, t.row0 + r0 + lane, col0 + 16 * c, acc + 8 * c);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  // After an abort, loads may still be in flight: they land before TMEM is released and the
+  // CTAs exit.  With pairs all complete on rank 0's barriers: rank 1 reports its fills, rank 0
+  // balances the bytes of fills that only one CTA issued and waits, then both leave together.
+  if constexpr (PAIR) {
+    if (rank == 1 && warp == 8 && lane == 0) {
+      st_shared_cluster_u32(mapa_shared(smem_u32(&sh.peer_issued), 0), issued);
+      for (uint32_t s = 0; s < S; ++s)
+        st_shared_cluster_u32(mapa_shared(smem_u32(&sh.peer_tx[s]), 0), sh.tx[s]);
+    }
+    cluster_sync_all();
+  }
+  if (rank == 0 && warp == 8 && lane == 0) {
+    const uint32_t peer = PAIR ? *const_cast<volatile uint32_t*>(&sh.peer_issued) : issued;
+    const uint32_t end = issued > peer ? issued : peer;
+    for (uint32_t f = *const_cast<volatile uint32_t*>(&sh.consumed); f < end; ++f) {
+      const uint32_t s = f % S;
+      if (f >= issued) mbar_arrive_expect_tx(full(s), sh.peer_tx[s]);
+      else if (f >= peer) mbar_complete_tx(full(s), sh.tx[s]);
+      wait(full(s), (f / S) & 1, nullptr, 82);
+    }
+  }
+  if constexpr (PAIR) {
+    __syncthreads();
+    cluster_sync_all();  // no load, remote arrival or MMA into the peer after this point
+  }
+  if (warp == 9) {
+    tc_fence_after();
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
+  }
+}
+
+template <int NT, bool PAIR>
+cudaError_t launch(const Params& p, int units, cudaStream_t s) {
+  auto kern = gemm_fp8_kernel<NT, PAIR>;
+  static std::atomic<unsigned long long> attr_set_mask{0ull};
+  int dev = 0;
+  cudaError_t st = cudaGetDevice(&dev);
+  if (st != cudaSuccess) return st;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit == 0ull || !(attr_set_mask.load(std::memory_order_acquire) & bit)) {
+    st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kSmemBytes));
+    if (st != cudaSuccess) return st;
+    attr_set_mask.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(Cfg<NT, PAIR>::kCtas * units));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                            const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                            const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// Codes: `rows` rows of K values, fp8_cols(K) bytes apart, 128-byte swizzle, boxes of 128 values x
+// box_rows.  Values past K and rows past the last are read as zeros, whatever is there.
+CUtensorMap code_map(const void* base, int K, uint64_t rows, uint32_t box_rows, cudaError_t* st) {
+  CUtensorMap m = {};
+  auto enc = reinterpret_cast<Encode>(tensor_map_encoder());
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), rows};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(fp8_cols(K))};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t ones[2] = {1, 1};
+  if (!enc || enc(&m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    *st = cudaErrorInvalidValue;
+  return m;
+}
+
+// Tile shapes: 256 x 256 on pairs, or 128 x 128, 64, 32 on single CTAs; by the rounds of tiles that
+// each takes over the SMs times what a block of K of a tile costs there (in cycles).  With `counts`,
+// which are on the device, the experts are taken to have equal shares of the rows less half a tile
+// of padding each.  MOE_FP8_SHAPE = 0 .. 3 sets the shape; every shape gives the same bits.
+struct Shape {
+  int rows, n, ctas, cost;
+};
+constexpr Shape kShapes[4] = {{256, 256, 2, 560}, {128, 128, 1, 400}, {128, 64, 1, 260}, {128, 32, 1, 200}};
+int choose_shape(int64_t rows, int N, int E, bool grouped, int sms) {
+  static const int forced = [] {
+    const char* v = std::getenv("MOE_FP8_SHAPE");
+    return v && *v >= '0' && *v <= '3' ? *v - '0' : -1;
+  }();
+  if (forced >= 0) return forced;
+  if (grouped) rows = rows > 65 * static_cast<int64_t>(E) ? rows - 64 * static_cast<int64_t>(E) : E;
+  const int64_t share = (rows + E - 1) / E;
+  int best = 0;
+  int64_t least = INT64_MAX;
+  for (int i = 0; i < 4; ++i) {
+    const Shape& s = kShapes[i];
+    const int64_t tiles = E * ((share + s.rows - 1) / s.rows) * ((N + s.n - 1) / s.n);
+    const int64_t units = sms / s.ctas, cost = (tiles + units - 1) / units * s.cost;
+    if (cost < least) {
+      least = cost;
+      best = i;
+    }
+  }
+  return best;
+}
+
+template <int NT, bool PAIR>
+cudaError_t run(Params& p, const uint8_t* a, const uint8_t* b, int K, int sms, cudaStream_t stream) {
+  using C = Cfg<NT, PAIR>;
+  cudaError_t st = cudaSuccess;
+  const int64_t blocks = (p.rows + C::kRows - 1) / C::kRows + (p.counts ? p.E : 0);
+  p.nt = (p.N + NT - 1) / NT;
+  p.mapB = code_map(b, K, static_cast<uint64_t>(p.E) * p.N, C::kLocalN, &st);
+  for (int i = 0; i < kBoxes; ++i)  // no block has more than `rows`
+    if (i == 0 || p.rows > (4 << i)) {
+      p.mapA[i] = code_map(a, K, static_cast<uint64_t>(p.rows), 8u << i, &st);
+      p.abytes = (8u << i) * 128u;
+    }
+  if (st != cudaSuccess) return st;
+  const int stages = static_cast<int>(kRingBytes / (p.abytes + C::kLocalN * 128u));
+  p.stages = stages < kMaxStages ? stages : kMaxStages;
+  const int64_t tiles = blocks * p.nt;  // checked by the caller to fit 31 bits
+  const int units = static_cast<int>(tiles < sms / C::kCtas ? tiles : sms / C::kCtas);
+  return launch<NT, PAIR>(p, units, stream);
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status_t moe_gemm_fp8(const uint8_t* a, const float* a_scales, int64_t rows,
+                          const int32_t* counts, const uint8_t* b, const float* b_scales, int E, int N,
+                          int K, void* out, int out_dtype, cudaStream_t stream) {
+  if (rows < 0 || E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (out_dtype != MOE_DTYPE_BF16 && out_dtype != MOE_DTYPE_F32) return MOE_ERR_INVALID_ARG;
+  if (!counts && E != 1) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  const int size = out_dtype == MOE_DTYPE_F32 ? 4 : 2;
+  if (!a || !a_scales || !b || !b_scales || !out || !aligned_to(a, 16) || !aligned_to(b, 16) ||
+      !aligned_to(a_scales, 4) || !aligned_to(b_scales, 4) || !aligned_to(counts, 4) || !aligned_to(out, size))
+    return MOE_ERR_INVALID_ARG;
+  if (E > kMaxE || N > kMaxFp8Cols || K > kMaxFp8Cols || rows > INT32_MAX - 256 ||
+      static_cast<int64_t>(E) * N > INT32_MAX - 256)  // rows of a tile past the last expert count too
+    return MOE_ERR_UNSUPPORTED;
+  // tiles of 128 x 32 at the least
+  if (((rows + 127) / 128 + E) * ((N + 31) / 32) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  Params p = {};
+  p.counts = counts;
+  p.sa = a_scales;
+  p.sb = b_scales;
+  p.rows = rows;
+  p.N = N;
+  p.kt = static_cast<int>(fp8_cols(K) / 128);
+  p.E = E;
+  p.nb = (N + 127) / 128;
+  const int64_t row = static_cast<int64_t>(N) * size;
+  p.vec = aligned_to(out, 32) && row % 32 == 0 ? 2 : aligned_to(out, 16) && row % 16 == 0 ? 1 : 0;
+  p.f32 = out_dtype == MOE_DTYPE_F32;
+  p.out = out;
+  p.wait_ns = wait_limit_ns();
+  p.withhold = withheld_loaders();
+  const int sms = num_sms_of_current_device();
+  const int shape = choose_shape(rows, N, E, counts != nullptr, sms);
+  const cudaError_t st = shape == 0   ? run<256, true>(p, a, b, K, sms, stream)
+                         : shape == 1 ? run<128, false>(p, a, b, K, sms, stream)
+                         : shape == 2 ? run<64, false>(p, a, b, K, sms, stream)
+                                      : run<32, false>(p, a, b, K, sms, stream);
+  return st == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_gemm_fp8_get_error(cudaStream_t stream) {
+  if (cudaStreamSynchronize(stream) != cudaSuccess) return MOE_ERR_CUDA;
+  static std::mutex m;  // g_taken8_status is one caller's at a time
+  const std::lock_guard<std::mutex> lock(m);
+  int status = 0;
+  if (cudaLaunchKernel(reinterpret_cast<const void*>(take_error_kernel), dim3(1), dim3(1), nullptr, 0,
+                       stream) != cudaSuccess ||
+      cudaMemcpyFromSymbolAsync(&status, g_taken8_status, sizeof(status), 0, cudaMemcpyDeviceToHost,
+                                stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  return static_cast<moe_status_t>(status);
+}
+
+}  // extern "C"

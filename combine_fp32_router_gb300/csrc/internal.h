@@ -16,6 +16,7 @@ constexpr int kMaxK = 16;
 constexpr int kMaxE = 1024;
 constexpr int kFewMaxTokens = 32;          // tokens of moe_forward_few_fp4 (one bit each)
 constexpr int kMaxFp4Cols = 1 << 20;       // values per row of a 4-bit matrix
+constexpr int kMaxFp8Cols = 1 << 20;       // and of an 8-bit one
 
 struct DevErr;
 

@@ -382,6 +382,154 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
                                  moe_bf16_t* out, void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Around 8-bit experts: rows and weights with a scale per 128 values, their product, the norm
+ * before the layer, and tokens sorted by expert and back, each with the gradient that training
+ * needs.  moe_rmsnorm gives 8-bit rows, moe_sort_tokens lays them out by expert, moe_gemm_fp8
+ * multiplies them by the experts' weights, moe_quantize_rows_fp8 (swiglu) makes the second
+ * product's rows of the first one's, and moe_unsort_tokens brings the experts' rows back.
+ *
+ * Format of a matrix of R rows and C columns: Kp = C rounded up to a multiple of 128.
+ *   codes  [R, Kp] E4M3 bytes (largest value 448); quantisers write zero codes past C.
+ *   scales [R, Kp / 128] fp32: a value is code * scale.
+ * scale = max(amax / 448, 2^-126) of the row's 128 columns, 1 where all are zero; the code is the
+ * E4M3 number nearest to x * (1 / scale) in fp32, ties to the even mantissa, saturating.  Columns
+ * that hold an infinity or a NaN have the scale NaN and zero codes: all 128 values are NaN.
+ * Weights have one scale per 128 x 128 block instead: codes [N, Kp], scales
+ * [ceil(N / 128), Kp / 128].  Codes are 16-byte aligned, other arrays aligned to their element
+ * (rows that start on 16 bytes are faster).  Groups of matrices (experts) lie one after another.
+ * Every entry point is asynchronous on `stream`, whose device has to be current.
+ * ------------------------------------------------------------------------------------- */
+
+/* Bytes of one row's codes. */
+int64_t moe_fp8_row_bytes(int cols);
+
+/* x [rows, cols] (MOE_DTYPE_*, row r at x + r * row_stride elements) -> q [rows, Kp], scales.
+ * swiglu = 1: a row of x holds a and b, cols values each (row_stride >= 2 cols), and
+ * silu(a) b = a / (1 + exp(-a)) b is quantised (forward only; its fp32 value is within
+ * (6 + |a|) 2^-23 of the exact one, relatively).  perm: NULL, or [rows] int32: rows with perm < 0 are neither read nor
+ * written (the padding of sorted rows).  cols <= 2^20, rows * ceil(cols / 128) < 2^31 - 64.
+ * rows = 0 writes nothing. */
+moe_status_t moe_quantize_rows_fp8(const void* x, int dtype, int64_t rows, int cols,
+                                   int64_t row_stride, int swiglu, const int32_t* perm, uint8_t* q,
+                                   float* scales, cudaStream_t stream);
+
+/* The values of 8-bit rows to out [rows, cols] (contiguous, 16-byte aligned), code * scale rounded
+ * to fp32 and then to `dtype`. */
+moe_status_t moe_dequantize_rows_fp8(const uint8_t* q, const float* scales, int64_t rows, int cols,
+                                     int dtype, void* out, cudaStream_t stream);
+
+/* Expert weights W [E, K, N] bf16 in 128 x 128 blocks.  transpose = 1: Wq [E, N, Kp] and scales
+ * [E, ceil(N / 128), ceil(K / 128)], for products over K (x W); 0: Wq [E, K, Np] and scales
+ * [E, ceil(K / 128), ceil(N / 128)], for products over N (dy W^T, the gradient of x).  Both hold
+ * the same values.  E <= 1024, K and N <= 2^20. */
+moe_status_t moe_quantize_blocks_fp8(const moe_bf16_t* W, int E, int K, int N, int transpose,
+                                     uint8_t* Wq, float* scales, cudaStream_t stream);
+
+/*
+ * out[r, n] = sum_kb a_scales[r, kb] b_scales[e(r), n / 128, kb] sum_{k in block kb} A[r, k]
+ * B[e(r)][n, k], every sum in fp32, in a K order that depends on K alone, rounded once to out_dtype
+ * (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
+ *   a [rows, Kp], a_scales [rows, Kp / 128]; b, b_scales: E matrices of N x K
+ *   (moe_quantize_blocks_fp8's layout); codes past K are not used; out [rows, N] contiguous.
+ *   counts : NULL (E = 1: every row), or a DEVICE array [E]: expert e's counts[e] rows start at row
+ *            sum_{j<e} round_up(counts[j], 128) (moe_sort_tokens's layout); rows between the
+ *            segments are left as they were.
+ * Any rows, N, K >= 1 (rows = 0 writes nothing) with E <= 1024, N and K <= 2^20,
+ * E * N < 2^31 - 256 and (ceil(rows / 128) + E) * ceil(N / 32) < 2^31, else MOE_ERR_UNSUPPORTED.
+ * Counts that are negative or do not fit `rows` record MOE_ERR_DEVICE_BOUNDS and nothing is
+ * written; device-side problems are read with moe_gemm_fp8_get_error, which synchronises `stream`,
+ * returns the first one recorded on the current device since the last call, and clears it in the
+ * same step.  The record is the device's: products on other streams share it, and of several
+ * callers one gets an error.  MOE_FP8_SHAPE (environment, read once per process): 0 to 3 sets the
+ * tile shape (256 x 256, 128 x 128, 128 x 64, 128 x 32), which changes no bit of a result.
+ */
+moe_status_t moe_gemm_fp8(const uint8_t* a, const float* a_scales, int64_t rows,
+                          const int32_t* counts, const uint8_t* b, const float* b_scales, int E,
+                          int N, int K, void* out, int out_dtype, cudaStream_t stream);
+moe_status_t moe_gemm_fp8_get_error(cudaStream_t stream);
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition, in the type and / or in 8 bits:
+ *   s = x + residual, rounded to dtype and written to sum_out (s = x without a residual)
+ *   rstd = 1 / sqrt(mean(s^2) + eps),  y = s * rstd * weight  (fp32)
+ *   out [rows, cols] = y in dtype; q, scales = y in 8 bits (of the fp32 values); rstd [rows] fp32
+ *   x [rows, cols] (MOE_DTYPE_*, row r at x + r * x_stride elements); residual, sum_out, out
+ *   contiguous; weight [cols] in dtype or fp32 (weight_dtype).  residual and sum_out go together,
+ *   q and scales too; at least one of out and q is needed, rstd may be NULL.  sum_out may be
+ *   residual or (with x_stride = cols) x; no other output may overlap an input.
+ * cols <= 16384, rows < 2^31.  A row whose squares sum beyond fp32 gives zeros or NaN.  A row's
+ * results do not depend on the other rows.
+ */
+moe_status_t moe_rmsnorm(const void* x, int64_t x_stride, const void* residual, const void* weight,
+                         int dtype, int weight_dtype, int64_t rows, int cols, float eps,
+                         void* sum_out, void* out, uint8_t* q, float* scales, float* rstd,
+                         cudaStream_t stream);
+
+/*
+ * Its gradient for dy [rows, cols] (the 8-bit rounding counts as the identity):
+ *   n = s * rstd,  g = dy * weight
+ *   dx      [rows, cols] dtype : rstd (g - n mean(g n)) + dsum, the gradient of x and of residual
+ *   dweight [cols] fp32        : sum over rows of dy n; NULL leaves it out
+ *   s: sum_out, or x without a residual; rstd from the forward; dsum: NULL, or the gradient that
+ *   arrives at sum_out [rows, cols]; all contiguous.  dx may be dy, s or dsum itself.
+ * ws: moe_rmsnorm_workspace_bytes(rows, cols) bytes of device memory, 256-byte aligned (0 for
+ * unsupported sizes), ordered between calls as for moe_forward; unused without dweight.  rows = 0
+ * writes dweight alone (zeros).  Bitwise reproducible on one kind of device.
+ */
+size_t moe_rmsnorm_workspace_bytes(int64_t rows, int cols);
+moe_status_t moe_rmsnorm_backward(const void* dy, const void* s, const void* weight,
+                                  const float* rstd, const void* dsum, int dtype, int weight_dtype,
+                                  int64_t rows, int cols, void* dx, float* dweight, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * Tokens sorted by expert.  Pair p = t * k + j with topk_idx[p] = e takes row
+ * seg(e) + (pairs p' < p of expert e), seg(e) = sum_{i<e} round_up(counts[i], 128): the layout of
+ * the grouped products.
+ *   x [T, row_bytes] (any type) and, with n_scales > 0, x_scales [T, n_scales] fp32
+ *   topk_idx [T, k] int32: -1 is no expert (a pair that is dropped or owned elsewhere); an expert
+ *            may occur twice in a token.  Others outside [0, E) count as -1 and record
+ *            MOE_ERR_DEVICE_BOUNDS.
+ *   rows [n_rows, row_bytes], rows_scales [n_rows, n_scales]: row of pair p = x[p / k]; rows
+ *            without a pair are left as they were.  n_rows >= moe_sort_rows_bound(T, k, E).
+ *   counts [E], perm [n_rows] (the pair of a row, -1 for none), pos [T, k] (the row of a pair, -1)
+ * k <= 16, E <= 1024, T k + 128 (E + 1) < 2^31, row_bytes and n_scales <= 2^20.  T = 0 writes
+ * counts and perm.  ws: moe_sort_workspace_bytes(T, E, k) bytes (0 for unsupported sizes), 256-byte
+ * aligned, ordered between calls as for moe_forward; its error word, which the call clears first,
+ * is read with moe_get_error.  Bitwise reproducible.
+ */
+int64_t moe_sort_rows_bound(int64_t T, int k, int E);
+size_t moe_sort_workspace_bytes(int64_t T, int E, int k);
+moe_status_t moe_sort_tokens(const void* x, int64_t row_bytes, const float* x_scales, int n_scales,
+                             const int32_t* topk_idx, int64_t T, int k, int E, void* rows,
+                             int64_t n_rows, float* rows_scales, int32_t* counts, int32_t* perm,
+                             int32_t* pos, void* ws, size_t ws_bytes, cudaStream_t stream);
+/* dx [T, d] = sum_j drows[pos[t, j]] (drows [n_rows, d]), otherwise as moe_unsort_tokens. */
+moe_status_t moe_sort_tokens_backward(const void* drows, int dtype, int64_t n_rows,
+                                      const int32_t* pos, int64_t T, int k, int d, void* dx,
+                                      void* err_word, cudaStream_t stream);
+
+/*
+ * And back, with weights: out [T, d] = sum_j gate[t, j] rows[pos[t, j]], fp32 in slot order, rounded
+ * once to dtype.  rows [n_rows, d] (MOE_DTYPE_*); gate [T, k] fp32, or NULL for ones; pos [T, k]:
+ * -1 adds nothing (a token without any row gets zeros); others outside [0, n_rows) count as -1 and
+ * record MOE_ERR_DEVICE_BOUNDS in the 16-byte error word err_word (device memory, e.g. the start of
+ * a workspace of moe_sort_tokens; not cleared; read with moe_get_error).  d <= 65536, k <= 16.
+ * T = 0 writes nothing.  Each token's results are bitwise independent of the others.
+ */
+moe_status_t moe_unsort_tokens(const void* rows, int dtype, int64_t n_rows, const float* gate,
+                               const int32_t* pos, int64_t T, int k, int d, void* out,
+                               void* err_word, cudaStream_t stream);
+/* Its gradient for dout [T, d]: drows[pos[t, j]] = gate[t, j] dout[t] in dtype (rows without a pair
+ * are left as they were; no row may be the place of two pairs) and dgate[t, j] =
+ * <rows[pos[t, j]], dout[t]> in fp32 (0 for a pair without a row).  dgate may be NULL, rows then
+ * too; gate may be NULL with it (ones).  drows may be rows itself. */
+moe_status_t moe_unsort_tokens_backward(const void* dout, const void* rows, int dtype,
+                                        int64_t n_rows, const float* gate, const int32_t* pos,
+                                        int64_t T, int k, int d, void* drows, float* dgate,
+                                        void* err_word, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
  * Fine-grained expert parallelism across R GPUs: the exchange plan and the pull-based row
  * copies (DeepSeek-V4 report, Thai translation, itsolotime.com, section 1.2 and Figure 5:
  * each GPU's experts run in waves, wave i+1's rows are fetched and wave i-1's outputs
@@ -506,8 +654,8 @@ void moe_set_wait_timeout_ns(uint64_t ns);
  * the timeout path on a tiny problem with a short timeout).  Bit 1: moe_forward dispatches
  * batches of T <= 128 with the multi-kernel sequence of larger batches instead of its
  * single launch (both give bitwise the same workspace contents and output).  Bits 0 and 2: the
- * first and the second CTA of moe_gemm_fp4 load nothing; the first of moe_forward_few_fp4 loads no
- * weights and no activations, so that their waits run out. */
+ * first and the second CTA of moe_gemm_fp4 and of moe_gemm_fp8 load nothing; the first of
+ * moe_forward_few_fp4 loads no weights and no activations, so that their waits run out. */
 void moe_debug_set_flags(int flags);
 
 /* Short English description of a status code. */
