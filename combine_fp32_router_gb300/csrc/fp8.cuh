@@ -1,6 +1,6 @@
 // The 8-bit format with a scale per 128 values: E4M3 codes (largest value 448) and one fp32 scale
 // per row and 128 columns of a matrix of rows, or per 128 x 128 block of a weight matrix.
-//   scale = max(amax / 448, 2^-126), 1 for a block of zeros, NaN for one that holds an infinity or
+//   scale = max(amax * (1 / 448), 2^-126) (the reciprocal and the product in fp32), 1 for zeros, NaN for one that holds an infinity or
 //           a NaN (its codes are zeros, so every value of it reads back as NaN)
 //   code  = the E4M3 number nearest to x * (1 / scale), ties to the even mantissa
 // 1 / scale is rounded to fp32 once per block, and the product once per value: a code is the nearest
@@ -23,19 +23,21 @@ __host__ __device__ inline int64_t fp8_cols(int64_t cols) { return (cols + 127) 
 
 __device__ __forceinline__ float f8_scale(uint32_t amax) {
   if (amax >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
-  return amax == 0u ? 1.0f : fmaxf(__uint_as_float(amax) / 448.0f, 1.17549435e-38f);
+  return amax == 0u ? 1.0f : fmaxf(__uint_as_float(amax) * (1.0f / 448.0f), 1.17549435e-38f);
 }
 // 1 / scale, 0 for a NaN scale
 __device__ __forceinline__ float f8_inverse(float scale) { return scale == scale ? 1.0f / scale : 0.0f; }
 
-// Codes of two values times inv, the earlier one in the low byte; inv = 0 gives zeros whatever the
-// values are.
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi, float inv) {
+// Codes of eight values times inv, the earlier ones in the low bytes; inv = 0 gives zeros whatever
+// the values are.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   uint16_t r;
-  lo = inv == 0.0f ? 0.0f : lo * inv;
-  hi = inv == 0.0f ? 0.0f : hi * inv;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv) {
+  const uint32_t w = e4m3x2(a * inv, b * inv) | (e4m3x2(c * inv, d * inv) << 16);
+  return inv == 0.0f ? 0u : w;
 }
 // Values of two codes
 __device__ __forceinline__ float2 e4m3x2_f32(uint16_t codes) {
@@ -101,8 +103,8 @@ __device__ __forceinline__ void quantize_seg(const float (&y)[8], uint8_t* q, fl
     for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     const float scale = f8_scale(amax), inv = f8_inverse(scale);
     if (8 * lane < np) {
-      const uint32_t lo = e4m3x2(y[0], y[1], inv) | (e4m3x2(y[2], y[3], inv) << 16);
-      const uint32_t hi = e4m3x2(y[4], y[5], inv) | (e4m3x2(y[6], y[7], inv) << 16);
+      const uint32_t lo = e4m3x4(y[0], y[1], y[2], y[3], inv);
+      const uint32_t hi = e4m3x4(y[4], y[5], y[6], y[7], inv);
       *reinterpret_cast<uint2*>(q + 8 * lane) = make_uint2(lo, hi);
       if ((lane & 15) == 0) s[lane >> 4] = scale;
     }
@@ -115,12 +117,9 @@ __device__ __forceinline__ void quantize_seg(const float (&y)[8], uint8_t* q, fl
       amax = __reduce_max_sync(0xFFFFFFFFu, amax);
       const float scale = f8_scale(amax), inv = f8_inverse(scale);
       if (128 * b < np) {
+        const uint32_t c = e4m3x4(y[4 * b], y[4 * b + 1], y[4 * b + 2], y[4 * b + 3], inv);
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          const uint32_t c = e4m3x2(y[4 * b + j], y[4 * b + j + 1], inv);
-          q[32 * (4 * b + j) + lane] = static_cast<uint8_t>(c);
-          q[32 * (4 * b + j + 1) + lane] = static_cast<uint8_t>(c >> 8);
-        }
+        for (int j = 0; j < 4; ++j) q[32 * (4 * b + j) + lane] = static_cast<uint8_t>(c >> (8 * j));
         if (lane == 0) s[b] = scale;
       }
     }

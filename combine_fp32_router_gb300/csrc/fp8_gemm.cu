@@ -8,13 +8,16 @@
 // to block, so the sum of each block is taken out of TMEM, scaled and added to the tile's sums, which
 // stay in registers:  acc = fma(sum, sa sb, acc), two values an instruction.  Every shape adds the
 // same products in the same order, so a row's results do not depend on the other rows.  Warps:
-//   0..7  sums: lanes 32 (w % 4) .. of TMEM, half w / 4 of the columns; then the output
-//   8     producer: codes by TMA (128-byte swizzle)
-//   9     MMAs, TMEM allocation
-// Ten warps leave 200 registers to a thread: 128 sums, 32 values in flight.
+//   0..7    sums: lanes 32 (w % 4) .. of TMEM, half w / 4 of the columns; then the output
+//   8       producer: codes by TMA (128-byte swizzle)
+//   9, 10   MMAs, groups of blocks of K in turn: what one spends on waiting, committing and looping
+//           (400 cycles a group) passes while the other's MMAs run; TMEM allocation
+//   11      scales: sa sb of every row and 8 blocks of K at a time, to shared memory
+// The summing warps take registers from the others: 128 sums and 64 values in flight.
 #include <cuda.h>
 
 #include <atomic>
+#include <cstddef>
 #include <cstdlib>
 #include <mutex>
 
@@ -33,21 +36,33 @@ __device__ DevErr g_gemm8_err;
 __device__ int g_taken8_status;
 __global__ void take_error_kernel() { g_taken8_status = atomicExch(&g_gemm8_err.status, 0); }
 
-constexpr int kThreads = 320;
-constexpr int kSumWarps = 8;
 constexpr int kMaxStages = 32;
-constexpr int kMaxBufs = 8;
+constexpr int kMaxBufs = 4;
+constexpr int kSumWarps = 8, kLoader = 8, kIssuer = 9, kScaler = 11;
+constexpr int kThreads = 384;
+// Registers of a thread: launched with 168 (65536 / 384, which ptxas gives to the launch bounds), of
+// which the last four warps keep 88 and the others get 208.
+constexpr int kLaunchRegs = 168, kSumRegs = 208, kOtherRegs = 88;
+static_assert(2 * kSumRegs + kOtherRegs <= 3 * kLaunchRegs, "registers at launch");
 constexpr int kBoxes = 5;  // box heights of the rows: 8, 16, 32, 64, 128
-constexpr uint32_t kRingBytes = 192 * 1024;
+constexpr uint32_t kRingBytes = 128 * 1024;
+// Factors of 8 blocks of K at a time; rows of one block 132 words apart, so that four rows of eight
+// blocks meet no bank twice.  Read from global memory by each summing lane for itself, the scales
+// took a warp 210 cycles of the 512 of a block of K.
+constexpr int kScaleBlocks = 8, kScaleRow = 132;
 
 template <int NT, bool PAIR>
 struct Cfg {
   static constexpr int kCtas = PAIR ? 2 : 1;
-  static constexpr int kRows = 128 * kCtas;       // rows of a tile
-  static constexpr int kLocalN = NT / kCtas;      // weight rows that a CTA loads
-  static constexpr int kCols = NT / 2;            // columns of a warp's sums
-  static constexpr int kBufs = 512 / NT < kMaxBufs ? 512 / NT : kMaxBufs;  // of block sums in TMEM
-  static constexpr uint32_t kTmemCols = kBufs * NT;
+  static constexpr int kRows = 128 * kCtas;     // rows of a tile
+  static constexpr int kLocalN = NT / kCtas;    // weight rows that a CTA loads
+  static constexpr int kCols = NT / 2;          // columns of a warp's sums
+  static constexpr int kChunk = kCols < 32 ? kCols : 32;  // of them taken at a time
+  // Blocks of K between two arrivals of the summing warps, and at most per stage: an MMA warp's turn
+  // (wait, issue, commit) takes 350 cycles, the MMAs of a block 160 with 32 columns, 256 with 128
+  static constexpr int kG = NT == 32 ? 4 : NT == 256 ? 1 : 2;
+  static constexpr int kBufs = 512 / NT / kG < kMaxBufs ? 512 / NT / kG : kMaxBufs;
+  static constexpr uint32_t kTmemCols = kBufs * kG * NT;
 };
 
 struct Params {
@@ -55,27 +70,33 @@ struct Params {
   const float *sa, *sb;
   int64_t rows;
   int N, kt, E, nt, nb;  // outputs, blocks of K, experts, weight tiles and scale blocks per expert
-  int stages;
-  uint32_t abytes;       // a stage's place for rows
+  int stages, ks;        // stages, and blocks of K in one
+  uint32_t abytes;       // place for the rows of a block of K
   int vec;               // output rows start on 32 (2), 16 (1) bytes or neither (0)
-  int f32;
+  int f32, tma_out;      // tma_out: rows of the output can be stored by TMA
   void* out;
   uint64_t wait_ns;
   uint32_t withhold;     // test hook: bit 0, 1: CTA 0, 1 loads nothing
-  CUtensorMap mapB, mapA[kBoxes];
+  CUtensorMap mapB, mapA[kBoxes], mapOut;
 };
 
-// behind the stages, and behind the 16 KB past the last one that an MMA of fewer than 128 rows reads
+// behind the stages (an MMA whose box has fewer than 128 rows reads up to 16 KB past its stage: what
+// it finds there meets rows that are not stored)
 struct Shared {
-  uint64_t bars[2 * kMaxStages + 2 * kMaxBufs + 1];
+  alignas(16) float factors[2][2][kScaleBlocks][kScaleRow];  // slot, half of the columns
+  int4 info[2];  // per slot: its tile's first row, valid rows and first column
+  uint64_t bars[2 * kMaxStages + 2 * kMaxBufs + 5];
   uint32_t tmem;
   int32_t abort_flag;
-  uint32_t consumed, peer_issued;                // fills used by MMAs, fills issued by the peer
+  uint32_t peer_issued;                          // fills issued by the peer
   uint32_t tx[kMaxStages], peer_tx[kMaxStages];  // bytes of the fill in a stage
   int32_t first_block[kMaxE + 1], first_row[kMaxE + 1], count[kMaxE];
 };
-constexpr size_t kSmemBytes = kRingBytes + 16384 + 1024 + sizeof(Shared);
+// A summing warp's place for outputs: 32 rows of 128 bytes, swizzled for TMA, or 16 columns.
+constexpr uint32_t kOutBytes = 8192;
+constexpr size_t kSmemBytes = kRingBytes + kSumWarps * kOutBytes + 1024 + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "fits the opt-in shared memory of a CTA (227 KB)");
+static_assert(sizeof(Shared) >= 16384, "what a box of fewer than 128 rows leaves out can be read");
 
 struct Tile {
   int e, row0, nvalid, n0;
@@ -103,8 +124,41 @@ __device__ __forceinline__ Tile decode(const Params& p, const Shared& sh, uint32
   return t;
 }
 
-// 16 columns of this thread's lane, not waited for; and the wait, after which they may be used.
-__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ bool mbar_try_wait_relaxed(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// 32 or 16 columns of this thread's lane, waited for.
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
+                 "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -112,8 +166,6 @@ __device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld16_done(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
@@ -121,15 +173,6 @@ __device__ __forceinline__ void tmem_ld16_done(uint32_t (&r)[16]) {
                :
                : "memory");
 }
-// Two fp32 sums += two values * a scale
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t lo, uint32_t hi, uint64_t s2) {
-  asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}"
-      : "+l"(acc)
-      : "r"(lo), "r"(hi), "l"(s2));
-}
-__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v)); }
-__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
-
 __device__ __forceinline__ void st_v8(void* p, const uint32_t (&v)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
                "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -145,36 +188,67 @@ __device__ __forceinline__ void store8(uint32_t* o, int vec, const uint32_t (&w)
   }
 }
 
-// 16 sums of a row to its columns col .. col + 15 (those below N).
-__device__ __forceinline__ void store16(const Params& p, int64_t row, int col, const uint64_t* acc) {
-  const int64_t at = row * p.N + col;
+// A warp's 16 sums of `n` rows (lane = row, from `row` on) to their columns col .. col + 15 (those
+// below N).  Where rows do not start on 16 bytes they go through shared memory, so that lanes store
+// neighbouring values.
+__device__ __forceinline__ void store16(const Params& p, int64_t row, int n, int col, const float* acc,
+                                        uint32_t* buf, int lane) {
   if (p.vec && col + 16 <= p.N) {
+    if (lane >= n) return;
+    const int64_t at = (row + lane) * p.N + col;
     uint32_t w[8];
     if (p.f32) {
       uint32_t* o = static_cast<uint32_t*>(p.out) + at;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          w[2 * i] = static_cast<uint32_t>(acc[4 * h + i]);
-          w[2 * i + 1] = static_cast<uint32_t>(acc[4 * h + i] >> 32);
-        }
+        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(acc[8 * h + i]);
         store8(o + 8 * h, p.vec, w);
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(lo_of(acc[i]), hi_of(acc[i]));
+      for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(acc[2 * i], acc[2 * i + 1]);
       store8(reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.out) + at), p.vec, w);
     }
     return;
   }
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float v = i & 1 ? hi_of(acc[i / 2]) : lo_of(acc[i / 2]);
-    if (col + i < p.N) {
-      if (p.f32) static_cast<float*>(p.out)[at + i] = v;
-      else static_cast<uint16_t*>(p.out)[at + i] = bf16_bits(v);
+  for (int i = 0; i < 16; ++i) buf[lane * 17 + i] = __float_as_uint(acc[i]);
+  __syncwarp();
+  const int c = lane & 15;
+  if (col + c < p.N) {
+    for (int r = lane >> 4; r < n; r += 2) {
+      const int64_t at = (row + r) * p.N + col + c;
+      if (p.f32) static_cast<uint32_t*>(p.out)[at] = buf[r * 17 + c];
+      else static_cast<uint16_t*>(p.out)[at] = bf16_bits(__uint_as_float(buf[r * 17 + c]));
     }
+  }
+}
+// 128 bytes of each of a warp's 32 rows (W sums, from column col on) through shared memory as one
+// TMA store, which leaves out columns past N: lanes storing their own rows take 32 memory lines an
+// instruction.  16-byte pieces are swizzled as the tensor map has it.
+template <int W>
+__device__ __forceinline__ void store_tile(const Params& p, int row, int col, const float* acc, uint32_t buf,
+                                           int lane) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float* v = acc + i * (W / 8);
+    uint4 u;
+    if constexpr (W == 32) {
+      u = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    } else {
+      u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(buf + 128 * lane + 16 * (i ^ (lane & 7))),
+                 "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w)
+                 : "memory");
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(&p.mapOut, buf, col, row);
+    bulk_commit();
   }
 }
 
@@ -184,14 +258,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (base - raw) + kRingBytes + 16384);
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (base - raw) + kRingBytes + kSumWarps * kOutBytes);
   const uint32_t S = static_cast<uint32_t>(p.stages);
-  const uint32_t stage_bytes = p.abytes + C::kLocalN * 128;
+  const uint32_t kb_bytes = p.abytes + C::kLocalN * 128, stage_bytes = p.ks * kb_bytes;
   const auto full = [&](uint32_t s) { return smem_u32(&sh.bars[s]); };
   const auto empty = [&](uint32_t s) { return smem_u32(&sh.bars[kMaxStages + s]); };
   const auto tfull = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + a]); };
   const auto tempty = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + kMaxBufs + a]); };
-  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs]);
+  const auto sfull = [&](uint32_t i) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + i]); };
+  const auto sempty = [&](uint32_t i) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + 2 + i]); };
+  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + 4]);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&sh.abort_flag);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
@@ -202,7 +278,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     if constexpr (PAIR) return mbar_wait_cluster(bar, parity, ab, err, site, p.wait_ns);
     else return mbar_wait(bar, parity, ab, err, site, p.wait_ns);
   };
+  const auto try_now = [&](uint32_t bar, uint32_t parity) {
+    if constexpr (PAIR) return mbar_try_wait_relaxed(bar, parity);
+    else return mbar_try_wait(bar, parity);
+  };
   const auto warp_wait = [&](uint32_t bar, uint32_t parity, int site) {
+    if (__all_sync(0xFFFFFFFFu, try_now(bar, parity))) return true;
     return __all_sync(0xFFFFFFFFu, wait(bar, parity, abort_flag, site)) != 0;
   };
 
@@ -215,18 +296,23 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       mbar_init(tfull(a), 1);
       mbar_init(tempty(a), kSumWarps * C::kCtas);  // rank 0's: an arrival of every summing warp
     }
-    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sfull(i), 1);
+      mbar_init(sempty(i), kSumWarps);
+    }
+    mbar_init(drain, 2);
     fence_mbar_init();
     sh.abort_flag = 0;
-    sh.consumed = sh.peer_issued = 0u;
+    sh.peer_issued = 0u;
     tma_prefetch_desc(&p.mapB);
+    if (p.tma_out) tma_prefetch_desc(&p.mapOut);
   }
-  if (warp == 9) {
+  if (warp == kIssuer) {
     if constexpr (PAIR) tmem_alloc_pair(smem_u32(&sh.tmem), C::kTmemCols);
     else tmem_alloc(smem_u32(&sh.tmem), C::kTmemCols);
   }
   griddep_wait();
-  if (warp == 8) {  // the experts' first blocks and rows
+  if (warp == kLoader) {  // the experts' first blocks and rows
     int nb = 0, nr = 0;
     bool bad = false;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -269,150 +355,249 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   const uint32_t tmem = sh.tmem;
   const uint32_t tiles = static_cast<uint32_t>(sh.first_block[p.E]) * p.nt;
   uint32_t issued = 0;  // fills that this CTA's producer issued
-
-  if (warp == 8) {
-    uint32_t s = 0, phase = 1;
-    bool ok = blockIdx.x > 1 || ((p.withhold >> blockIdx.x) & 1u) == 0u;
-    const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
-      if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, x, y);
-      else tma_load_2d(dst, m, bar, x, y);
-    };
-    for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
-      const Tile t = decode<NT, PAIR>(p, sh, tile);
-      const CUtensorMap* ma = &p.mapA[t.box];
-      const uint32_t bytes = (8u << t.box) * 128u + C::kLocalN * 128u;
-      const int wrow = t.e * p.N + t.n0 + C::kLocalN * rank, arow = t.row0 + 128 * rank;
-      for (int kb = 0; kb < p.kt; ++kb) {
-        if (issued >= S) ok = warp_wait(empty(s), phase, 81);
-        if (!ok) break;
-        const uint32_t st = base + s * stage_bytes;
-        const uint32_t bar = PAIR ? mapa_shared(full(s), 0) : full(s);
-        if (elect_one()) {
-          sh.tx[s] = bytes;
-          if (rank == 0) mbar_arrive_expect_tx(full(s), bytes * C::kCtas);
-          load(st, ma, bar, kb * 128, arow);
-          load(st + p.abytes, &p.mapB, bar, kb * 128, wrow);
+  if (warp >= kSumWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kLoader) {
+      uint32_t s = 0, phase = 1;
+      bool ok = blockIdx.x > 1 || ((p.withhold >> blockIdx.x) & 1u) == 0u;
+      const auto load = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
+        if constexpr (PAIR) tma_load_2d_pair(dst, m, bar, x, y);
+        else tma_load_2d(dst, m, bar, x, y);
+      };
+      for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
+        const Tile t = decode<NT, PAIR>(p, sh, tile);
+        const CUtensorMap* ma = &p.mapA[t.box];
+        const uint32_t kb_tx = (8u << t.box) * 128u + C::kLocalN * 128u;
+                const int wrow = t.e * p.N + t.n0 + C::kLocalN * rank, arow = t.row0 + 128 * rank;
+        for (int k0 = 0; k0 < p.kt; k0 += p.ks) {
+          if (issued >= S) ok = warp_wait(empty(s), phase, 81);
+          if (!ok) break;
+          const int nk = min(p.ks, p.kt - k0);
+          const uint32_t bytes = nk * kb_tx;
+          const uint32_t bar = PAIR ? mapa_shared(full(s), 0) : full(s);
+          if (elect_one()) {
+            sh.tx[s] = bytes;
+            if (rank == 0) mbar_arrive_expect_tx(full(s), bytes * C::kCtas);
+            for (int j = 0; j < nk; ++j) {
+              const uint32_t st = base + s * stage_bytes + j * kb_bytes;
+              load(st, ma, bar, (k0 + j) * 128, arow);
+              load(st + p.abytes, &p.mapB, bar, (k0 + j) * 128, wrow);
+            }
+          }
+          __syncwarp();
+          ++issued;
+          if (++s == S) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        __syncwarp();
-        ++issued;
-        if (++s == S) {
-          s = 0;
-          phase ^= 1;
+      }
+    } else if (warp < kScaler && rank == 0) {
+      constexpr uint32_t idesc = idesc_e4m3_f32(C::kRows, NT);
+      uint32_t s = 0, phase = 0, a = 0, aphase = 1, group = 0;
+      bool ok = true;
+      for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
+        for (int left = p.kt; ok && left > 0; left -= C::kG, ++group) {
+          const int nk = min(C::kG, left);
+          const bool mine = (group & 1) == static_cast<uint32_t>(warp - kIssuer);
+          for (int j0 = 0; j0 < nk; j0 += p.ks) {  // ks divides kG: a stage
+            if (mine) {
+              ok = warp_wait(full(s), phase, 84);
+              if (ok && j0 == 0 && group >= C::kBufs) ok = warp_wait(tempty(a), aphase, 83);
+              if (!ok) break;
+              tc_fence_after();
+              const int n = min(p.ks, nk - j0);
+              if (elect_one()) {
+                for (int j = 0; j < n; ++j) {
+                  const uint32_t st = base + s * stage_bytes + j * kb_bytes;
+                  const uint32_t d = tmem + (a * C::kG + j0 + j) * NT;
+                  const uint64_t da = smem_desc_sw128(st, 16, 1024);
+                  const uint64_t db = smem_desc_sw128(st + p.abytes, 16, 1024);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {  // 32 values of K each
+                    if constexpr (PAIR) umma_f8_pair(d, da + 2 * i, db + 2 * i, idesc, i > 0);
+                    else umma_f8(d, da + 2 * i, db + 2 * i, idesc, i > 0);
+                  }
+                }
+                if constexpr (PAIR) {
+                  if (j0 + n == nk) umma_commit_pair(tfull(a), 3);
+                  umma_commit_pair(empty(s), 3);
+                } else {
+                  if (j0 + n == nk) umma_commit(tfull(a));
+                  umma_commit(empty(s));
+                }
+              }
+              __syncwarp();
+            }
+            if (++s == S) {
+              s = 0;
+              phase ^= 1;
+            }
+          }
+          if (++a == C::kBufs) {
+            a = 0;
+            aphase ^= 1;
+          }
+        }
+      }
+      __syncwarp();
+      if (elect_one()) {  // every MMA issued is complete before TMEM is freed
+        if constexpr (PAIR) umma_commit_pair(drain, 1);
+        else umma_commit(drain);
+      }
+      mbar_wait(drain, 0, nullptr, err, 85, p.wait_ns);
+    } else if (warp == kScaler) {
+      uint32_t slot = 0, phase = 1, fills = 0;
+      bool ok = true;
+      for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
+        const Tile t = decode<NT, PAIR>(p, sh, tile);
+        const int nrows = min(t.nvalid - 128 * rank, 128);  // none: the factors are not used
+        const float* sa = p.sa + static_cast<int64_t>(t.row0 + 128 * rank) * p.kt;
+        // columns past N take the last block's
+        const float* sb0 = p.sb + (static_cast<int64_t>(t.e) * p.nb + t.n0 / 128) * p.kt;
+        const float* sb1 = p.sb + (static_cast<int64_t>(t.e) * p.nb + min(t.n0 / 128 + 1, p.nb - 1)) * p.kt;
+        for (int k0 = 0; k0 < p.kt; k0 += kScaleBlocks) {
+          const int kb = min(k0 + (lane & 7), p.kt - 1);
+          const float b0 = __ldg(sb0 + kb), b1 = NT == 256 ? __ldg(sb1 + kb) : 0.0f;
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            const int r0 = 64 * part + (lane >> 3);
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              v[i] = r0 + 4 * i < nrows ? __ldg(sa + static_cast<int64_t>(r0 + 4 * i) * p.kt + kb) : 0.0f;
+            if (part == 0 && fills >= 2) ok = warp_wait(sempty(slot), phase, 87);
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              sh.factors[slot][0][lane & 7][r0 + 4 * i] = v[i] * b0;
+              if (NT == 256) sh.factors[slot][1][lane & 7][r0 + 4 * i] = v[i] * b1;
+            }
+          }
+          if (!ok) break;
+          __syncwarp();
+          if (lane == 0) {
+            sh.info[slot] = make_int4(t.row0, t.nvalid, t.n0, 0);
+            mbar_arrive(sfull(slot));
+          }
+          ++fills;
+          if (++slot == 2) {
+            slot = 0;
+            phase ^= 1;
+          }
         }
       }
     }
-  } else if (warp == 9 && rank == 0) {
-    constexpr uint32_t idesc = idesc_e4m3_f32(C::kRows, NT);
-    uint32_t s = 0, phase = 0, a = 0, aphase = 1, used = 0;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    constexpr int kCols = C::kCols, G = C::kG, B = C::kChunk;
+    const int q = warp & 3, part = warp >> 2, half = part * kCols / 128;
+    // addresses of this warp's TMEM lanes and columns, its factors, and the buffers' barriers
+    const uint32_t shared = base + kRingBytes + kSumWarps * kOutBytes;
+    const uint32_t tcols = tmem + part * kCols + (static_cast<uint32_t>(32 * q) << 16);
+    const uint32_t factors = shared + static_cast<uint32_t>(offsetof(Shared, factors)) +
+                             4 * ((NT == 256 ? half : 0) * (kScaleBlocks * kScaleRow) + 32 * q + lane);
+    const uint32_t out_buf = base + kRingBytes + warp * kOutBytes;
+    const uint32_t tfull0 = tfull(0);
+    const uint32_t tempty0 = PAIR ? mapa_shared(tempty(0), 0) : tempty(0);
+    uint32_t a = 0, aphase = 0, slot = 0, sphase = 0;
     bool ok = true;
     for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
-      for (int kb = 0; kb < p.kt; ++kb) {
-        if (used >= C::kBufs) ok = warp_wait(tempty(a), aphase, 83);
-        if (ok) ok = warp_wait(full(s), phase, 84);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t st = base + s * stage_bytes, d = tmem + a * NT;
-        if (elect_one()) {
-          const uint64_t da = smem_desc_sw128(st, 16, 1024);
-          const uint64_t db = smem_desc_sw128(st + p.abytes, 16, 1024);
+      if (!(ok = warp_wait(sfull(slot), sphase, 88))) break;
+      const int4 t = sh.info[slot];
+      const int r0 = 128 * rank + 32 * q, col0 = t.z + part * kCols;
+      const bool live = r0 < t.y && col0 < p.N;  // else nothing of it is stored
+      float acc[kCols];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {  // 32 values of K each
-            if constexpr (PAIR) umma_f8_pair(d, da + 2 * j, db + 2 * j, idesc, j > 0);
-            else umma_f8(d, da + 2 * j, db + 2 * j, idesc, j > 0);
+      for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+      for (int left = p.kt; left > 0; left -= kScaleBlocks) {
+        if (left < p.kt) ok = ok && warp_wait(sfull(slot), sphase, 88);
+        if (!ok) break;
+        uint32_t f = factors + slot * (2 * kScaleBlocks * kScaleRow * 4);
+#pragma unroll 1
+        for (int n = min(left, kScaleBlocks); n > 0; n -= G) {
+          // one answer for the warp: the tcgen05.ld below is .sync.aligned
+          ok = warp_wait(tfull0 + 8 * a, aphase, 86);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t ta = tcols + a * (G * NT);
+#pragma unroll
+          for (int j = 0; j < G; ++j) {
+            if (live && j < n) {
+              float scale;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(scale) : "r"(f + j * (kScaleRow * 4)));
+#pragma unroll
+              for (int c = 0; c < kCols; c += B) {
+                uint32_t v[B];
+                tmem_ld(ta + j * NT + c, v);
+                if (c + B == kCols && (j == G - 1 || j + 1 == n)) {
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster_relaxed(tempty0 + 8 * a);
+                    else mbar_arrive(tempty0 + 8 * a);
+                  }
+                }
+#pragma unroll
+                for (int i = 0; i < B; i += 2)
+                  asm("{\n\t.reg .b64 v, s, a;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
+                      "mov.b64 a, {%0, %1};\n\tfma.rn.f32x2 a, v, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
+                      : "+f"(acc[c + i]), "+f"(acc[c + i + 1])
+                      : "r"(v[i]), "r"(v[i + 1]), "f"(scale));
+              }
+            }
           }
-          if constexpr (PAIR) {
-            umma_commit_pair(empty(s), 3);
-            umma_commit_pair(tfull(a), 3);
-          } else {
-            umma_commit(empty(s));
-            umma_commit(tfull(a));
+          if (!live) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              if constexpr (PAIR) mbar_arrive_cluster_relaxed(tempty0 + 8 * a);
+              else mbar_arrive(tempty0 + 8 * a);
+            }
+          }
+          f += G * kScaleRow * 4;
+          if (++a == C::kBufs) {
+            a = 0;
+            aphase ^= 1;
           }
         }
         __syncwarp();
-        ++used;
-        if (++s == S) {
-          s = 0;
-          phase ^= 1;
-        }
-        if (++a == C::kBufs) {
-          a = 0;
-          aphase ^= 1;
+        if (lane == 0) mbar_arrive(sempty(slot));
+        if (++slot == 2) {
+          slot = 0;
+          sphase ^= 1;
         }
       }
-    }
-    __syncwarp();
-    if (elect_one()) {  // every MMA issued is complete before TMEM is freed
-      sh.consumed = used;
-      if constexpr (PAIR) umma_commit_pair(drain, 1);
-      else umma_commit(drain);
-    }
-    mbar_wait(drain, 0, nullptr, err, 85, p.wait_ns);
-  } else if (warp < kSumWarps) {
-    const int q = warp & 3, half = warp >> 2;
-    constexpr int kCols = C::kCols, kChunks = kCols / 16;
-    const uint32_t lane0 = static_cast<uint32_t>(32 * q) << 16;
-    uint32_t a = 0, aphase = 0;
-    bool ok = true;
-    for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
-      const Tile t = decode<NT, PAIR>(p, sh, tile);
-      const int r0 = 128 * rank + 32 * q, col0 = t.n0 + half * kCols;
-      const bool live = r0 < t.nvalid && col0 < p.N;  // else nothing of it is stored
-      // rows past the last valid one take its scale (it exists), columns past N the last block's
-      const float* sa = p.sa + static_cast<int64_t>(t.row0 + min(r0 + lane, t.nvalid - 1)) * p.kt;
-      const float* sb = p.sb + (static_cast<int64_t>(t.e) * p.nb + min(col0 / 128, p.nb - 1)) * p.kt;
-      uint64_t acc[kCols / 2];
-#pragma unroll
-      for (int i = 0; i < kCols / 2; ++i) acc[i] = 0ull;
-      float a0 = 0, a1 = 0, b0 = 0, b1 = 0;  // scales of this block and the next
-      if (live) {
-        a0 = __ldg(sa);
-        b0 = __ldg(sb);
-        a1 = __ldg(sa + min(1, p.kt - 1));
-        b1 = __ldg(sb + min(1, p.kt - 1));
-      }
-      for (int kb = 0; kb < p.kt; ++kb) {
-        const float scale = a0 * b0;
-        if (live) {
-          const int next = min(kb + 2, p.kt - 1);
-          a0 = a1;
-          b0 = b1;
-          a1 = __ldg(sa + next);
-          b1 = __ldg(sb + next);
-        }
-        // one answer for the warp: the tcgen05.ld below is .sync.aligned
-        ok = warp_wait(tfull(a), aphase, 86);
-        if (!ok) break;
-        tc_fence_after();
-        if (live) {
-          uint64_t s2;
-          asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "r"(__float_as_uint(scale)));
-          const uint32_t ta = tmem + a * NT + half * kCols + lane0;
-          uint32_t v[2][16];
-          tmem_ld16_start(ta, v[0]);
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) {
-            tmem_ld16_done(v[c & 1]);
-            if (c + 1 < kChunks) tmem_ld16_start(ta + 16 * (c + 1), v[(c + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], s2);
-          }
-        }
-        tc_fence_before();
+      if (ok && live) {
+        const int n = min(t.y - r0, 32), row = t.x + r0;
+        if (lane == 0) bulk_wait_read_all();  // the last tile's stores have left the buffer
         __syncwarp();
-        if (lane == 0) {
-          if constexpr (PAIR) mbar_arrive_cluster_relaxed(mapa_shared(tempty(a), 0));
-          else mbar_arrive(tempty(a));
-        }
-        if (++a == C::kBufs) {
-          a = 0;
-          aphase ^= 1;
-        }
-      }
-      if (ok && live && r0 + lane < t.nvalid) {
+        if (kCols % 64 == 0 && p.tma_out && !p.f32 && n == 32) {
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c) store16(p, t.row0 + r0 + lane, col0 + 16 * c, acc + 8 * c);
+          for (int c = 0; c < kCols / 64 * 64; c += 64) {
+            if (c * 64 >= static_cast<int>(kOutBytes)) {
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+            }
+            if (col0 + c < p.N) store_tile<64>(p, row, col0 + c, acc + c, out_buf + c * 64 % kOutBytes, lane);
+          }
+        } else if (kCols % 32 == 0 && p.tma_out && p.f32 && n == 32) {
+#pragma unroll
+          for (int c = 0; c < kCols / 32 * 32; c += 32) {
+            if (c * 128 >= static_cast<int>(kOutBytes)) {
+              if (lane == 0) bulk_wait_read_all();
+              __syncwarp();
+            }
+            if (col0 + c < p.N) store_tile<32>(p, row, col0 + c, acc + c, out_buf + c * 128 % kOutBytes, lane);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kCols; c += 16)
+            store16(p, row, n, col0 + c, acc + c, reinterpret_cast<uint32_t*>(smem_raw + (out_buf - raw)), lane);
+        }
       }
     }
+    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -420,17 +605,18 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   // CTAs exit.  With pairs all complete on rank 0's barriers: rank 1 reports its fills, rank 0
   // balances the bytes of fills that only one CTA issued and waits, then both leave together.
   if constexpr (PAIR) {
-    if (rank == 1 && warp == 8 && lane == 0) {
+    if (rank == 1 && warp == kLoader && lane == 0) {
       st_shared_cluster_u32(mapa_shared(smem_u32(&sh.peer_issued), 0), issued);
       for (uint32_t s = 0; s < S; ++s)
         st_shared_cluster_u32(mapa_shared(smem_u32(&sh.peer_tx[s]), 0), sh.tx[s]);
     }
     cluster_sync_all();
   }
-  if (rank == 0 && warp == 8 && lane == 0) {
+  if (rank == 0 && warp == kLoader && lane == 0) {
     const uint32_t peer = PAIR ? *const_cast<volatile uint32_t*>(&sh.peer_issued) : issued;
     const uint32_t end = issued > peer ? issued : peer;
-    for (uint32_t f = *const_cast<volatile uint32_t*>(&sh.consumed); f < end; ++f) {
+    // (the last S fills: earlier ones have landed, or their stages would not have been filled again)
+    for (uint32_t f = end > S ? end - S : 0; f < end; ++f) {
       const uint32_t s = f % S;
       if (f >= issued) mbar_arrive_expect_tx(full(s), sh.peer_tx[s]);
       else if (f >= peer) mbar_complete_tx(full(s), sh.tx[s]);
@@ -441,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     __syncthreads();
     cluster_sync_all();  // no load, remote arrival or MMA into the peer after this point
   }
-  if (warp == 9) {
+  if (warp == kIssuer) {
     tc_fence_after();
     if constexpr (PAIR) tmem_dealloc_pair(tmem, C::kTmemCols);
     else tmem_dealloc(tmem, C::kTmemCols);
@@ -460,6 +646,9 @@ cudaError_t launch(const Params& p, int units, cudaStream_t s) {
     st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(kSmemBytes));
     if (st != cudaSuccess) return st;
+    cudaFuncAttributes fa;  // the split of the registers has to fit the launch's
+    if ((st = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return st;
+    if (fa.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
     attr_set_mask.fetch_or(bit, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
@@ -504,13 +693,14 @@ CUtensorMap code_map(const void* base, int K, uint64_t rows, uint32_t box_rows, 
 }
 
 // Tile shapes: 256 x 256 on pairs, or 128 x 128, 64, 32 on single CTAs; by the rounds of tiles that
-// each takes over the SMs times what a block of K of a tile costs there (in cycles).  With `counts`,
+// each takes over the SMs times what a block of K of a tile costs there (in ns, measured on 8192 rows
+// of 7168 x 7168).  With `counts`,
 // which are on the device, the experts are taken to have equal shares of the rows less half a tile
 // of padding each.  MOE_FP8_SHAPE = 0 .. 3 sets the shape; every shape gives the same bits.
 struct Shape {
   int rows, n, ctas, cost;
 };
-constexpr Shape kShapes[4] = {{256, 256, 2, 560}, {128, 128, 1, 400}, {128, 64, 1, 260}, {128, 32, 1, 200}};
+constexpr Shape kShapes[4] = {{256, 256, 2, 478}, {128, 128, 1, 338}, {128, 64, 1, 280}, {128, 32, 1, 215}};
 int choose_shape(int64_t rows, int N, int E, bool grouped, int sms) {
   static const int forced = [] {
     const char* v = std::getenv("MOE_FP8_SHAPE");
@@ -545,8 +735,22 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* b, int K, int sms, c
       p.mapA[i] = code_map(a, K, static_cast<uint64_t>(p.rows), 8u << i, &st);
       p.abytes = (8u << i) * 128u;
     }
+  if (p.vec) {  // rows start on 16 bytes
+    auto enc = reinterpret_cast<Encode>(tensor_map_encoder());
+    const cuuint64_t size = p.f32 ? 4 : 2, dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.rows)};
+    const cuuint64_t strides[1] = {p.N * size};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 32}, ones[2] = {1, 1};
+    if (!enc || enc(&p.mapOut, p.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out,
+                    dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+    p.tma_out = 1;
+  }
   if (st != cudaSuccess) return st;
-  const int stages = static_cast<int>(kRingBytes / (p.abytes + C::kLocalN * 128u));
+  // as many blocks of K in a stage as leave three of them
+  const uint32_t kb_bytes = p.abytes + C::kLocalN * 128u;
+  for (p.ks = C::kG; p.ks > 1 && 3 * p.ks * kb_bytes > kRingBytes;) p.ks /= 2;
+  const int stages = static_cast<int>(kRingBytes / (p.ks * kb_bytes));
   p.stages = stages < kMaxStages ? stages : kMaxStages;
   const int64_t tiles = blocks * p.nt;  // checked by the caller to fit 31 bits
   const int units = static_cast<int>(tiles < sms / C::kCtas ? tiles : sms / C::kCtas);

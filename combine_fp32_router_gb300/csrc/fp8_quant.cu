@@ -13,13 +13,15 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kTiles = 4;  // tiles of 128 values per half warp, all loaded before the first is used
 
-// silu(a) b.  The fast exponential and reciprocal are off by some 2^-21 of the value, against the
-// 2^-4 of a code; with expf and an IEEE division the kernel would be bound by issuing them.  The
-// reciprocal of a sum near the largest fp32 is a subnormal, so silu reaches its limits on both sides.
+// silu(a) b.  The fast exponential and reciprocal keep the value to (6 + |a|) 2^-23, against the
+// 2^-4 of a code; with expf and an IEEE division the kernel would be bound by issuing them.  Both
+// flush subnormals: silu(a) is 0 below a = -87.3, where it is less than 1.1e-36 in magnitude.
 __device__ __forceinline__ float swiglu(float a, float b) {
-  float r;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-a)));
-  return (a == -INFINITY ? 0.0f : a * r) * b;
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.44269504088896340736f));  // -log2 e
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  // a = -infinity gives 0 as its neighbours do, not -infinity * 0 (a NaN stays in r)
+  return fmaxf(a, -3.402823466e38f) * r * b;
 }
 
 // ---- rows that start on 16 bytes: the matrix as tiles of 128 values, row-major; a warp takes
@@ -69,8 +71,8 @@ __global__ void __launch_bounds__(32 * kWarps)
     for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     if (live[i]) {
       const float scale = f8_scale(amax), inv = f8_inverse(scale);
-      const uint32_t lo = e4m3x2(y[0], y[1], inv) | (e4m3x2(y[2], y[3], inv) << 16);
-      const uint32_t hi = e4m3x2(y[4], y[5], inv) | (e4m3x2(y[6], y[7], inv) << 16);
+      const uint32_t lo = e4m3x4(y[0], y[1], y[2], y[3], inv);
+      const uint32_t hi = e4m3x4(y[4], y[5], y[6], y[7], inv);
       const int64_t o = static_cast<int64_t>(tile) + 2 * i;
       *reinterpret_cast<uint2*>(q + o * 128 + 8 * l) = make_uint2(lo, hi);
       if (l == 0) scales[o] = scale;
@@ -184,14 +186,17 @@ __global__ void __launch_bounds__(32 * kWarps)
   store_seg<false>(out + row * static_cast<int64_t>(cols) + c0, cols - c0, lane, r);
 }
 
-// ---- weights [E, K, N] bf16 in 128 x 128 blocks, one block per CTA: thread (k group, n) holds
-// four K rows x 8 columns twice.  Codes go as [E, N, Kp] (through shared memory: words of four
-// consecutive K, at (n, k / 4 xor n / 8) so that neither side meets a bank twice), or in the
-// weights' own order as [E, K, Np].
+// ---- weights [E, K, N] bf16 in 128 x 128 blocks, one block per CTA: a thread holds two groups of
+// four K rows x 8 columns.  Codes go as [E, N, Kp] (through shared memory), or in the weights' own
+// order as [E, K, Np].
 template <bool TRANSPOSE>
 __global__ void __launch_bounds__(256)
     quantize_blocks_kernel(const uint16_t* __restrict__ W, int K, int N, int n_tiles, int vec,
                            uint8_t* __restrict__ q, float* __restrict__ scales) {
+  // Word kg (K rows 4 kg .. 4 kg + 3) of column n = 8 c + j at
+  //   4 ((kg / 4) xor c % 8) + (kg % 4 xor 2 (c / 8)):
+  // neither a warp's words (16 c, two kg that follow each other) nor its 16-byte reads of whole rows
+  // meet in a bank.
   __shared__ uint32_t codes[TRANSPOSE ? 128 : 1][32];
   __shared__ uint32_t tops[8];
   griddep_wait();
@@ -199,16 +204,14 @@ __global__ void __launch_bounds__(256)
   const int64_t e = blockIdx.y;
   const int nb = static_cast<int>(blockIdx.x % n_tiles), kb = static_cast<int>(blockIdx.x / n_tiles);
   const int n0 = nb * 128, k0 = kb * 128;
-  const int c = lane & 15;                         // columns 8 c .. 8 c + 7
-  const int g = warp + 8 * (lane >> 4);            // K rows 4 g .. 4 g + 3, and 64 further on
+  const int c = lane & 15;  // columns 8 c .. 8 c + 7
   const uint16_t* We = W + e * K * static_cast<int64_t>(N);
   Raw8<uint16_t> v[2][4];
-  uint32_t amax = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = k0 + 64 * h + 4 * g + i;
+      const int k = k0 + 4 * (2 * (8 * h + warp) + (lane >> 4)) + i;
       const uint16_t* p = We + static_cast<int64_t>(k) * N + n0;
       const int n = k < K ? N - n0 : 0;
       if (vec) {
@@ -218,13 +221,16 @@ __global__ void __launch_bounds__(256)
         for (int j = 0; j < 8; ++j) v[h][i].v[j] = 8 * c + j < n ? __ldg(p + 8 * c + j) : uint16_t(0);
       }
     }
+  uint32_t top = 0;  // magnitudes order like their bits: two at a time
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max(amax, static_cast<uint32_t>(v[h][i].v[j]) & 0x7FFFu);
-  amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    for (int i = 0; i < 4; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(&v[h][i]);
+      constexpr uint32_t m = 0x7FFF7FFFu;
+      top = __vimax3_u16x2(top, __vimax3_u16x2(u.x & m, u.y & m, u.z & m), u.w & m);
+    }
+  uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
   if (lane == 0) tops[warp] = amax;
   __syncthreads();
 #pragma unroll
@@ -235,24 +241,24 @@ __global__ void __launch_bounds__(256)
     scales[TRANSPOSE ? (e * n_tiles + nb) * (kp / 128) + kb : (e * (kp / 128) + kb) * n_tiles + nb] = scale;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
+    const int kg = 2 * (8 * h + warp) + (lane >> 4);
     float f[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 8; ++j) f[i][j] = In<MOE_DTYPE_BF16>::f32(v[h][i].v[j]);
     if constexpr (TRANSPOSE) {
+      const int w = 4 * ((kg >> 2) ^ (c & 7)) + ((kg & 3) ^ (2 * (c >> 3)));
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        codes[8 * c + j][(16 * h + g) ^ c] =
-            e4m3x2(f[0][j], f[1][j], inv) | (e4m3x2(f[2][j], f[3][j], inv) << 16);
+      for (int j = 0; j < 8; ++j) codes[8 * c + j][w] = e4m3x4(f[0][j], f[1][j], f[2][j], f[3][j], inv);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int k = k0 + 64 * h + 4 * g + i;
+        const int k = k0 + 4 * kg + i;
         if (k < K)
-          *reinterpret_cast<uint2*>(q + (e * K + k) * np + n0 + 8 * c) = make_uint2(
-              e4m3x2(f[i][0], f[i][1], inv) | (e4m3x2(f[i][2], f[i][3], inv) << 16),
-              e4m3x2(f[i][4], f[i][5], inv) | (e4m3x2(f[i][6], f[i][7], inv) << 16));
+          *reinterpret_cast<uint2*>(q + (e * K + k) * np + n0 + 8 * c) =
+              make_uint2(e4m3x4(f[i][0], f[i][1], f[i][2], f[i][3], inv),
+                         e4m3x4(f[i][4], f[i][5], f[i][6], f[i][7], inv));
       }
     }
   }
@@ -260,11 +266,10 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int n = 32 * i + (tid >> 3), w = 4 * (tid & 7);  // 16 bytes of a row of 128
-      if (n0 + n < N)
-        st_v4(q + (e * N + n0 + n) * kp + k0 + 4 * w,
-              make_uint4(codes[n][(w + 0) ^ (n >> 3)], codes[n][(w + 1) ^ (n >> 3)],
-                         codes[n][(w + 2) ^ (n >> 3)], codes[n][(w + 3) ^ (n >> 3)]));
+      const int n = 32 * i + (tid >> 3), g = tid & 7;  // 16 bytes of a row of 128
+      uint4 u = *reinterpret_cast<const uint4*>(&codes[n][4 * (g ^ ((n >> 3) & 7))]);
+      if (i >= 2) u = make_uint4(u.z, u.w, u.x, u.y);  // n / 8 / 8 = 1
+      if (n0 + n < N) st_v4(q + (e * N + n0 + n) * kp + k0 + 16 * g, u);
     }
   }
 }

@@ -391,7 +391,7 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
  * Format of a matrix of R rows and C columns: Kp = C rounded up to a multiple of 128.
  *   codes  [R, Kp] E4M3 bytes (largest value 448); quantisers write zero codes past C.
  *   scales [R, Kp / 128] fp32: a value is code * scale.
- * scale = max(amax / 448, 2^-126) of the row's 128 columns, 1 where all are zero; the code is the
+ * scale = max(amax * (1 / 448), 2^-126) in fp32 of the row's 128 columns, 1 where all are zero; the code is the
  * E4M3 number nearest to x * (1 / scale) in fp32, ties to the even mantissa, saturating.  Columns
  * that hold an infinity or a NaN have the scale NaN and zero codes: all 128 values are NaN.
  * Weights have one scale per 128 x 128 block instead: codes [N, Kp], scales

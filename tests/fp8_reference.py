@@ -19,7 +19,7 @@ def half_step(dt):
 
 
 def scales_of(amax):
-    s = torch.clamp(amax / 448.0, min=2.0 ** -126)
+    s = torch.clamp(amax * torch.tensor(1.0 / 448.0, dtype=torch.float32), min=2.0 ** -126)
     s = torch.where(amax > 0, s, torch.ones_like(s))
     return torch.where(torch.isfinite(amax), s, torch.full_like(s, float("nan")))
 

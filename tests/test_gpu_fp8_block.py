@@ -109,7 +109,7 @@ def test_swiglu_values_that_are_not_finite(moe):
     b = torch.tensor([[nan], [2.0], [2.0], [2.0], [inf]], device=DEV).expand(5, 128)
     q, s = moe.moe_quantize_rows_fp8(torch.cat([a, b], 1).contiguous(), swiglu=True)
     assert torch.equal(torch.isnan(s[:, 0]).cpu(), torch.tensor([True, False, True, True, True]))
-    assert float(s[1, 0]) == 1.0 and int(q.max()) == 0
+    assert float(s[1, 0]) == 1.0 and int((q & 127).max()) == 0  # silu(-inf) is -0: a zero code with a sign
 
 
 @pytest.mark.parametrize("E,K,N", [(1, 1, 1), (1, 128, 128), (2, 130, 250), (3, 256, 384), (2, 1001, 129), (5, 100, 8)])
