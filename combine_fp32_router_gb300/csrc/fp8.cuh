@@ -28,6 +28,14 @@ __device__ __forceinline__ float f8_scale(uint32_t amax) {
 // 1 / scale, 0 for a NaN scale
 __device__ __forceinline__ float f8_inverse(float scale) { return scale == scale ? 1.0f / scale : 0.0f; }
 
+// The largest magnitude among eight values, as bits; a NaN if one is.
+__device__ __forceinline__ uint32_t amax8(const float (&y)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2)
+    asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(m) : "f"(y[j]), "f"(y[j + 1]));
+  return __float_as_uint(m) & 0x7FFFFFFFu;
+}
 // Codes of eight values times inv, the earlier ones in the low bytes; inv = 0 gives zeros whatever
 // the values are.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -70,13 +78,15 @@ __device__ __forceinline__ Raw8<T> load_seg(const T* seg, int n, int lane) {
   }
   return r;
 }
-template <bool VEC, typename T>
+// (STREAM: written once and not read again soon)
+template <bool VEC, bool STREAM = false, typename T>
 __device__ __forceinline__ void store_seg(T* seg, int n, int lane, const Raw8<T>& r) {
   if constexpr (VEC) {
     if (8 * lane + 8 <= n) {
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i)
-        st_v4(reinterpret_cast<char*>(seg + 8 * lane) + 16 * i, reinterpret_cast<const uint4*>(&r)[i]);
+        if constexpr (STREAM) __stcs(reinterpret_cast<uint4*>(seg + 8 * lane) + i, reinterpret_cast<const uint4*>(&r)[i]);
+        else st_v4(reinterpret_cast<char*>(seg + 8 * lane) + 16 * i, reinterpret_cast<const uint4*>(&r)[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -96,9 +106,7 @@ __device__ __forceinline__ void quantize_seg(const float (&y)[8], uint8_t* q, fl
                                              int lane) {
   // magnitudes order like their bits
   if constexpr (VEC) {
-    uint32_t amax = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(y[j]) & 0x7FFFFFFFu);
+    uint32_t amax = amax8(y);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     const float scale = f8_scale(amax), inv = f8_inverse(scale);

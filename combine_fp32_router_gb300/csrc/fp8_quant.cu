@@ -60,13 +60,12 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
     float y[8];
-    uint32_t amax = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       y[j] = In<DT>::f32(a[i].v[j]);
       if constexpr (GLU) y[j] = swiglu(y[j], In<DT>::f32(b[i].v[j]));
-      amax = max(amax, __float_as_uint(y[j]) & 0x7FFFFFFFu);
     }
+    uint32_t amax = amax8(y);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
     if (live[i]) {

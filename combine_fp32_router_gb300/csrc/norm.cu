@@ -7,6 +7,8 @@
 // and each output written once.  A row is cut into segments of 256 values, one or more per warp
 // (`V`); a segment's sum is a warp's, and the segments' sums are added in one order, so a row's
 // results do not depend on the other rows or on how many warps share it.
+#include <atomic>
+
 #include "fp8.cuh"
 #include "internal.h"
 
@@ -15,6 +17,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxSegs = 64;  // cols <= 16384
+constexpr int kStreamThreads = 512;
 
 struct NormArgs {
   const void *x, *residual, *w;
@@ -54,9 +57,63 @@ __device__ __forceinline__ float sum_parts(const float* part, int segs, int lane
   return warp_sum(v);
 }
 
+// The sum over a row of its segments' per-lane sums v: a warp's for each segment, then the segments'
+// in one order, whatever V and W are.  With several warps per row all threads synchronise once; the
+// caller alternates between two arrays `part`.
+template <int V>
+__device__ __forceinline__ float row_total(float (&v)[V], float* part, int w0, int W, int segs, int lane) {
+  // The sums of several segments at once: a step of 16 lanes leaves segment 2 i to the lanes below 16
+  // and 2 i + 1 to the others, a step of 8 then halves these; every sum is formed in warp_sum's order.
+  const bool hi = lane & 16, second = lane & 8;
+  float u = v[0];
+  if constexpr (V == 1) {
+    u += __shfl_xor_sync(0xFFFFFFFFu, u, 16);
+    u += __shfl_xor_sync(0xFFFFFFFFu, u, 8);
+  } else {
+    u = (hi ? v[1] : v[0]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? v[0] : v[1], 16);
+    if constexpr (V == 4) {
+      const float t = (hi ? v[3] : v[2]) + __shfl_xor_sync(0xFFFFFFFFu, hi ? v[2] : v[3], 16);
+      u = (second ? t : u) + __shfl_xor_sync(0xFFFFFFFFu, second ? u : t, 8);
+    } else {
+      u += __shfl_xor_sync(0xFFFFFFFFu, u, 8);
+    }
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) u += __shfl_xor_sync(0xFFFFFFFFu, u, o);
+  const int i = V == 1 ? 0 : V == 2 ? hi : 2 * second + hi;  // the segment whose sum this lane has
+  if (W == 1) {  // the order of sum_parts: one segment to a lane
+    u = __shfl_sync(0xFFFFFFFFu, u, V == 1 ? 0 : V == 2 ? (lane & 1) * 16 : (lane & 1) * 16 + (lane & 2) * 4);
+    return warp_sum(lane < V ? u : 0.0f);
+  }
+  if ((lane & (V == 1 ? 31 : V == 2 ? 15 : 7)) == 0 && w0 + i * W < segs) part[w0 + i * W] = u;
+  __syncthreads();
+  return sum_parts(part, segs, lane);
+}
+
+// The outputs of a segment: y = s rstd w in the type and in 8 bits.
+template <int DT, bool VEC>
+__device__ __forceinline__ void emit(const NormArgs& a, int64_t row, int c0, int lane,
+                                     const float (&s)[8], float rstd, const float (&w)[8]) {
+  using T = typename In<DT>::T;
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = s[j] * rstd * w[j];
+  if (a.out) {
+    Raw8<T> o;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o.v[j] = In<DT>::of(y[j]);
+    store_seg<VEC>(static_cast<T*>(a.out) + row * a.cols + c0, a.cols - c0, lane, o);
+  }
+  if (a.q) {
+    const int64_t kp = fp8_cols(a.cols);
+    quantize_seg<VEC>(y, a.q + row * kp + c0, a.scales + row * (kp / 128) + c0 / 128,
+                      static_cast<int>(kp - c0 < kSeg ? kp - c0 : kSeg), lane);
+  }
+}
+
 // One row per CTA of W warps, or (W = 1) a row per warp.
 template <int DT, int V, bool VEC>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512)
+__global__ void __launch_bounds__(1024)
     rmsnorm_kernel(const NormArgs a) {
   using T = typename In<DT>::T;
   __shared__ float part[kMaxSegs];
@@ -91,7 +148,7 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
       store_seg<VEC>(static_cast<T*>(a.sum) + at + c0, a.cols - c0, lane, s[i]);
     }
   }
-  float total = 0.0f, sq[V];
+  float sq[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     sq[i] = 0.0f;
@@ -100,42 +157,121 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
       const float f = In<DT>::f32(s[i].v[j]);
       sq[i] = fmaf(f, f, sq[i]);
     }
-    sq[i] = warp_sum(sq[i]);
   }
-  if (alone) {  // the order of sum_parts: at most 32 segments, one to a lane
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) v = lane == i ? sq[i] : v;
-    total = warp_sum(v);
-  } else {
-    if (lane == 0) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (w0 + i * a.W < segs) part[w0 + i * a.W] = sq[i];
-    }
-    __syncthreads();
-    total = sum_parts(part, segs, lane);
-  }
+  const float total = row_total<V>(sq, part, w0, a.W, segs, lane);
   const float rstd = __frsqrt_rn(total / static_cast<float>(a.cols) + a.eps);
   if (a.rstd && w0 == 0 && lane == 0) a.rstd[row] = rstd;
-  const int64_t kp = fp8_cols(a.cols);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c0 = (w0 + i * a.W) * kSeg;
     if (c0 >= a.cols) break;
-    float y[8], w[8];
+    float w[8];
     load_weights<DT, VEC>(a.w, a.w_f32, c0, a.cols, lane, w);
+    float f[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = In<DT>::f32(s[i].v[j]) * rstd * w[j];
-    if (a.out) {
-      Raw8<T> o;
+    for (int j = 0; j < 8; ++j) f[j] = In<DT>::f32(s[i].v[j]);
+    emit<DT, VEC>(a, row, c0, lane, f, rstd, w);
+  }
+}
+
+// ---- many rows that start on 16 bytes.  Persistent CTAs; the next kAhead rows are on their way to
+// shared memory (cp.async, every thread its own values, so nothing is waited for but the thread's own
+// copies) while a row is normalised.  The weights stay in registers.  16384 x 7168 bf16 with
+// residual and both outputs: 180 us, 5.9 TB/s.
+constexpr int kAhead = 2;
+// A thread's places: kAhead rows of `tensors` tensors of V segments, 16-byte pieces a CTA apart.
+template <int DT, int V>
+struct Ring {
+  static constexpr int kPieces = 8 * sizeof(typename In<DT>::T) / 16;
+  uint4* base;
+  int tensors;
+  __device__ __forceinline__ uint4* at(int slot, int t, int i) const {
+    return base + ((slot * tensors + t) * V + i) * kPieces * blockDim.x;
+  }
+  __device__ __forceinline__ void copy(int slot, int t, int i, const typename In<DT>::T* src) const {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o.v[j] = In<DT>::of(y[j]);
-      store_seg<VEC>(static_cast<T*>(a.out) + at + c0, a.cols - c0, lane, o);
+    for (int k = 0; k < kPieces; ++k)
+      cp_async_16(smem_u32(at(slot, t, i) + k * blockDim.x), reinterpret_cast<const char*>(src) + 16 * k);
+  }
+  __device__ __forceinline__ Raw8<typename In<DT>::T> get(int slot, int t, int i) const {
+    Raw8<typename In<DT>::T> r;
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) reinterpret_cast<uint4*>(&r)[k] = at(slot, t, i)[k * blockDim.x];
+    return r;
+  }
+};
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void cp_async_close() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+template <int DT, int V>
+__global__ void __launch_bounds__(kStreamThreads, V == 4 ? 1 : 2) rmsnorm_stream_kernel(const NormArgs a) {
+  using T = typename In<DT>::T;
+  constexpr int D = kAhead;
+  __shared__ float part[2][kMaxSegs];
+  extern __shared__ uint4 ring_mem[];
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool alone = a.W == 1;
+  const int w0 = alone ? 0 : warp;
+  const int segs = (a.cols + kSeg - 1) / kSeg;
+  const int64_t first = alone ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+  const int64_t step = alone ? static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) : gridDim.x;
+  const Ring<DT, V> ring{ring_mem + threadIdx.x, a.residual ? 2 : 1};
+  const auto fetch = [&](int64_t row, int slot) {
+    if (row < a.rows) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = (w0 + i * a.W) * kSeg + 8 * lane;
+        if (c < a.cols) {
+          ring.copy(slot, 0, i, static_cast<const T*>(a.x) + row * a.x_stride + c);
+          if (a.residual) ring.copy(slot, 1, i, static_cast<const T*>(a.residual) + row * a.cols + c);
+        }
+      }
     }
-    if (a.q)
-      quantize_seg<VEC>(y, a.q + row * kp + c0, a.scales + row * (kp / 128) + c0 / 128,
-                        static_cast<int>(kp - c0 < kSeg ? kp - c0 : kSeg), lane);
+    cp_async_close();
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(first + d * step, d);
+  float w[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) load_weights<DT, true>(a.w, a.w_f32, (w0 + i * a.W) * kSeg, a.cols, lane, w[i]);
+  int turn = 0, slot = 0;
+  for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
+    cp_async_wait<D - 1>();
+    float s[V][8], sq[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c0 = (w0 + i * a.W) * kSeg;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
+      if (c0 + 8 * lane < a.cols) {
+        Raw8<T> x = ring.get(slot, 0, i);
+        if (a.residual) {
+          const Raw8<T> r = ring.get(slot, 1, i);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x.v[j] = In<DT>::of(In<DT>::f32(x.v[j]) + In<DT>::f32(r.v[j]));
+          store_seg<true>(static_cast<T*>(a.sum) + row * a.cols + c0, a.cols - c0, lane, x);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] = In<DT>::f32(x.v[j]);
+      }
+      sq[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq[i] = fmaf(s[i][j], s[i][j], sq[i]);
+    }
+    fetch(row + D * step, slot);
+    if (++slot == D) slot = 0;
+    const float total = row_total<V>(sq, part[turn], w0, a.W, segs, lane);
+    const float rstd = __frsqrt_rn(total / static_cast<float>(a.cols) + a.eps);
+    if (a.rstd && w0 == 0 && lane == 0) a.rstd[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c0 = (w0 + i * a.W) * kSeg;
+      if (c0 < a.cols) emit<DT, true>(a, row, c0, lane, s[i], rstd, w[i]);
+    }
   }
 }
 
@@ -148,11 +284,44 @@ struct NormGradArgs {
   int cols, W, w_f32;
 };
 
+// A CTA's sums of dy n to its row of `part`; with a row per warp through `sums` [warps][cols].
+template <int V, bool VEC>
+__device__ __forceinline__ void flush_dw(const NormGradArgs& a, const float (&dw)[V][8], float* sums, int w0, int lane) {
+  if (!a.part) return;
+  const bool alone = a.W == 1;
+  const int warp = threadIdx.x >> 5;
+  float* mine = alone ? sums + warp * a.cols : a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c0 = (w0 + i * a.W) * kSeg;
+    Raw8<float> v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v.v[j] = dw[i][j];
+    if (alone || !VEC) {  // (rows of `sums` need not start on 16 bytes)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = c0 + (VEC ? 8 * lane + j : 32 * j + lane);
+        if (c < a.cols) mine[c] = v.v[j];
+      }
+    } else {
+      store_seg<true>(mine + c0, a.cols - c0, lane, v);
+    }
+  }
+  if (alone) {
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
+      float v = 0.0f;
+      for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v += sums[i * a.cols + c];
+      a.part[static_cast<int64_t>(blockIdx.x) * a.cols + c] = v;
+    }
+  }
+}
+
 // Each CTA (W = 1: each warp) walks over rows and keeps its columns' sums of dy n in registers; a
 // second kernel adds the CTAs' sums in their order.  The gradient of the weights is bitwise
 // reproducible on one device; it depends on the number of CTAs.
 template <int DT, int V, bool VEC>
-__global__ void __launch_bounds__(V == 1 ? 1024 : 512)
+__global__ void __launch_bounds__(1024)
     rmsnorm_backward_kernel(const NormGradArgs a) {
   using T = typename In<DT>::T;
   __shared__ float part[2][kMaxSegs];
@@ -200,24 +369,8 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
         dw[i][j] = fmaf(d, n, dw[i][j]);
         dot[i] = fmaf(d * w[j], n, dot[i]);
       }
-      dot[i] = warp_sum(dot[i]);
     }
-    float total;
-    if (alone) {
-      float v = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) v = lane == i ? dot[i] : v;
-      total = warp_sum(v);
-    } else {
-      if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (w0 + i * a.W < segs) part[turn][w0 + i * a.W] = dot[i];
-      }
-      // one barrier a row: the other half of `part` is written before the next one
-      __syncthreads();
-      total = sum_parts(part[turn], segs, lane);
-    }
+    const float total = row_total<V>(dot, part[turn], w0, a.W, segs, lane);
     const float mean = total / static_cast<float>(a.cols);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -235,32 +388,93 @@ __global__ void __launch_bounds__(V == 1 ? 1024 : 512)
       store_seg<VEC>(static_cast<T*>(a.dx) + at + c0, a.cols - c0, lane, o);
     }
   }
-  if (!a.part) return;
-  float* mine = alone ? sums + warp * a.cols : a.part + static_cast<int64_t>(blockIdx.x) * a.cols;
+  flush_dw<V, VEC>(a, dw, sums, w0, lane);
+}
+
+// The same with the next rows on their way (as in rmsnorm_stream_kernel): dy, s and dsum are read from
+// shared memory where they are used.  8192 x 4096 bf16 with dsum: 56 us, 4.8 TB/s
+// (the weights' part 4 of them; with three rows ahead an SM holds two CTAs instead of four: 73 us).
+template <int DT, int V>
+__global__ void __launch_bounds__(kStreamThreads, V == 4 ? 1 : 2)
+    rmsnorm_backward_stream_kernel(const NormGradArgs a) {
+  using T = typename In<DT>::T;
+  constexpr int D = kAhead;
+  __shared__ float part[2][kMaxSegs];
+  extern __shared__ uint4 ring_mem[];  // and, with a row per warp, their sums at the end
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool alone = a.W == 1;
+  const int w0 = alone ? 0 : warp;
+  const int segs = (a.cols + kSeg - 1) / kSeg;
+  const int64_t first = alone ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + warp : blockIdx.x;
+  const int64_t step = alone ? static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5) : gridDim.x;
+  const Ring<DT, V> ring{ring_mem + threadIdx.x, a.dsum ? 3 : 2};
+  const auto fetch = [&](int64_t row, int slot) {
+    if (row < a.rows) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = (w0 + i * a.W) * kSeg + 8 * lane;
+        const int64_t at = row * a.cols + c;
+        if (c < a.cols) {
+          ring.copy(slot, 0, i, static_cast<const T*>(a.s) + at);
+          ring.copy(slot, 1, i, static_cast<const T*>(a.dy) + at);
+          if (a.dsum) ring.copy(slot, 2, i, static_cast<const T*>(a.dsum) + at);
+        }
+      }
+    }
+    cp_async_close();
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(first + d * step, d);
+  float w[V][8], dw[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c0 = (w0 + i * a.W) * kSeg;
-    Raw8<float> v;
+    load_weights<DT, true>(a.w, a.w_f32, (w0 + i * a.W) * kSeg, a.cols, lane, w[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v.v[j] = dw[i][j];
-    if (alone || !VEC) {  // (rows of `sums` need not start on 16 bytes)
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  }
+  int turn = 0, slot = 0;
+  for (int64_t row = first; row < a.rows; row += step, turn ^= 1) {
+    const float rstd = a.rstd[row];
+    cp_async_wait<D - 1>();
+    float dot[V];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = c0 + (VEC ? 8 * lane + j : 32 * j + lane);
-        if (c < a.cols) mine[c] = v.v[j];
+    for (int i = 0; i < V; ++i) {
+      dot[i] = 0.0f;
+      if ((w0 + i * a.W) * kSeg + 8 * lane < a.cols) {
+        const Raw8<T> s = ring.get(slot, 0, i), dy = ring.get(slot, 1, i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float n = In<DT>::f32(s.v[j]) * rstd, d = In<DT>::f32(dy.v[j]);
+          dw[i][j] = fmaf(d, n, dw[i][j]);
+          dot[i] = fmaf(d * w[i][j], n, dot[i]);
+        }
       }
-    } else {
-      store_seg<true>(mine + c0, a.cols - c0, lane, v);
     }
-  }
-  if (alone) {
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) {
-      float v = 0.0f;
-      for (int i = 0; i < static_cast<int>(blockDim.x >> 5); ++i) v += sums[i * a.cols + c];
-      a.part[static_cast<int64_t>(blockIdx.x) * a.cols + c] = v;
+    const float mean = row_total<V>(dot, part[turn], w0, a.W, segs, lane) / static_cast<float>(a.cols);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c0 = (w0 + i * a.W) * kSeg;
+      if (c0 + 8 * lane < a.cols) {
+        const Raw8<T> s = ring.get(slot, 0, i), dy = ring.get(slot, 1, i);
+        Raw8<T> ds, o;
+        if (a.dsum) ds = ring.get(slot, 2, i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float n = In<DT>::f32(s.v[j]) * rstd;
+          float v = rstd * fmaf(-n, mean, In<DT>::f32(dy.v[j]) * w[i][j]);
+          if (a.dsum) v += In<DT>::f32(ds.v[j]);
+          o.v[j] = In<DT>::of(v);
+        }
+        store_seg<true>(static_cast<T*>(a.dx) + row * a.cols + c0, a.cols - c0, lane, o);
+      }
     }
+    fetch(row + D * step, slot);
+    if (++slot == D) slot = 0;
   }
+  cp_async_wait<0>();
+  flush_dw<V, true>(a, dw, reinterpret_cast<float*>(ring_mem + static_cast<size_t>(D) * ring.tensors * V *
+                                                                  Ring<DT, V>::kPieces * blockDim.x), w0, lane);
 }
 
 // dw[c] = sum over n partial rows: 32 columns a CTA, each of 32 warps every 32nd row, then the
@@ -291,54 +505,117 @@ bool known_dtype(int dt) {
 int64_t dtype_bytes(int dt) { return dt == MOE_DTYPE_F32 ? 4 : 2; }
 moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-// Segments per warp and warps per row.  Four segments keep loads of 4 x 16 bytes per lane in flight;
-// with no more rows than SMs a row is spread over as many warps as it has segments.
+// How rows are cut: segments per warp, warps per row, threads of a CTA (a row, or kAloneWarps rows of
+// one warp each).
+//   kStream  16-bit rows that start on 16 bytes, more of them than SMs: two segments a warp, four beyond
+//            32 segments.  (16384 x 7168 bf16 with residual and both outputs 180 us, 215 as kFew; fp32,
+//            8192 x 4096: 120 us, 94 as kFew, since an SM then holds few rows.)
+//   kFew     others that start on 16 bytes: a row over as many warps as it has segments, up to 32
+//   kAny     rows that do not: the same cut (16384 x 1925 fp32 80 us, 92 with four segments a warp)
+enum Path { kStream, kFew, kAny };
 struct Shape {
   int v, W, threads;
 };
-constexpr int kAloneWarps = 8;  // warps of a CTA whose warps have a row each
-Shape shape_of(int64_t rows, int cols, int sms) {
+constexpr int kAloneWarps = 8;
+Shape shape_of(Path path, int cols) {
   const int segs = (cols + kSeg - 1) / kSeg;
+  const int most = path != kStream ? (segs > 32 ? 2 : 1) : segs > 32 ? 4 : 2;
   Shape s;
   s.v = 1;
-  while (s.v < segs && s.v < 4) s.v *= 2;
-  if (rows <= sms && segs <= 32) s.v = 1;
+  while (s.v < segs && s.v < most) s.v *= 2;
   s.W = (segs + s.v - 1) / s.v;
   s.threads = 32 * (s.W == 1 ? kAloneWarps : s.W);
   return s;
 }
-int64_t grad_ctas(int64_t rows, int cols, int sms) {
-  const Shape s = shape_of(rows, cols, sms);
-  const int64_t most = s.W == 1 ? (rows + kAloneWarps - 1) / kAloneWarps : rows;
-  const int64_t per_sm = s.threads <= 256 ? 4 : s.threads <= 512 ? 2 : 1;
-  return most < per_sm * sms ? most : per_sm * sms;
+constexpr size_t kMostRing = 110000;  // two CTAs share an SM's memory
+size_t ring_bytes(const Shape& s, int tensors) {
+  return static_cast<size_t>(kAhead) * tensors * s.v * 16 * s.threads;
+}
+Path path_of(int64_t rows, int cols, int size, int tensors, bool vec, int sms) {
+  if (!vec) return kAny;
+  return size == 2 && rows > sms && ring_bytes(shape_of(kStream, cols), tensors) <= kMostRing ? kStream : kFew;
+}
+int64_t units(int64_t rows, const Shape& s) { return s.W == 1 ? (rows + kAloneWarps - 1) / kAloneWarps : rows; }
+// CTAs that walk over rows: as many as make 32 warps an SM, fewer where shared memory holds fewer.
+int64_t walkers(int64_t rows, const Shape& s, size_t smem, int sms) {
+  int64_t per_sm = 1024 / s.threads;
+  if (per_sm > 16) per_sm = 16;
+  if (smem > 0 && per_sm > static_cast<int64_t>(2 * kMostRing / smem)) per_sm = static_cast<int64_t>(2 * kMostRing / smem);
+  if (per_sm < 1) per_sm = 1;
+  const int64_t n = units(rows, s);
+  return n < per_sm * sms ? n : per_sm * sms;
+}
+int64_t most_walkers(int64_t rows, int cols, int sms) {
+  int64_t most = 0;
+  for (Path path : {kStream, kFew, kAny}) {
+    const int64_t n = walkers(rows, shape_of(path, cols), 0, sms);
+    if (n > most) most = n;
+  }
+  return most;
+}
+// Allows a kernel its dynamic shared memory (once per device).
+template <typename K>
+cudaError_t allow_smem(K kern, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t st = cudaGetDevice(&dev);
+  if (st != cudaSuccess) return st;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (bit == 0ull || !(done.load(std::memory_order_acquire) & bit)) {
+    st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(kMostRing) + 32768);  // and a CTA's sums
+    if (st != cudaSuccess) return st;
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  return cudaSuccess;
 }
 
 template <int DT, int V>
-cudaError_t launch_norm(const NormArgs& a, const Shape& s, bool vec, cudaStream_t st) {
-  const int64_t per = s.W == 1 ? kAloneWarps : 1;
-  const dim3 grid(static_cast<unsigned>((a.rows + per - 1) / per)), block(s.threads);
-  return vec ? launch_pdl(rmsnorm_kernel<DT, V, true>, grid, block, 0, st, a)
-             : launch_pdl(rmsnorm_kernel<DT, V, false>, grid, block, 0, st, a);
+cudaError_t launch_norm(const NormArgs& a, Path path, const Shape& s, int sms, cudaStream_t st) {
+  if constexpr (DT != MOE_DTYPE_F32)
+    if (path == kStream) {
+      static std::atomic<unsigned long long> done{0ull};
+      const cudaError_t e = allow_smem(rmsnorm_stream_kernel<DT, V>, done);
+      if (e != cudaSuccess) return e;
+      const size_t smem = ring_bytes(s, a.residual ? 2 : 1);
+      return launch_pdl(rmsnorm_stream_kernel<DT, V>, dim3(static_cast<unsigned>(walkers(a.rows, s, smem, sms))),
+                        dim3(s.threads), smem, st, a);
+    }
+  if constexpr (V <= 2) {
+    const dim3 grid(static_cast<unsigned>(units(a.rows, s))), block(s.threads);
+    return path == kFew ? launch_pdl(rmsnorm_kernel<DT, V, true>, grid, block, 0, st, a)
+                        : launch_pdl(rmsnorm_kernel<DT, V, false>, grid, block, 0, st, a);
+  }
+  return cudaErrorInvalidValue;
 }
 template <int DT>
-cudaError_t launch_norm(const NormArgs& a, const Shape& s, bool vec, cudaStream_t st) {
-  return s.v == 1   ? launch_norm<DT, 1>(a, s, vec, st)
-         : s.v == 2 ? launch_norm<DT, 2>(a, s, vec, st)
-                    : launch_norm<DT, 4>(a, s, vec, st);
+cudaError_t launch_norm(const NormArgs& a, Path path, const Shape& s, int sms, cudaStream_t st) {
+  return s.v == 1   ? launch_norm<DT, 1>(a, path, s, sms, st)
+         : s.v == 2 ? launch_norm<DT, 2>(a, path, s, sms, st)
+                    : launch_norm<DT, 4>(a, path, s, sms, st);
 }
+// *ctas: rows of partial sums that the launch leaves in a.part
 template <int DT, int V>
-cudaError_t launch_grad(const NormGradArgs& a, const Shape& s, int ctas, bool vec, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(ctas)), block(s.threads);
-  const size_t smem = s.W == 1 ? static_cast<size_t>(kAloneWarps) * a.cols * 4 : 0;  // <= 32 KB
-  return vec ? launch_pdl(rmsnorm_backward_kernel<DT, V, true>, grid, block, smem, st, a)
-             : launch_pdl(rmsnorm_backward_kernel<DT, V, false>, grid, block, smem, st, a);
+cudaError_t launch_grad(const NormGradArgs& a, Path path, const Shape& s, int sms, int* ctas, cudaStream_t st) {
+  const size_t sums = s.W == 1 ? static_cast<size_t>(kAloneWarps) * a.cols * 4 : 0;  // <= 32 KB
+  const size_t smem = sums + (path == kStream ? ring_bytes(s, a.dsum ? 3 : 2) : 0);
+  *ctas = static_cast<int>(walkers(a.rows, s, smem, sms));
+  const dim3 grid(static_cast<unsigned>(*ctas)), block(s.threads);
+  if constexpr (DT != MOE_DTYPE_F32)
+    if (path == kStream) {
+      static std::atomic<unsigned long long> done{0ull};
+      const cudaError_t e = allow_smem(rmsnorm_backward_stream_kernel<DT, V>, done);
+      return e != cudaSuccess ? e : launch_pdl(rmsnorm_backward_stream_kernel<DT, V>, grid, block, smem, st, a);
+    }
+  if constexpr (V <= 2)
+    return path == kFew ? launch_pdl(rmsnorm_backward_kernel<DT, V, true>, grid, block, smem, st, a)
+                        : launch_pdl(rmsnorm_backward_kernel<DT, V, false>, grid, block, smem, st, a);
+  return cudaErrorInvalidValue;
 }
 template <int DT>
-cudaError_t launch_grad(const NormGradArgs& a, const Shape& s, int ctas, bool vec, cudaStream_t st) {
-  return s.v == 1   ? launch_grad<DT, 1>(a, s, ctas, vec, st)
-         : s.v == 2 ? launch_grad<DT, 2>(a, s, ctas, vec, st)
-                    : launch_grad<DT, 4>(a, s, ctas, vec, st);
+cudaError_t launch_grad(const NormGradArgs& a, Path path, const Shape& s, int sms, int* ctas, cudaStream_t st) {
+  return s.v == 1   ? launch_grad<DT, 1>(a, path, s, sms, ctas, st)
+         : s.v == 2 ? launch_grad<DT, 2>(a, path, s, sms, ctas, st)
+                    : launch_grad<DT, 4>(a, path, s, sms, ctas, st);
 }
 
 }  // namespace
@@ -372,17 +649,19 @@ moe_status_t moe_rmsnorm(const void* x, int64_t x_stride, const void* residual, 
                    aligned16(out) && aligned16(weight);
   const NormArgs a{x,     residual, weight, sum_out,  out,  q, scales, rstd,
                    rows,  x_stride, cols,   0,        weight_dtype == MOE_DTYPE_F32, eps};
-  const Shape s = shape_of(rows, cols, num_sms_of_current_device());
+  const int sms = num_sms_of_current_device();
+  const Path path = path_of(rows, cols, size, residual ? 2 : 1, vec, sms);
+  const Shape s = shape_of(path, cols);
   NormArgs b = a;
   b.W = s.W;
-  return cuda_status(dtype == MOE_DTYPE_BF16  ? launch_norm<MOE_DTYPE_BF16>(b, s, vec, stream)
-                     : dtype == MOE_DTYPE_F16 ? launch_norm<MOE_DTYPE_F16>(b, s, vec, stream)
-                                              : launch_norm<MOE_DTYPE_F32>(b, s, vec, stream));
+  return cuda_status(dtype == MOE_DTYPE_BF16  ? launch_norm<MOE_DTYPE_BF16>(b, path, s, sms, stream)
+                     : dtype == MOE_DTYPE_F16 ? launch_norm<MOE_DTYPE_F16>(b, path, s, sms, stream)
+                                              : launch_norm<MOE_DTYPE_F32>(b, path, s, sms, stream));
 }
 
 size_t moe_rmsnorm_workspace_bytes(int64_t rows, int cols) {
   if (rows < 0 || cols < 1 || cols > kMaxSegs * kSeg || rows > INT32_MAX) return 0;
-  const int64_t n = grad_ctas(rows, cols, num_sms_of_current_device());
+  const int64_t n = most_walkers(rows, cols, num_sms_of_current_device());
   const int64_t bytes = (n * cols * 4 + 255) / 256 * 256;
   return static_cast<size_t>(bytes < 256 ? 256 : bytes);
 }
@@ -408,15 +687,16 @@ moe_status_t moe_rmsnorm_backward(const void* dy, const void* s, const void* wei
   if (rows == 0)
     return dweight ? cuda_status(cudaMemsetAsync(dweight, 0, 4ull * cols, stream)) : MOE_OK;
   const int sms = num_sms_of_current_device();
-  const Shape sh = shape_of(rows, cols, sms);
-  const int ctas = static_cast<int>(grad_ctas(rows, cols, sms));
   const bool vec = cols % 8 == 0 && aligned16(dy) && aligned16(s) && aligned16(dsum) &&
                    aligned16(dx) && aligned16(weight);
+  const Path path = path_of(rows, cols, size, dsum ? 3 : 2, vec, sms);
+  const Shape sh = shape_of(path, cols);
+  int ctas = 0;
   const NormGradArgs a{dy,   s,    weight, dsum, rstd, dx, dweight ? static_cast<float*>(ws) : nullptr,
                        rows, cols, sh.W,   weight_dtype == MOE_DTYPE_F32};
-  cudaError_t st = dtype == MOE_DTYPE_BF16  ? launch_grad<MOE_DTYPE_BF16>(a, sh, ctas, vec, stream)
-                   : dtype == MOE_DTYPE_F16 ? launch_grad<MOE_DTYPE_F16>(a, sh, ctas, vec, stream)
-                                            : launch_grad<MOE_DTYPE_F32>(a, sh, ctas, vec, stream);
+  cudaError_t st = dtype == MOE_DTYPE_BF16  ? launch_grad<MOE_DTYPE_BF16>(a, path, sh, sms, &ctas, stream)
+                   : dtype == MOE_DTYPE_F16 ? launch_grad<MOE_DTYPE_F16>(a, path, sh, sms, &ctas, stream)
+                                            : launch_grad<MOE_DTYPE_F32>(a, path, sh, sms, &ctas, stream);
   if (st == cudaSuccess && dweight)
     st = launch_pdl(rmsnorm_dweight_kernel, dim3((cols + 31) / 32), dim3(1024), 0, stream,
                     static_cast<const float*>(ws), ctas, cols, dweight);
