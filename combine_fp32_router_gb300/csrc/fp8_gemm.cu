@@ -3,7 +3,7 @@
 // rows grouped by expert in 128-row segments, or one matrix.
 //
 // One persistent launch.  A tile is 256 x 256 on a CTA pair (cta_group::2: each CTA holds 128 rows
-// and half of the weights) or 128 rows x 128, 64 or 32 weight rows on one CTA.  The tensor cores
+// and half of the weights) or 128 rows x 128 or 64, or 64 rows x 32 weight rows on one CTA.  The tensor cores
 // (tcgen05.mma kind::f8f6f4) sum the 128 values of a block of K into TMEM; scales differ from block
 // to block, so the sum of each block is taken out of TMEM, scaled and added to the tile's sums, which
 // stay in registers:  acc = fma(sum, sa sb, acc), two values an instruction.  Every shape adds the
@@ -54,10 +54,13 @@ constexpr int kScaleBlocks = 8, kScaleRow = 132;
 template <int NT, bool PAIR>
 struct Cfg {
   static constexpr int kCtas = PAIR ? 2 : 1;
-  static constexpr int kRows = 128 * kCtas;     // rows of a tile
+  // Rows of a CTA's MMAs.  Few columns go with few rows: 64 rows take 96 cycles a block of K with 32
+  // columns, 128 take 160.  64 rows lie in lanes 0 .. 15 of each of the four quarters of TMEM.
+  static constexpr int kM = NT == 32 ? 64 : 128;
+  static constexpr int kRows = kM * kCtas;      // rows of a tile
   static constexpr int kLocalN = NT / kCtas;    // weight rows that a CTA loads
   static constexpr int kCols = NT / 2;          // columns of a warp's sums
-  static constexpr int kChunk = kCols < 32 ? kCols : 32;  // of them taken at a time
+  static constexpr int kChunk = kCols < 16 ? kCols : 16;  // of them taken at a time
   // Blocks of K between two arrivals of the summing warps, and at most per stage: an MMA warp's turn
   // (wait, issue, commit) takes 350 cycles, the MMAs of a block 160 with 32 columns, 256 with 128
   static constexpr int kG = NT == 32 ? 4 : NT == 256 ? 1 : 2;
@@ -137,7 +140,7 @@ __device__ __forceinline__ bool mbar_try_wait_relaxed(uint32_t bar, uint32_t par
 }
 
 // 32 or 16 columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -148,6 +151,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_done(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
@@ -158,7 +163,7 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) {
                :
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -166,6 +171,8 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_done(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
@@ -218,6 +225,7 @@ __device__ __forceinline__ void store16(const Params& p, int64_t row, int n, int
   __syncwarp();
   const int c = lane & 15;
   if (col + c < p.N) {
+#pragma unroll 8
     for (int r = lane >> 4; r < n; r += 2) {
       const int64_t at = (row + r) * p.N + col + c;
       if (p.f32) static_cast<uint32_t*>(p.out)[at] = buf[r * 17 + c];
@@ -496,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     const uint32_t shared = base + kRingBytes + kSumWarps * kOutBytes;
     const uint32_t tcols = tmem + part * kCols + (static_cast<uint32_t>(32 * q) << 16);
     const uint32_t factors = shared + static_cast<uint32_t>(offsetof(Shared, factors)) +
-                             4 * ((NT == 256 ? half : 0) * (kScaleBlocks * kScaleRow) + 32 * q + lane);
+                             4 * ((NT == 256 ? half : 0) * (kScaleBlocks * kScaleRow) + C::kM / 4 * q + lane);
     const uint32_t out_buf = base + kRingBytes + warp * kOutBytes;
     const uint32_t tfull0 = tfull(0);
     const uint32_t tempty0 = PAIR ? mapa_shared(tempty(0), 0) : tempty(0);
@@ -505,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
       if (!(ok = warp_wait(sfull(slot), sphase, 88))) break;
       const int4 t = sh.info[slot];
-      const int r0 = 128 * rank + 32 * q, col0 = t.z + part * kCols;
+      const int r0 = 128 * rank + C::kM / 4 * q, col0 = t.z + part * kCols;
       const bool live = r0 < t.y && col0 < p.N;  // else nothing of it is stored
       float acc[kCols];
 #pragma unroll
@@ -526,10 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
             if (live && j < n) {
               float scale;
               asm volatile("ld.shared.f32 %0, [%1];" : "=f"(scale) : "r"(f + j * (kScaleRow * 4)));
+              uint32_t v[2][B];
+              tmem_start(ta + j * NT, v[0]);
 #pragma unroll
               for (int c = 0; c < kCols; c += B) {
-                uint32_t v[B];
-                tmem_ld(ta + j * NT + c, v);
+                const int b = c / B & 1;
+                tmem_done(v[b]);
+                if (c + B < kCols) tmem_start(ta + j * NT + c + B, v[b ^ 1]);
                 if (c + B == kCols && (j == G - 1 || j + 1 == n)) {
                   tc_fence_before();
                   __syncwarp();
@@ -543,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
                   asm("{\n\t.reg .b64 v, s, a;\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %4};\n\t"
                       "mov.b64 a, {%0, %1};\n\tfma.rn.f32x2 a, v, s, a;\n\tmov.b64 {%0, %1}, a;\n\t}"
                       : "+f"(acc[c + i]), "+f"(acc[c + i + 1])
-                      : "r"(v[i]), "r"(v[i + 1]), "f"(scale));
+                      : "r"(v[b][i]), "r"(v[b][i + 1]), "f"(scale));
               }
             }
           }
@@ -569,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         }
       }
       if (ok && live) {
-        const int n = min(t.y - r0, 32), row = t.x + r0;
+        const int n = min(t.y - r0, C::kM / 4), row = t.x + r0;
         if (lane == 0) bulk_wait_read_all();  // the last tile's stores have left the buffer
         __syncwarp();
         if (kCols % 64 == 0 && p.tma_out && !p.f32 && n == 32) {
@@ -692,7 +703,7 @@ CUtensorMap code_map(const void* base, int K, uint64_t rows, uint32_t box_rows, 
   return m;
 }
 
-// Tile shapes: 256 x 256 on pairs, or 128 x 128, 64, 32 on single CTAs; by the rounds of tiles that
+// Tile shapes: 256 x 256 on pairs, or 128 x 128, 128 x 64 or 64 x 32 on single CTAs; by the rounds of tiles that
 // each takes over the SMs times what a block of K of a tile costs there (in ns, measured on 8192 rows
 // of 7168 x 7168).  With `counts`,
 // which are on the device, the experts are taken to have equal shares of the rows less half a tile
@@ -700,7 +711,8 @@ CUtensorMap code_map(const void* base, int K, uint64_t rows, uint32_t box_rows, 
 struct Shape {
   int rows, n, ctas, cost;
 };
-constexpr Shape kShapes[4] = {{256, 256, 2, 478}, {128, 128, 1, 338}, {128, 64, 1, 280}, {128, 32, 1, 215}};
+constexpr int kNumShapes = 4;
+constexpr Shape kShapes[kNumShapes] = {{256, 256, 2, 446}, {128, 128, 1, 340}, {128, 64, 1, 280}, {64, 32, 1, 160}};
 int choose_shape(int64_t rows, int N, int E, bool grouped, int sms) {
   static const int forced = [] {
     const char* v = std::getenv("MOE_FP8_SHAPE");
@@ -711,7 +723,7 @@ int choose_shape(int64_t rows, int N, int E, bool grouped, int sms) {
   const int64_t share = (rows + E - 1) / E;
   int best = 0;
   int64_t least = INT64_MAX;
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kNumShapes; ++i) {
     const Shape& s = kShapes[i];
     const int64_t tiles = E * ((share + s.rows - 1) / s.rows) * ((N + s.n - 1) / s.n);
     const int64_t units = sms / s.ctas, cost = (tiles + units - 1) / units * s.cost;
@@ -730,7 +742,7 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* b, int K, int sms, c
   const int64_t blocks = (p.rows + C::kRows - 1) / C::kRows + (p.counts ? p.E : 0);
   p.nt = (p.N + NT - 1) / NT;
   p.mapB = code_map(b, K, static_cast<uint64_t>(p.E) * p.N, C::kLocalN, &st);
-  for (int i = 0; i < kBoxes; ++i)  // no block has more than `rows`
+  for (int i = 0; i < kBoxes && (8 << i) <= C::kM; ++i)  // no block has more than `rows`
     if (i == 0 || p.rows > (4 << i)) {
       p.mapA[i] = code_map(a, K, static_cast<uint64_t>(p.rows), 8u << i, &st);
       p.abytes = (8u << i) * 128u;
@@ -779,8 +791,8 @@ moe_status_t moe_gemm_fp8(const uint8_t* a, const float* a_scales, int64_t rows,
   if (E > kMaxE || N > kMaxFp8Cols || K > kMaxFp8Cols || rows > INT32_MAX - 256 ||
       static_cast<int64_t>(E) * N > INT32_MAX - 256)  // rows of a tile past the last expert count too
     return MOE_ERR_UNSUPPORTED;
-  // tiles of 128 x 32 at the least
-  if (((rows + 127) / 128 + E) * ((N + 31) / 32) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  // tiles of 64 x 32 at the least
+  if (((rows + 63) / 64 + E) * ((N + 31) / 32) > INT32_MAX) return MOE_ERR_UNSUPPORTED;
   Params p = {};
   p.counts = counts;
   p.sa = a_scales;

@@ -435,13 +435,13 @@ moe_status_t moe_quantize_blocks_fp8(const moe_bf16_t* W, int E, int K, int N, i
  *            sum_{j<e} round_up(counts[j], 128) (moe_sort_tokens's layout); rows between the
  *            segments are left as they were.
  * Any rows, N, K >= 1 (rows = 0 writes nothing) with E <= 1024, N and K <= 2^20,
- * E * N < 2^31 - 256 and (ceil(rows / 128) + E) * ceil(N / 32) < 2^31, else MOE_ERR_UNSUPPORTED.
+ * E * N < 2^31 - 256 and (ceil(rows / 64) + E) * ceil(N / 32) < 2^31, else MOE_ERR_UNSUPPORTED.
  * Counts that are negative or do not fit `rows` record MOE_ERR_DEVICE_BOUNDS and nothing is
  * written; device-side problems are read with moe_gemm_fp8_get_error, which synchronises `stream`,
  * returns the first one recorded on the current device since the last call, and clears it in the
  * same step.  The record is the device's: products on other streams share it, and of several
  * callers one gets an error.  MOE_FP8_SHAPE (environment, read once per process): 0 to 3 sets the
- * tile shape (256 x 256, 128 x 128, 128 x 64, 128 x 32), which changes no bit of a result.
+ * tile shape (256 x 256, 128 x 128, 128 x 64, 64 x 32), which changes no bit of a result.
  */
 moe_status_t moe_gemm_fp8(const uint8_t* a, const float* a_scales, int64_t rows,
                           const int32_t* counts, const uint8_t* b, const float* b_scales, int E,
