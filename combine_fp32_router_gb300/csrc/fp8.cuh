@@ -99,37 +99,68 @@ __device__ __forceinline__ void store_seg(T* seg, int n, int lane, const Raw8<T>
   }
 }
 
-// The 8-bit form of a warp's segment (two blocks; the values past the row's end are zeros): codes
-// to q, np of them (a multiple of 128, up to 256), and scales to s.  q is 8-byte aligned.
-template <bool VEC>
-__device__ __forceinline__ void quantize_seg(const float (&y)[8], uint8_t* q, float* s, int np,
-                                             int lane) {
-  // magnitudes order like their bits
-  if constexpr (VEC) {
-    uint32_t amax = amax8(y);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    const float scale = f8_scale(amax), inv = f8_inverse(scale);
-    if (8 * lane < np) {
-      const uint32_t lo = e4m3x4(y[0], y[1], y[2], y[3], inv);
-      const uint32_t hi = e4m3x4(y[4], y[5], y[6], y[7], inv);
-      *reinterpret_cast<uint2*>(q + 8 * lane) = make_uint2(lo, hi);
-      if ((lane & 15) == 0) s[lane >> 4] = scale;
+// The largest magnitudes of V blocks at a time (as bits; m[i]: this lane's part of block i of its half
+// warp) and their scales.  A step of 8 lanes, and with four blocks one of 4, leaves each lane with one
+// block, so that a scale and its reciprocal are computed once for V blocks: the scale of block
+// which(lane), and every block's reciprocal.
+template <int V>
+struct Scales {
+  float scale, inv[V];
+  static __device__ __forceinline__ int which(int lane) {
+    return V == 1 ? 0 : V == 2 ? (lane >> 3) & 1 : (lane >> 2) & 3;
+  }
+  // one lane per block
+  static __device__ __forceinline__ bool stores(int lane) {
+    return (lane & (V == 1 ? 15 : V == 2 ? 7 : 3)) == 0;
+  }
+  __device__ __forceinline__ Scales(const uint32_t (&m)[V], int lane) {
+    constexpr uint32_t kAll = 0xFFFFFFFFu;
+    uint32_t a = m[0];
+    if constexpr (V == 1) {
+      a = max(a, __shfl_xor_sync(kAll, a, 8));
+      a = max(a, __shfl_xor_sync(kAll, a, 4));
+    } else if constexpr (V == 2) {
+      const bool h = lane & 8;
+      a = max(h ? m[1] : m[0], __shfl_xor_sync(kAll, h ? m[0] : m[1], 8));
+      a = max(a, __shfl_xor_sync(kAll, a, 4));
+    } else {
+      const bool h = lane & 8, g = lane & 4;
+      const uint32_t b = max(h ? m[2] : m[0], __shfl_xor_sync(kAll, h ? m[0] : m[2], 8));
+      const uint32_t c = max(h ? m[3] : m[1], __shfl_xor_sync(kAll, h ? m[1] : m[3], 8));
+      a = max(g ? c : b, __shfl_xor_sync(kAll, g ? b : c, 4));
     }
-  } else {
+    a = max(a, __shfl_xor_sync(kAll, a, 2));
+    a = max(a, __shfl_xor_sync(kAll, a, 1));
+    scale = f8_scale(a);
+    const float own = f8_inverse(scale);
+    if constexpr (V == 1) {
+      inv[0] = own;
+    } else {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      uint32_t amax = 0;
+      for (int i = 0; i < V; ++i) inv[i] = __shfl_sync(kAll, own, (lane & 16) | (i * (16 / V)));
+    }
+  }
+};
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
+  return make_uint2(e4m3x4(y[0], y[1], y[2], y[3], inv), e4m3x4(y[4], y[5], y[6], y[7], inv));
+}
+
+// The 8-bit form of a warp's segment (two blocks; the values past the row's end are zeros), neighbouring
+// lanes holding neighbouring values: codes to q, np of them (a multiple of 128, up to 256), and scales
+// to s.
+__device__ __forceinline__ void quantize_seg(const float (&y)[8], uint8_t* q, float* s, int np, int lane) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(y[4 * b + j]) & 0x7FFFFFFFu);
-      amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-      const float scale = f8_scale(amax), inv = f8_inverse(scale);
-      if (128 * b < np) {
-        const uint32_t c = e4m3x4(y[4 * b], y[4 * b + 1], y[4 * b + 2], y[4 * b + 3], inv);
+  for (int b = 0; b < 2; ++b) {
+    uint32_t amax = 0;  // magnitudes order like their bits
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[32 * (4 * b + j) + lane] = static_cast<uint8_t>(c >> (8 * j));
-        if (lane == 0) s[b] = scale;
-      }
+    for (int j = 0; j < 4; ++j) amax = max(amax, __float_as_uint(y[4 * b + j]) & 0x7FFFFFFFu);
+    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    const float scale = f8_scale(amax), inv = f8_inverse(scale);
+    if (128 * b < np) {
+      const uint32_t c = e4m3x4(y[4 * b], y[4 * b + 1], y[4 * b + 2], y[4 * b + 3], inv);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[32 * (4 * b + j) + lane] = static_cast<uint8_t>(c >> (8 * j));
+      if (lane == 0) s[b] = scale;
     }
   }
 }

@@ -57,26 +57,25 @@ __global__ void __launch_bounds__(32 * kWarps)
     if constexpr (GLU) b[i] = load8(v + cols, n, l);
     at.step(kt);
   }
+  float y[kTiles][8];
+  uint32_t m[kTiles], alive = 0;
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
-    float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      y[j] = In<DT>::f32(a[i].v[j]);
-      if constexpr (GLU) y[j] = swiglu(y[j], In<DT>::f32(b[i].v[j]));
+      y[i][j] = In<DT>::f32(a[i].v[j]);
+      if constexpr (GLU) y[i][j] = swiglu(y[i][j], In<DT>::f32(b[i].v[j]));
     }
-    uint32_t amax = amax8(y);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-    if (live[i]) {
-      const float scale = f8_scale(amax), inv = f8_inverse(scale);
-      const uint32_t lo = e4m3x4(y[0], y[1], y[2], y[3], inv);
-      const uint32_t hi = e4m3x4(y[4], y[5], y[6], y[7], inv);
-      const int64_t o = static_cast<int64_t>(tile) + 2 * i;
-      *reinterpret_cast<uint2*>(q + o * 128 + 8 * l) = make_uint2(lo, hi);
-      if (l == 0) scales[o] = scale;
-    }
+    m[i] = amax8(y[i]);
+    alive |= static_cast<uint32_t>(live[i]) << i;
   }
+  const Scales<kTiles> s(m, lane);
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i)
+    if (live[i])
+      *reinterpret_cast<uint2*>(q + (static_cast<int64_t>(tile) + 2 * i) * 128 + 8 * l) = codes8(y[i], s.inv[i]);
+  const int own = s.which(lane);
+  if (s.stores(lane) && (alive >> own & 1)) scales[static_cast<int64_t>(tile) + 2 * own] = s.scale;
 }
 
 // A value = code * scale, rounded once.
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = swiglu(y[j], In<DT>::f32(b.v[j]));
   }
-  quantize_seg<false>(y, q + row * kp + c0, scales + row * (kp / 128) + c0 / 128,
+  quantize_seg(y, q + row * kp + c0, scales + row * (kp / 128) + c0 / 128,
                       static_cast<int>(kp - c0 < kSeg ? kp - c0 : kSeg), lane);
 }
 template <int DT>

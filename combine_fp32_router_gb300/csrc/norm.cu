@@ -90,30 +90,47 @@ __device__ __forceinline__ float row_total(float (&v)[V], float* part, int w0, i
   return sum_parts(part, segs, lane);
 }
 
-// The outputs of a segment: y = s rstd w in the type and in 8 bits.
-template <int DT, bool VEC>
-__device__ __forceinline__ void emit(const NormArgs& a, int64_t row, int c0, int lane,
-                                     const float (&s)[8], float rstd, const float (&w)[8]) {
+// The outputs of a warp's segments (the i-th from column c0 + i step on): y = s rstd w in the type and in
+// 8 bits.
+template <int DT, int V, bool VEC>
+__device__ __forceinline__ void emit(const NormArgs& a, int64_t row, int c0, int step, int lane,
+                                     float (&y)[V][8], float rstd, const float (&w)[V][8]) {
   using T = typename In<DT>::T;
-  float y[8];
+  const int64_t kp = fp8_cols(a.cols);
+  uint8_t* q = a.q + row * kp;
+  float* scales = a.scales + row * (kp / 128);
+  uint32_t m[V];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = s[j] * rstd * w[j];
-  if (a.out) {
-    Raw8<T> o;
+  for (int i = 0; i < V; ++i) {
+    const int c = c0 + i * step;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o.v[j] = In<DT>::of(y[j]);
-    store_seg<VEC>(static_cast<T*>(a.out) + row * a.cols + c0, a.cols - c0, lane, o);
+    for (int j = 0; j < 8; ++j) y[i][j] = y[i][j] * rstd * w[i][j];
+    if (a.out && c < a.cols) {
+      Raw8<T> o;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o.v[j] = In<DT>::of(y[i][j]);
+      store_seg<VEC>(static_cast<T*>(a.out) + row * a.cols + c, a.cols - c, lane, o);
+    }
+    if constexpr (VEC) m[i] = amax8(y[i]);
+    else if (a.q && c < a.cols)
+      quantize_seg(y[i], q + c, scales + c / 128, static_cast<int>(kp - c < kSeg ? kp - c : kSeg), lane);
   }
-  if (a.q) {
-    const int64_t kp = fp8_cols(a.cols);
-    quantize_seg<VEC>(y, a.q + row * kp + c0, a.scales + row * (kp / 128) + c0 / 128,
-                      static_cast<int>(kp - c0 < kSeg ? kp - c0 : kSeg), lane);
+  if constexpr (VEC) {
+    if (!a.q) return;
+    const Scales<V> s(m, lane);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = c0 + i * step + 8 * lane;
+      if (c < kp) *reinterpret_cast<uint2*>(q + c) = codes8(y[i], s.inv[i]);
+    }
+    const int b = (c0 + s.which(lane) * step) / 128 + (lane >> 4);
+    if (s.stores(lane) && b < kp / 128) scales[b] = s.scale;
   }
 }
 
 // One row per CTA of W warps, or (W = 1) a row per warp.
 template <int DT, int V, bool VEC>
-__global__ void __launch_bounds__(1024)
+__global__ void __launch_bounds__(1024, V == 1 ? 2 : 1)
     rmsnorm_kernel(const NormArgs a) {
   using T = typename In<DT>::T;
   __shared__ float part[kMaxSegs];
@@ -161,17 +178,14 @@ __global__ void __launch_bounds__(1024)
   const float total = row_total<V>(sq, part, w0, a.W, segs, lane);
   const float rstd = __frsqrt_rn(total / static_cast<float>(a.cols) + a.eps);
   if (a.rstd && w0 == 0 && lane == 0) a.rstd[row] = rstd;
+  float y[V][8], w[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c0 = (w0 + i * a.W) * kSeg;
-    if (c0 >= a.cols) break;
-    float w[8];
-    load_weights<DT, VEC>(a.w, a.w_f32, c0, a.cols, lane, w);
-    float f[8];
+    load_weights<DT, VEC>(a.w, a.w_f32, (w0 + i * a.W) * kSeg, a.cols, lane, w[i]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = In<DT>::f32(s[i].v[j]);
-    emit<DT, VEC>(a, row, c0, lane, f, rstd, w);
+    for (int j = 0; j < 8; ++j) y[i][j] = In<DT>::f32(s[i].v[j]);
   }
+  emit<DT, V, VEC>(a, row, w0 * kSeg, a.W * kSeg, lane, y, rstd, w);
 }
 
 // ---- many rows that start on 16 bytes.  Persistent CTAs; the next kAhead rows are on their way to
@@ -267,11 +281,7 @@ __global__ void __launch_bounds__(kStreamThreads, V == 4 ? 1 : 2) rmsnorm_stream
     const float total = row_total<V>(sq, part[turn], w0, a.W, segs, lane);
     const float rstd = __frsqrt_rn(total / static_cast<float>(a.cols) + a.eps);
     if (a.rstd && w0 == 0 && lane == 0) a.rstd[row] = rstd;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c0 = (w0 + i * a.W) * kSeg;
-      if (c0 < a.cols) emit<DT, true>(a, row, c0, lane, s[i], rstd, w[i]);
-    }
+    emit<DT, V, true>(a, row, w0 * kSeg, a.W * kSeg, lane, s, rstd, w);
   }
 }
 
