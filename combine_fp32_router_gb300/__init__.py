@@ -449,12 +449,15 @@ _F32, _I32 = torch.float32, torch.int32
 _CODES8 = (torch.uint8, torch.float8_e4m3fn)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _device_of(t):
     """The index of the tensor's device, which has to be the current one: the launches go there."""
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensor arguments must be CUDA tensors")
-    if dev != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError("the tensors are on cuda:%d, which is not the current device" % dev)
     return dev
 
@@ -472,6 +475,15 @@ def _arg(t, dev, name, dtype, numel):
     if t.numel() != numel or not t.is_contiguous():
         raise ValueError("%s must hold %d values and be contiguous: got %s with strides %s" %
                          (name, numel, tuple(t.shape), t.stride()))
+    return t.data_ptr()
+
+
+def _buffer(t, dev, name, least):
+    """Address of a contiguous tensor of any type with `least` bytes or more on device `dev`."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor on the device of the others" % name)
+    if t.nbytes < least:
+        raise ValueError("%s must hold %d bytes or more: got %d" % (name, least, t.nbytes))
     return t.data_ptr()
 
 
@@ -631,7 +643,7 @@ def moe_rmsnorm_backward(dy, s, weight, rstd, dx, dweight, ws, dsum=None, stream
     t, n, dev = dy.dtype, rows * cols, _device_of(dy)
     dt = _dtype(t)
     wt = weight.dtype
-    wsa, wsb = (None, 0) if ws is None else (_addr(ws), _nbytes(ws))
+    wsa, wsb = (None, 0) if ws is None else (_buffer(ws, dev, "ws", 0), ws.nbytes)
     st = _lib.moe_rmsnorm_backward(_arg(dy, dev, "dy", t, n), _arg(s, dev, "s", t, n),
                                    _arg(weight, dev, "weight", (t, _F32), cols),
                                    _arg(rstd, dev, "rstd", _F32, rows),
@@ -677,8 +689,8 @@ def moe_sort_tokens(x, topk_idx, rows, counts, perm, pos, ws, x_scales=None, row
                               _arg(rows_scales, dev, "rows_scales", _F32, n_rows * ns),
                               _arg(counts, dev, "counts", _I32, E),
                               _arg(perm, dev, "perm", _I32, n_rows),
-                              _arg(pos, dev, "pos", _I32, T * k), _addr(ws), _nbytes(ws),
-                              _raw_stream(stream, x))
+                              _arg(pos, dev, "pos", _I32, T * k), _buffer(ws, dev, "ws", 0),
+                              ws.nbytes, _raw_stream(stream, x))
     if st:
         raise MoeError(st, "moe_sort_tokens")
 
@@ -695,7 +707,8 @@ def moe_sort_tokens_backward(drows, pos, dx, err_word, stream=None):
     t, dev = drows.dtype, _device_of(drows)
     st = _lib.moe_sort_tokens_backward(_arg(drows, dev, "drows", t, n_rows * d), _dtype(t), n_rows,
                                        _arg(pos, dev, "pos", _I32, T * k), T, k, d,
-                                       _arg(dx, dev, "dx", t, T * d), _addr(err_word),
+                                       _arg(dx, dev, "dx", t, T * d),
+                                       _buffer(err_word, dev, "err_word", 16),
                                        _raw_stream(stream, drows))
     if st:
         raise MoeError(st, "moe_sort_tokens_backward")
@@ -711,7 +724,8 @@ def moe_unsort_tokens(rows, gate, pos, out, err_word, stream=None):
     st = _lib.moe_unsort_tokens(_arg(rows, dev, "rows", t, n_rows * d), _dtype(t), n_rows,
                                 _arg(gate, dev, "gate", _F32, T * k),
                                 _arg(pos, dev, "pos", _I32, T * k), T, k, d,
-                                _arg(out, dev, "out", t, T * d), _addr(err_word),
+                                _arg(out, dev, "out", t, T * d),
+                                _buffer(err_word, dev, "err_word", 16),
                                 _raw_stream(stream, rows))
     if st:
         raise MoeError(st, "moe_unsort_tokens")
@@ -728,7 +742,8 @@ def moe_unsort_tokens_backward(dout, rows, gate, pos, drows, dgate, err_word, st
                                          _arg(gate, dev, "gate", _F32, T * k),
                                          _arg(pos, dev, "pos", _I32, T * k), T, k, d,
                                          _arg(drows, dev, "drows", t, n_rows * d),
-                                         _arg(dgate, dev, "dgate", _F32, T * k), _addr(err_word),
+                                         _arg(dgate, dev, "dgate", _F32, T * k),
+                                         _buffer(err_word, dev, "err_word", 16),
                                          _raw_stream(stream, dout))
     if st:
         raise MoeError(st, "moe_unsort_tokens_backward")

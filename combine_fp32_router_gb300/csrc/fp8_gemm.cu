@@ -286,13 +286,19 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     if constexpr (PAIR) return mbar_wait_cluster(bar, parity, ab, err, site, p.wait_ns);
     else return mbar_wait(bar, parity, ab, err, site, p.wait_ns);
   };
-  const auto try_now = [&](uint32_t bar, uint32_t parity) {
-    if constexpr (PAIR) return mbar_try_wait_relaxed(bar, parity);
-    else return mbar_try_wait(bar, parity);
-  };
   const auto warp_wait = [&](uint32_t bar, uint32_t parity, int site) {
-    if (__all_sync(0xFFFFFFFFu, try_now(bar, parity))) return true;
     return __all_sync(0xFFFFFFFFu, wait(bar, parity, abort_flag, site)) != 0;
+  };
+  // factors pass between warps of one CTA
+  const auto own_wait = [&](uint32_t bar, uint32_t parity, int site) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, err, site, p.wait_ns)) != 0;
+  };
+  // TMEM alone passes over tfull and tempty, ordered by the tcgen05 fences on both sides, so the first
+  // look need not acquire: at cluster scope that took 5 % of the whole product.
+  const auto tmem_wait = [&](uint32_t bar, uint32_t parity, int site) {
+    if constexpr (PAIR)
+      if (__all_sync(0xFFFFFFFFu, mbar_try_wait_relaxed(bar, parity))) return true;
+    return warp_wait(bar, parity, site);
   };
 
   if (threadIdx.x == 0) {
@@ -411,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
           for (int j0 = 0; j0 < nk; j0 += p.ks) {  // ks divides kG: a stage
             if (mine) {
               ok = warp_wait(full(s), phase, 84);
-              if (ok && j0 == 0 && group >= C::kBufs) ok = warp_wait(tempty(a), aphase, 83);
+              if (ok && j0 == 0 && group >= C::kBufs) ok = tmem_wait(tempty(a), aphase, 83);
               if (!ok) break;
               tc_fence_after();
               const int n = min(p.ks, nk - j0);
@@ -474,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               v[i] = r0 + 4 * i < nrows ? __ldg(sa + static_cast<int64_t>(r0 + 4 * i) * p.kt + kb) : 0.0f;
-            if (part == 0 && fills >= 2) ok = warp_wait(sempty(slot), phase, 87);
+            if (part == 0 && fills >= 2) ok = own_wait(sempty(slot), phase, 87);
             if (!ok) break;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -511,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     uint32_t a = 0, aphase = 0, slot = 0, sphase = 0;
     bool ok = true;
     for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
-      if (!(ok = warp_wait(sfull(slot), sphase, 88))) break;
+      if (!(ok = own_wait(sfull(slot), sphase, 88))) break;
       const int4 t = sh.info[slot];
       const int r0 = 128 * rank + C::kM / 4 * q, col0 = t.z + part * kCols;
       const bool live = r0 < t.y && col0 < p.N;  // else nothing of it is stored
@@ -519,13 +525,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
       for (int left = p.kt; left > 0; left -= kScaleBlocks) {
-        if (left < p.kt) ok = ok && warp_wait(sfull(slot), sphase, 88);
+        if (left < p.kt) ok = ok && own_wait(sfull(slot), sphase, 88);
         if (!ok) break;
         uint32_t f = factors + slot * (2 * kScaleBlocks * kScaleRow * 4);
 #pragma unroll 1
         for (int n = min(left, kScaleBlocks); n > 0; n -= G) {
           // one answer for the warp: the tcgen05.ld below is .sync.aligned
-          ok = warp_wait(tfull0 + 8 * a, aphase, 86);
+          ok = tmem_wait(tfull0 + 8 * a, aphase, 86);
           if (!ok) break;
           tc_fence_after();
           const uint32_t ta = tcols + a * (G * NT);
