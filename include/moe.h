@@ -391,9 +391,9 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
  * Format of a matrix of R rows and C columns: Kp = C rounded up to a multiple of 128.
  *   codes  [R, Kp] E4M3 bytes (largest value 448); quantisers write zero codes past C.
  *   scales [R, Kp / 128] fp32: a value is code * scale.
- * scale = max(amax * (1 / 448), 2^-126) in fp32 of the row's 128 columns, 1 where all are zero; the code is the
- * E4M3 number nearest to x * (1 / scale) in fp32, ties to the even mantissa, saturating.  Columns
- * that hold an infinity or a NaN have the scale NaN and zero codes: all 128 values are NaN.
+ * scale = max(amax * (1 / 448), 2^-126) in fp32 of the row's 128 columns, 1 where all are zero; the
+ * code is the E4M3 number nearest to x * (1 / scale) in fp32, ties to the even mantissa, saturating.
+ * Columns that hold an infinity or a NaN have the scale NaN and zero codes: all 128 values are NaN.
  * Weights have one scale per 128 x 128 block instead: codes [N, Kp], scales
  * [ceil(N / 128), Kp / 128].  Codes are 16-byte aligned, other arrays aligned to their element
  * (rows that start on 16 bytes are faster).  Groups of matrices (experts) lie one after another.
@@ -406,8 +406,9 @@ int64_t moe_fp8_row_bytes(int cols);
 /* x [rows, cols] (MOE_DTYPE_*, row r at x + r * row_stride elements) -> q [rows, Kp], scales.
  * swiglu = 1: a row of x holds a and b, cols values each (row_stride >= 2 cols), and
  * silu(a) b = a / (1 + exp(-a)) b is quantised (forward only; its fp32 value is within
- * (6 + |a|) 2^-23 of the exact one, relatively).  perm: NULL, or [rows] int32: rows with perm < 0 are neither read nor
- * written (the padding of sorted rows).  cols <= 2^20, rows * ceil(cols / 128) < 2^31 - 64.
+ * (6 + |a|) 2^-23 of the exact one, relatively, and silu(a), below 1.1e-36 in magnitude there, is 0
+ * for a < -87.3).  perm: NULL, or [rows] int32: rows with perm < 0 are neither read nor written (the
+ * padding of sorted rows).  cols <= 2^20, rows * ceil(cols / 128) < 2^31 - 64.
  * rows = 0 writes nothing. */
 moe_status_t moe_quantize_rows_fp8(const void* x, int dtype, int64_t rows, int cols,
                                    int64_t row_stride, int swiglu, const int32_t* perm, uint8_t* q,
@@ -428,7 +429,8 @@ moe_status_t moe_quantize_blocks_fp8(const moe_bf16_t* W, int E, int K, int N, i
 /*
  * out[r, n] = sum_kb a_scales[r, kb] b_scales[e(r), n / 128, kb] sum_{k in block kb} A[r, k]
  * B[e(r)][n, k], every sum in fp32, in a K order that depends on K alone, rounded once to out_dtype
- * (MOE_DTYPE_BF16 or MOE_DTYPE_F32).
+ * (MOE_DTYPE_BF16 or MOE_DTYPE_F32).  The product of the two scales is rounded to fp32 first: one
+ * beyond its range makes the block's part infinite or NaN, one below it zero.
  *   a [rows, Kp], a_scales [rows, Kp / 128]; b, b_scales: E matrices of N x K
  *   (moe_quantize_blocks_fp8's layout); codes past K are not used; out [rows, N] contiguous.
  *   counts : NULL (E = 1: every row), or a DEVICE array [E]: expert e's counts[e] rows start at row
