@@ -66,6 +66,7 @@ struct Cfg {
   static constexpr int kG = NT == 32 ? 4 : NT == 256 ? 1 : 2;
   static constexpr int kBufs = 512 / NT / kG < kMaxBufs ? 512 / NT / kG : kMaxBufs;
   static constexpr uint32_t kTmemCols = kBufs * kG * NT;
+  static_assert(kBufs % 2 == 0, "a buffer is always the same MMA warp's, which so sees each of its phases");
 };
 
 struct Params {
@@ -88,7 +89,7 @@ struct Params {
 struct Shared {
   alignas(16) float factors[2][2][kScaleBlocks][kScaleRow];  // slot, half of the columns
   int4 info[2];  // per slot: its tile's first row, valid rows and first column
-  uint64_t bars[2 * kMaxStages + 2 * kMaxBufs + 5];
+  uint64_t bars[2 * kMaxStages + 2 * kMaxBufs + 7];
   uint32_t tmem;
   int32_t abort_flag;
   uint32_t peer_issued;                          // fills issued by the peer
@@ -276,6 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   const auto sfull = [&](uint32_t i) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + i]); };
   const auto sempty = [&](uint32_t i) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + 2 + i]); };
   const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + 4]);
+  const auto turn = [&](uint32_t w) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + 5 + w]); };
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&sh.abort_flag);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
@@ -313,6 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull(i), 1);
       mbar_init(sempty(i), kSumWarps);
+      mbar_init(turn(i), 1);
     }
     mbar_init(drain, 2);
     fence_mbar_init();
@@ -408,17 +411,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       }
     } else if (warp < kScaler && rank == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(C::kRows, NT);
+      const uint32_t me = warp - kIssuer;
       uint32_t s = 0, phase = 0, a = 0, aphase = 1, group = 0;
       bool ok = true;
       for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
         for (int left = p.kt; ok && left > 0; left -= C::kG, ++group) {
           const int nk = min(C::kG, left);
-          const bool mine = (group & 1) == static_cast<uint32_t>(warp - kIssuer);
+          const bool mine = (group & 1) == me;
+          // A wait by parity for a fill needs the stage's fill before it to have landed, else it takes
+          // the one before that for its own, and copies may land out of order.  With one stage to a
+          // group and an even number of them a stage's fills are all this warp's; elsewhere the warps
+          // pass a turn: every fill of the groups before has been waited for.
+          if (C::kG > 1 && mine && group > 0 && !(ok = own_wait(turn(me), (group - 1) / 2 & 1, 89))) break;
           for (int j0 = 0; j0 < nk; j0 += p.ks) {  // ks divides kG: a stage
             if (mine) {
               ok = warp_wait(full(s), phase, 84);
               if (ok && j0 == 0 && group >= C::kBufs) ok = tmem_wait(tempty(a), aphase, 83);
               if (!ok) break;
+              if (C::kG > 1 && j0 + p.ks >= nk && lane == 0) mbar_arrive(turn(me ^ 1));
               tc_fence_after();
               const int n = min(p.ks, nk - j0);
               if (elect_one()) {
@@ -770,6 +780,7 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* b, int K, int sms, c
   for (p.ks = C::kG; p.ks > 1 && 3 * p.ks * kb_bytes > kRingBytes;) p.ks /= 2;
   const int stages = static_cast<int>(kRingBytes / (p.ks * kb_bytes));
   p.stages = stages < kMaxStages ? stages : kMaxStages;
+  if (C::kG == 1) p.stages &= ~1;  // each stage one MMA warp's
   const int64_t tiles = blocks * p.nt;  // checked by the caller to fit 31 bits
   const int units = static_cast<int>(tiles < sms / C::kCtas ? tiles : sms / C::kCtas);
   return launch<NT, PAIR>(p, units, stream);

@@ -106,6 +106,24 @@ def test_weights_past_2_31_values(moe):
             assert torch.equal(o, want)
 
 
+@pytest.mark.parametrize("rows,N,K", [(1, 16384, 7168), (1, 16384, 7040), (5, 16000, 4992), (70, 8192, 7168),
+                                      (130, 16384, 2176)])
+def test_few_rows_of_long_weights(moe, rows, N, K):
+    """Weights from HBM, so that copies land late and out of order; several times, on two sets in turn."""
+    a = moe.moe_quantize_rows_fp8(randn(rows, K))
+    bs = [moe.moe_quantize_blocks_fp8((randn(1, K, N, seed=i) * K ** -0.5).bfloat16()) for i in (1, 2)]
+    outs = [torch.empty(rows, N, device=DEV) for _ in bs]
+    for b, o in zip(bs, outs):
+        moe.moe_gemm_fp8(*a, *b, o, K)
+        A, B = ref.rows64(*a, K), ref.weights64(b[0][0], b[1][0], K)
+        ref.within(o, A @ B.t(), (258 + -(-K // 128)) * ref.U * (A.abs() @ B.abs().t()), "out")
+    o = torch.empty(rows, N, device=DEV)
+    for i in range(20):
+        moe.moe_gemm_fp8(*a, *bs[i % 2], o, K)
+        assert torch.equal(o, outs[i % 2])
+    assert moe.moe_gemm_fp8_get_error() == moe.MOE_OK
+
+
 # ------------------------------------------------------------------------- tile shapes
 def products(moe):
     """One digest of products of many sizes."""
