@@ -3,11 +3,16 @@
 // rows grouped by expert in 128-row segments, or one matrix.
 //
 // One persistent launch.  A tile is 256 x 256 on a CTA pair (cta_group::2: each CTA holds 128 rows
-// and half of the weights) or 128 rows x 128 or 64, or 64 rows x 32 weight rows on one CTA.  The tensor cores
-// (tcgen05.mma kind::f8f6f4) sum the 128 values of a block of K into TMEM; scales differ from block
-// to block, so the sum of each block is taken out of TMEM, scaled and added to the tile's sums, which
-// stay in registers:  acc = fma(sum, sa sb, acc), two values an instruction.  Every shape adds the
-// same products in the same order, so a row's results do not depend on the other rows.  Warps:
+// and half of the weights) or 128 rows x 128 or 64, or 64 rows x 32 weight rows on one CTA.  The
+// tensor cores (tcgen05.mma kind::f8f6f4) sum the 128 values of a block of K into TMEM; scales differ
+// from block to block, so the sum of each block is taken out of TMEM, scaled and added to the tile's
+// sums, which stay in registers:  acc = fma(sum, sa sb, acc), two values an instruction.  Every shape
+// adds the same products in the same order, so a row's results do not depend on the other rows.
+//
+// 8192 x 7168 x 7168 takes 306 us in bf16, 2.75 PFLOP/s; bound by bringing codes into the SMs, 32 KB a
+// block of K and SM, 83 GB/s: with all sums and scales and three quarters of the MMAs left out it takes
+// 266.  One row of 7168 x 4096 takes 11.1 us, 7.6 and 4.1 with a half and none of K: 4 KB a block from
+// HBM on 128 SMs, 4.3 TB/s.  Warps:
 //   0..7    sums: lanes 32 (w % 4) .. of TMEM, half w / 4 of the columns; then the output
 //   8       producer: codes by TMA (128-byte swizzle)
 //   9, 10   MMAs, groups of blocks of K in turn: what one spends on waiting, committing and looping
@@ -37,7 +42,7 @@ __device__ int g_taken8_status;
 __global__ void take_error_kernel() { g_taken8_status = atomicExch(&g_gemm8_err.status, 0); }
 
 constexpr int kMaxStages = 32;
-constexpr int kMaxBufs = 4;
+constexpr int kBufs = 2;
 constexpr int kSumWarps = 8, kLoader = 8, kIssuer = 9, kScaler = 11;
 constexpr int kThreads = 384;
 // Registers of a thread: launched with 168 (65536 / 384, which ptxas gives to the launch bounds), of
@@ -45,7 +50,8 @@ constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168, kSumRegs = 208, kOtherRegs = 88;
 static_assert(2 * kSumRegs + kOtherRegs <= 3 * kLaunchRegs, "registers at launch");
 constexpr int kBoxes = 5;  // box heights of the rows: 8, 16, 32, 64, 128
-constexpr uint32_t kRingBytes = 128 * 1024;
+// The stages, and behind them each summing warp's place for outputs: 32 rows of 128 bytes, once or twice.
+constexpr uint32_t kBufferBytes = 192 * 1024;
 // Factors of 8 blocks of K at a time; rows of one block 132 words apart, so that four rows of eight
 // blocks meet no bank twice.  Read from global memory by each summing lane for itself, the scales
 // took a warp 210 cycles of the 512 of a block of K.
@@ -60,13 +66,14 @@ struct Cfg {
   static constexpr int kRows = kM * kCtas;      // rows of a tile
   static constexpr int kLocalN = NT / kCtas;    // weight rows that a CTA loads
   static constexpr int kCols = NT / 2;          // columns of a warp's sums
-  static constexpr int kChunk = kCols < 16 ? kCols : 16;  // of them taken at a time
   // Blocks of K between two arrivals of the summing warps, and at most per stage: an MMA warp's turn
   // (wait, issue, commit) takes 350 cycles, the MMAs of a block 160 with 32 columns, 256 with 128
   static constexpr int kG = NT == 32 ? 4 : NT == 256 ? 1 : 2;
-  static constexpr int kBufs = 512 / NT / kG < kMaxBufs ? 512 / NT / kG : kMaxBufs;
   static constexpr uint32_t kTmemCols = kBufs * kG * NT;
-  static_assert(kBufs % 2 == 0, "a buffer is always the same MMA warp's, which so sees each of its phases");
+  static constexpr uint32_t kOutBytes = PAIR ? 8192 : 4096;
+  static constexpr uint32_t kRingBytes = kBufferBytes - kSumWarps * kOutBytes;
+  static_assert(kTmemCols <= 512, "");
+  static_assert(kRingBytes >= kBufs * kG * (kM + kLocalN) * 128, "the ring holds kBufs groups");
 };
 
 struct Params {
@@ -75,7 +82,6 @@ struct Params {
   int64_t rows;
   int N, kt, E, nt, nb;  // outputs, blocks of K, experts, weight tiles and scale blocks per expert
   int stages, ks;        // stages, and blocks of K in one
-  int turns;             // a stage's fills are not all one MMA warp's
   uint32_t abytes;       // place for the rows of a block of K
   int vec;               // output rows start on 32 (2), 16 (1) bytes or neither (0)
   int f32, tma_out;      // tma_out: rows of the output can be stored by TMA
@@ -90,16 +96,14 @@ struct Params {
 struct Shared {
   alignas(16) float factors[2][2][kScaleBlocks][kScaleRow];  // slot, half of the columns
   int4 info[2];  // per slot: its tile's first row, valid rows and first column
-  uint64_t bars[2 * kMaxStages + 2 * kMaxBufs + 7];
+  uint64_t bars[2 * kMaxStages + 2 * kBufs + 5];
   uint32_t tmem;
   int32_t abort_flag;
   uint32_t peer_issued;                          // fills issued by the peer
   uint32_t tx[kMaxStages], peer_tx[kMaxStages];  // bytes of the fill in a stage
   int32_t first_block[kMaxE + 1], first_row[kMaxE + 1], count[kMaxE];
 };
-// A summing warp's place for outputs: 32 rows of 128 bytes, swizzled for TMA, or 16 columns.
-constexpr uint32_t kOutBytes = 8192;
-constexpr size_t kSmemBytes = kRingBytes + kSumWarps * kOutBytes + 1024 + sizeof(Shared);
+constexpr size_t kSmemBytes = kBufferBytes + 1024 + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "fits the opt-in shared memory of a CTA (227 KB)");
 static_assert(sizeof(Shared) >= 16384, "what a box of fewer than 128 rows leaves out can be read");
 
@@ -141,30 +145,7 @@ __device__ __forceinline__ bool mbar_try_wait_relaxed(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
-// 32 or 16 columns of this thread's lane, waited for.
-__device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_done(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
-                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
-                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
-                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                 "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]),
-                 "+r"(r[31])
-               :
-               : "memory");
-}
+// 16 columns of this thread's lane, and the wait for them.
 __device__ __forceinline__ void tmem_start(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -275,35 +256,36 @@ __device__ __forceinline__ void store_tile(const Params& p, int row, int col, co
 // 16-byte pieces where its place in memory has them, and value by value the 16 bytes before the first
 // and behind the last of them.  8192 x 7161 x 2048: bf16 128 us, fp32 144, both 164 with 16 columns at a
 // time as in store16; bf16 a row at a time in words of two: 182 (7168 columns, by TMA: 101 and 121).
-constexpr uint32_t kRowPitch = 144;  // eight rows meet no bank twice
-static_assert(32 * kRowPitch <= kOutBytes, "");
 template <int W>
 __device__ __forceinline__ void store_rows(const Params& p, int64_t row, int n, int col, const float* acc,
                                            uint32_t buf, int lane) {
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) st_shared_v4(buf + kRowPitch * lane + 16 * i, pack16<W>(acc + i * (W / 8)));
+  for (int i = 0; i < 8; ++i) st_shared_v4(buf + 128 * lane + 16 * (i ^ (lane & 7)), pack16<W>(acc + i * (W / 8)));
   __syncwarp();
+  const auto word = [&](int r, uint32_t b) {  // the one at byte b of row r
+    return ld_shared_u32(buf + 128 * r + ((b & ~15u) ^ 16 * (r & 7)) + (b & 12));
+  };
   if constexpr (W == 32) {
     uint32_t* o = static_cast<uint32_t*>(p.out) + row * p.N + col + lane;
 #pragma unroll 8
-    for (int r = 0; r < n; ++r, o += p.N) *o = ld_shared_u32(buf + kRowPitch * r + 4 * lane);
+    for (int r = 0; r < n; ++r, o += p.N) *o = word(r, 4 * lane);
   } else {
     const int j = lane & 7;
     uint16_t* o = static_cast<uint16_t*>(p.out) + (row + (lane >> 3)) * p.N + col;
 #pragma unroll 2
     for (int r = lane >> 3; r < n; r += 4, o += 4 * static_cast<int64_t>(p.N)) {
-      const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(o)) & 15, src = buf + kRowPitch * r;
+      const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(o)) & 15;
       if (j > 0) {
         uint32_t x[5];
 #pragma unroll
-        for (int i = 0; i < 5; ++i) x[i] = ld_shared_u32(src + ((16 * j - off) & ~3u) + 4 * i);
+        for (int i = 0; i < 5; ++i) x[i] = word(r, min(((16 * j - off) & ~3u) + 4 * i, 124u));
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = __funnelshift_r(x[i], x[i + 1], 8 * (off & 2));
         st_v4(reinterpret_cast<char*>(o) + 16 * j - off, make_uint4(x[0], x[1], x[2], x[3]));
       }
       const int e = j < static_cast<int>(16 - off) / 2 ? j : 56 + j;
-      o[e] = static_cast<uint16_t>(ld_shared_u32(src + (2 * e & ~3)) >> (16 * (e & 1)));
+      o[e] = static_cast<uint16_t>(word(r, 2 * e) >> (16 * (e & 1)));
     }
   }
 }
@@ -314,17 +296,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (base - raw) + kRingBytes + kSumWarps * kOutBytes);
+  Shared& sh = *reinterpret_cast<Shared*>(smem_raw + (base - raw) + kBufferBytes);
   const uint32_t S = static_cast<uint32_t>(p.stages);
   const uint32_t kb_bytes = p.abytes + C::kLocalN * 128, stage_bytes = p.ks * kb_bytes;
   const auto full = [&](uint32_t s) { return smem_u32(&sh.bars[s]); };
   const auto empty = [&](uint32_t s) { return smem_u32(&sh.bars[kMaxStages + s]); };
   const auto tfull = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + a]); };
-  const auto tempty = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + kMaxBufs + a]); };
-  const auto sfull = [&](uint32_t i) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + i]); };
-  const auto sempty = [&](uint32_t i) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + 2 + i]); };
-  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + 4]);
-  const auto turn = [&](uint32_t w) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kMaxBufs + 5 + w]); };
+  const auto tempty = [&](uint32_t a) { return smem_u32(&sh.bars[2 * kMaxStages + kBufs + a]); };
+  const auto sfull = [&](uint32_t i) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kBufs + i]); };
+  const auto sempty = [&](uint32_t i) { return smem_u32(&sh.bars[2 * kMaxStages + 2 * kBufs + 2 + i]); };
+  const uint32_t drain = smem_u32(&sh.bars[2 * kMaxStages + 2 * kBufs + 4]);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(&sh.abort_flag);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
@@ -355,14 +336,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       mbar_init(full(s), 1);  // rank 0's: its arming arrival and both CTAs' bytes
       mbar_init(empty(s), 1);
     }
-    for (int a = 0; a < C::kBufs; ++a) {
+    for (int a = 0; a < kBufs; ++a) {
       mbar_init(tfull(a), 1);
       mbar_init(tempty(a), kSumWarps * C::kCtas);  // rank 0's: an arrival of every summing warp
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(sfull(i), 1);
       mbar_init(sempty(i), kSumWarps);
-      mbar_init(turn(i), 1);
     }
     mbar_init(drain, 2);
     fence_mbar_init();
@@ -458,24 +438,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
       }
     } else if (warp < kScaler && rank == 0) {
       constexpr uint32_t idesc = idesc_e4m3_f32(C::kRows, NT);
-      const uint32_t me = warp - kIssuer;
-      const bool turns = C::kG > 1 && p.turns;
       uint32_t s = 0, phase = 0, a = 0, aphase = 1, group = 0;
       bool ok = true;
       for (uint32_t tile = unit; ok && tile < tiles; tile += units) {
         for (int left = p.kt; ok && left > 0; left -= C::kG, ++group) {
           const int nk = min(C::kG, left);
-          const bool mine = (group & 1) == me;
-          // A wait by parity for a fill needs the stage's fill before it to have landed, else it takes
-          // the one before that for its own, and copies may land out of order.  Where that fill can be
-          // the other warp's they pass a turn: every fill of the groups before has been waited for.
-          if (turns && mine && group > 0 && !(ok = own_wait(turn(me), (group - 1) / 2 & 1, 89))) break;
+          const bool mine = (group & 1) == static_cast<uint32_t>(warp - kIssuer);
+          // A wait by parity for a fill needs the stage's fill before it to have landed; while that is on
+          // its way it takes the one before for its own.  That fill is this warp's own where groups are
+          // a stage and the stages even; elsewhere the buffer is waited for first: its last sums taken,
+          // every fill up to its last group's has landed, and the ring holds kBufs groups.
+          const bool wait_buffer = mine && group >= kBufs;
+          if (C::kG > 1 && wait_buffer && !(ok = tmem_wait(tempty(a), aphase, 83))) break;
           for (int j0 = 0; j0 < nk; j0 += p.ks) {  // ks divides kG: a stage
             if (mine) {
               ok = warp_wait(full(s), phase, 84);
-              if (ok && j0 == 0 && group >= C::kBufs) ok = tmem_wait(tempty(a), aphase, 83);
+              // (of the pairs, what an MMA warp waits for last: with the stage after it 5 % slower)
+              if (ok && C::kG == 1 && wait_buffer) ok = tmem_wait(tempty(a), aphase, 83);
               if (!ok) break;
-              if (turns && j0 + p.ks >= nk && lane == 0) mbar_arrive(turn(me ^ 1));
               tc_fence_after();
               const int n = min(p.ks, nk - j0);
               if (elect_one()) {
@@ -505,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
               phase ^= 1;
             }
           }
-          if (++a == C::kBufs) {
+          if (++a == kBufs) {
             a = 0;
             aphase ^= 1;
           }
@@ -561,14 +541,15 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
-    constexpr int kCols = C::kCols, G = C::kG, B = C::kChunk;
+    constexpr int kCols = C::kCols, G = C::kG, B = 16;  // B: columns taken at a time
     const int q = warp & 3, part = warp >> 2, half = part * kCols / 128;
     // addresses of this warp's TMEM lanes and columns, its factors, and the buffers' barriers
-    const uint32_t shared = base + kRingBytes + kSumWarps * kOutBytes;
+    const uint32_t shared = base + kBufferBytes;
     const uint32_t tcols = tmem + part * kCols + (static_cast<uint32_t>(32 * q) << 16);
     const uint32_t factors = shared + static_cast<uint32_t>(offsetof(Shared, factors)) +
                              4 * ((NT == 256 ? half : 0) * (kScaleBlocks * kScaleRow) + C::kM / 4 * q + lane);
-    const uint32_t out_buf = base + kRingBytes + warp * kOutBytes;
+    constexpr uint32_t kOutBytes = C::kOutBytes;
+    const uint32_t out_buf = base + C::kRingBytes + warp * kOutBytes;
     const uint32_t tfull0 = tfull(0);
     const uint32_t tempty0 = PAIR ? mapa_shared(tempty(0), 0) : tempty(0);
     uint32_t a = 0, aphase = 0, slot = 0, sphase = 0;
@@ -630,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
             }
           }
           f += G * kScaleRow * 4;
-          if (++a == C::kBufs) {
+          if (++a == kBufs) {
             a = 0;
             aphase ^= 1;
           }
@@ -776,17 +757,20 @@ CUtensorMap code_map(const void* base, int K, uint64_t rows, uint32_t box_rows, 
   return m;
 }
 
-// Tile shapes: 256 x 256 on pairs, or 128 x 128, 128 x 64 or 64 x 32 on single CTAs; by the rounds of tiles that
-// each takes over the SMs times what a block of K of a tile costs there (in ns, measured on 8192 rows
-// of 7168 x 7168).  With `counts`, which are on the device, `rows` is taken for moe_sort_rows_bound of
-// the pairs, and the pairs for equal shares of the experts (37 pairs over 49 experts, 84 x 6373: 14.1 us,
-// 22.2 when the padding counted as rows by half).  MOE_FP8_SHAPE = 0 .. 3 sets the shape; every shape gives the same bits.
+// Tile shapes: 256 x 256 on pairs, or 128 x 128, 128 x 64 or 64 x 32 on single CTAs; by the rounds of
+// tiles that each takes over the SMs, times what a block of K of a tile costs there and a tile besides
+// (ns, of 8192 x 7168 x 7168 and 4000 x 7168 x 512 in each shape: 306, 465, 567, 1205 us and 26, 30,
+// 46, 90; one row of 7168 x 4096 takes 28, 18, 16 and 11 us).  With `counts`, which are on the device,
+// `rows` is taken for moe_sort_rows_bound of the pairs, and the pairs for equal shares of the experts
+// (37 pairs over 49 experts, 84 x 6373: 10.7 us, 15.6 when the padding counted as rows by half).
+// MOE_FP8_SHAPE = 0 .. 3 sets the shape; every shape gives the same bits.
 struct Shape {
-  int rows, n, ctas, cost;
+  int rows, n, ctas, block, tile;
 };
 constexpr int kNumShapes = 4;
-constexpr Shape kShapes[kNumShapes] = {{256, 256, 2, 446}, {128, 128, 1, 340}, {128, 64, 1, 280}, {64, 32, 1, 160}};
-int choose_shape(int64_t rows, int N, int E, bool grouped, int sms) {
+constexpr Shape kShapes[kNumShapes] = {
+    {256, 256, 2, 450, 1800}, {128, 128, 1, 345, 870}, {128, 64, 1, 210, 900}, {64, 32, 1, 115, 470}};
+int choose_shape(int64_t rows, int N, int kt, int E, bool grouped, int sms) {
   static const int forced = [] {
     const char* v = std::getenv("MOE_FP8_SHAPE");
     return v && *v >= '0' && *v <= '3' ? *v - '0' : -1;
@@ -799,7 +783,7 @@ int choose_shape(int64_t rows, int N, int E, bool grouped, int sms) {
   for (int i = 0; i < kNumShapes; ++i) {
     const Shape& s = kShapes[i];
     const int64_t tiles = E * ((share + s.rows - 1) / s.rows) * ((N + s.n - 1) / s.n);
-    const int64_t units = sms / s.ctas, cost = (tiles + units - 1) / units * s.cost;
+    const int64_t units = sms / s.ctas, cost = (tiles + units - 1) / units * (kt * s.block + s.tile);
     if (cost < least) {
       least = cost;
       best = i;
@@ -834,14 +818,10 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* b, int K, int sms, c
   if (st != cudaSuccess) return st;
   // as many blocks of K in a stage as leave three of them
   const uint32_t kb_bytes = p.abytes + C::kLocalN * 128u;
-  for (p.ks = C::kG; p.ks > 1 && 3 * p.ks * kb_bytes > kRingBytes;) p.ks /= 2;
-  const int stages = static_cast<int>(kRingBytes / (p.ks * kb_bytes));
+  for (p.ks = C::kG; p.ks > 1 && 3 * p.ks * kb_bytes > C::kRingBytes;) p.ks /= 2;
+  const int stages = static_cast<int>(C::kRingBytes / (p.ks * kb_bytes));
   p.stages = stages < kMaxStages ? stages : kMaxStages;
-  // A stage is always the same MMA warp's where two groups divide the stages and every group takes as
-  // many; no turns then (777 x 1545 x 2700: 15.4 us, 16.1 with them).  Pairs are arranged so.
   if (C::kG == 1) p.stages &= ~1;
-  const int group = C::kG / p.ks, last = (p.kt - 1) % C::kG / p.ks + 1;
-  p.turns = p.stages % (2 * group) != 0 || last != group;
   const int64_t tiles = blocks * p.nt;  // checked by the caller to fit 31 bits
   const int units = static_cast<int>(tiles < sms / C::kCtas ? tiles : sms / C::kCtas);
   return launch<NT, PAIR>(p, units, stream);
@@ -887,7 +867,7 @@ moe_status_t moe_gemm_fp8(const uint8_t* a, const float* a_scales, int64_t rows,
   p.wait_ns = wait_limit_ns();
   p.withhold = withheld_loaders();
   const int sms = num_sms_of_current_device();
-  const int shape = choose_shape(rows, N, E, counts != nullptr, sms);
+  const int shape = choose_shape(rows, N, p.kt, E, counts != nullptr, sms);
   const cudaError_t st = shape == 0   ? run<256, true>(p, a, b, K, sms, stream)
                          : shape == 1 ? run<128, false>(p, a, b, K, sms, stream)
                          : shape == 2 ? run<64, false>(p, a, b, K, sms, stream)
