@@ -33,6 +33,27 @@ struct In<MOE_DTYPE_F32> {
   static __device__ __forceinline__ T of(float v) { return v; }
 };
 
+// Two values an instruction, each rounded as by itself: the pipe takes as long, but an issue slot less.
+__device__ __forceinline__ void mul2(float& x, float& y, float a, float b) {  // x *= a, y *= b
+  asm("{\n\t.reg .b64 v, m;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %3};\n\t"
+      "mul.rn.f32x2 v, v, m;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {  // x += a, y += b
+  asm("{\n\t.reg .b64 v, m;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %3};\n\t"
+      "add.rn.f32x2 v, v, m;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+// x = a c + x, y = b d + y
+__device__ __forceinline__ void fma2(float& x, float& y, float a, float b, float c, float d) {
+  asm("{\n\t.reg .b64 v, m, n;\n\tmov.b64 v, {%0, %1};\n\tmov.b64 m, {%2, %3};\n\t"
+      "mov.b64 n, {%4, %5};\n\tfma.rn.f32x2 v, m, n, v;\n\tmov.b64 {%0, %1}, v;\n\t}"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+}
+
 // Values 8 l .. 8 l + 7 of a tile that has n of its 128 (zeros past them), raw: converting waits
 // for the loads, so it is left for later.
 template <typename T>

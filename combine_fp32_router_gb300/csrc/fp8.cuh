@@ -44,7 +44,9 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d, float inv) {
-  const uint32_t w = e4m3x2(a * inv, b * inv) | (e4m3x2(c * inv, d * inv) << 16);
+  mul2(a, b, inv, inv);
+  mul2(c, d, inv, inv);
+  const uint32_t w = e4m3x2(a, b) | (e4m3x2(c, d) << 16);
   return inv == 0.0f ? 0u : w;
 }
 // Values of two codes

@@ -16,12 +16,25 @@ constexpr int kTiles = 4;  // tiles of 128 values per half warp, all loaded befo
 // silu(a) b.  The fast exponential and reciprocal keep the value to (6 + |a|) 2^-23, against the
 // 2^-4 of a code; with expf and an IEEE division the kernel would be bound by issuing them.  Both
 // flush subnormals: silu(a) is 0 below a = -87.3, where it is less than 1.1e-36 in magnitude.
-__device__ __forceinline__ float swiglu(float a, float b) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a * -1.44269504088896340736f));  // -log2 e
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  // a = -infinity gives 0 as its neighbours do, not -infinity * 0 (a NaN stays in r)
-  return fmaxf(a, -3.402823466e38f) * r * b;
+template <int DT>
+__device__ __forceinline__ void swiglu8(const Raw8<typename In<DT>::T>& ar, const Raw8<typename In<DT>::T>& br,
+                                        float (&y)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float a = In<DT>::f32(ar.v[j]), c = In<DT>::f32(ar.v[j + 1]);
+    float e = a, f = c;
+    mul2(e, f, -1.44269504088896340736f, -1.44269504088896340736f);  // -log2 e
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f));
+    add2(e, f, 1.0f, 1.0f);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f));
+    // a = -infinity gives 0 as its neighbours do, not -infinity * 0 (a NaN stays in e)
+    mul2(e, f, fmaxf(a, -3.402823466e38f), fmaxf(c, -3.402823466e38f));
+    mul2(e, f, In<DT>::f32(br.v[j]), In<DT>::f32(br.v[j + 1]));
+    y[j] = e;
+    y[j + 1] = f;
+  }
 }
 
 // ---- rows that start on 16 bytes: the matrix as tiles of 128 values, row-major; a warp takes
@@ -61,10 +74,11 @@ __global__ void __launch_bounds__(32 * kWarps)
   uint32_t m[kTiles], alive = 0;
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
+    if constexpr (GLU) {
+      swiglu8<DT>(a[i], b[i], y[i]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      y[i][j] = In<DT>::f32(a[i].v[j]);
-      if constexpr (GLU) y[i][j] = swiglu(y[i][j], In<DT>::f32(b[i].v[j]));
+      for (int j = 0; j < 8; ++j) y[i][j] = In<DT>::f32(a[i].v[j]);
     }
     m[i] = amax8(y[i]);
     alive |= static_cast<uint32_t>(live[i]) << i;
@@ -152,12 +166,11 @@ __global__ void __launch_bounds__(32 * kWarps)
   const T* v = x + row * stride + c0;
   const Raw8<T> a = load_seg<false>(v, cols - c0, lane);
   float y[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = In<DT>::f32(a.v[j]);
   if constexpr (GLU) {
-    const Raw8<T> b = load_seg<false>(v + cols, cols - c0, lane);
+    swiglu8<DT>(a, load_seg<false>(v + cols, cols - c0, lane), y);
+  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) y[j] = swiglu(y[j], In<DT>::f32(b.v[j]));
+    for (int j = 0; j < 8; ++j) y[j] = In<DT>::f32(a.v[j]);
   }
   quantize_seg(y, q + row * kp + c0, scales + row * (kp / 128) + c0 / 128,
                       static_cast<int>(kp - c0 < kSeg ? kp - c0 : kSeg), lane);
