@@ -60,6 +60,29 @@ template <typename T>
 struct alignas(16) Raw8 {
   T v[8];
 };
+// Values j and j + 1 (j even) in fp32 and back, a 16-bit pair as one word.
+template <int DT>
+__device__ __forceinline__ float2 get2(const Raw8<typename In<DT>::T>& r, int j) {
+  if constexpr (DT == MOE_DTYPE_F32) {
+    return make_float2(r.v[j], r.v[j + 1]);
+  } else {
+    const uint32_t w = reinterpret_cast<const uint32_t*>(r.v)[j / 2];
+    if constexpr (DT == MOE_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  }
+}
+template <int DT>
+__device__ __forceinline__ void set2(Raw8<typename In<DT>::T>& r, int j, float x, float y) {
+  if constexpr (DT == MOE_DTYPE_F32) {
+    r.v[j] = x;
+    r.v[j + 1] = y;
+  } else if constexpr (DT == MOE_DTYPE_BF16) {
+    reinterpret_cast<uint32_t*>(r.v)[j / 2] = pack_bf16x2(x, y);
+  } else {
+    const __half2 h = __floats2half2_rn(x, y);
+    reinterpret_cast<uint32_t*>(r.v)[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
 template <typename T>
 __device__ __forceinline__ Raw8<T> load8(const T* tile, int n, int l) {
   Raw8<T> r;

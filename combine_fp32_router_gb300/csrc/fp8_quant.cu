@@ -21,8 +21,8 @@ __device__ __forceinline__ void swiglu8(const Raw8<typename In<DT>::T>& ar, cons
                                         float (&y)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    const float a = In<DT>::f32(ar.v[j]), c = In<DT>::f32(ar.v[j + 1]);
-    float e = a, f = c;
+    const float2 a = get2<DT>(ar, j), b = get2<DT>(br, j);
+    float e = a.x, f = a.y;
     mul2(e, f, -1.44269504088896340736f, -1.44269504088896340736f);  // -log2 e
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(f));
@@ -30,8 +30,8 @@ __device__ __forceinline__ void swiglu8(const Raw8<typename In<DT>::T>& ar, cons
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e));
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(f));
     // a = -infinity gives 0 as its neighbours do, not -infinity * 0 (a NaN stays in e)
-    mul2(e, f, fmaxf(a, -3.402823466e38f), fmaxf(c, -3.402823466e38f));
-    mul2(e, f, In<DT>::f32(br.v[j]), In<DT>::f32(br.v[j + 1]));
+    mul2(e, f, fmaxf(a.x, -3.402823466e38f), fmaxf(a.y, -3.402823466e38f));
+    mul2(e, f, b.x, b.y);
     y[j] = e;
     y[j + 1] = f;
   }
@@ -78,7 +78,11 @@ __global__ void __launch_bounds__(32 * kWarps)
       swiglu8<DT>(a[i], b[i], y[i]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] = In<DT>::f32(a[i].v[j]);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 v = get2<DT>(a[i], j);
+        y[i][j] = v.x;
+        y[i][j + 1] = v.y;
+      }
     }
     m[i] = amax8(y[i]);
     alive |= static_cast<uint32_t>(live[i]) << i;
@@ -100,8 +104,7 @@ __device__ __forceinline__ Raw8<typename In<DT>::T> dequantize8(uint2 c, float s
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 v = e4m3x2_f32(static_cast<uint16_t>(w[j]));
-    r.v[2 * j] = In<DT>::of(v.x * s);
-    r.v[2 * j + 1] = In<DT>::of(v.y * s);
+    set2<DT>(r, 2 * j, v.x * s, v.y * s);
   }
   return r;
 }

@@ -324,12 +324,15 @@ __global__ void __launch_bounds__(kThreads) unsort_kernel(const BackArgs a) {
         for (int j = 0; j < KB; ++j)
           if (rs[j] >= 0) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = fmaf(gs[j], In<DT>::f32(v[j].v[i]), acc[i]);
+            for (int i = 0; i < 8; i += 2) {
+              const float2 x = get2<DT>(v[j], i);
+              fma2(acc[i], acc[i + 1], x.x, x.y, gs[j], gs[j]);
+            }
           }
       }
       Raw8<T> o;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o.v[i] = In<DT>::of(acc[i]);
+      for (int i = 0; i < 8; i += 2) set2<DT>(o, i, acc[i], acc[i + 1]);
       store_seg<VEC>(static_cast<T*>(a.out) + t * a.d + c0, n, lane, o);
     }
   }
@@ -370,10 +373,13 @@ __global__ void __launch_bounds__(kThreads) unsort_backward_kernel(const BackArg
         if (rs[j] < 0) continue;
         Raw8<T> o;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float f = In<DT>::f32(dy.v[i]);
-          if (a.dgate) acc[j0 + j] = fmaf(In<DT>::f32(y[j].v[i]), f, acc[j0 + j]);
-          o.v[i] = In<DT>::of(gj * f);
+        for (int i = 0; i < 8; i += 2) {
+          const float2 f = get2<DT>(dy, i);
+          if (a.dgate) {
+            const float2 v = get2<DT>(y[j], i);
+            acc[j0 + j] = fmaf(v.y, f.y, fmaf(v.x, f.x, acc[j0 + j]));
+          }
+          set2<DT>(o, i, gj * f.x, gj * f.y);
         }
         store_seg<VEC, true>(static_cast<T*>(a.drows) + static_cast<int64_t>(rs[j]) * a.d + c0, n, lane, o);
       }
