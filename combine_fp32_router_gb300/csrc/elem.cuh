@@ -67,8 +67,10 @@ __device__ __forceinline__ float2 get2(const Raw8<typename In<DT>::T>& r, int j)
     return make_float2(r.v[j], r.v[j + 1]);
   } else {
     const uint32_t w = reinterpret_cast<const uint32_t*>(r.v)[j / 2];
-    if constexpr (DT == MOE_DTYPE_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-    else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    if constexpr (DT == MOE_DTYPE_BF16)
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+    else
+      return __half22float2(*reinterpret_cast<const __half2*>(&w));
   }
 }
 template <int DT>

@@ -1,7 +1,8 @@
 // The 8-bit format with a scale per 128 values: E4M3 codes (largest value 448) and one fp32 scale
 // per row and 128 columns of a matrix of rows, or per 128 x 128 block of a weight matrix.
-//   scale = max(amax * (1 / 448), 2^-126) (the reciprocal and the product in fp32), 1 for zeros, NaN for one that holds an infinity or
-//           a NaN (its codes are zeros, so every value of it reads back as NaN)
+//   scale = max(amax * (1 / 448), 2^-126) (the reciprocal and the product in fp32), 1 for zeros, NaN for
+//           one that holds an infinity or a NaN (its codes are zeros, so every value of it reads back as
+//           NaN)
 //   code  = the E4M3 number nearest to x * (1 / scale), ties to the even mantissa
 // 1 / scale is rounded to fp32 once per block, and the product once per value: a code is the nearest
 // one of a number that is off by at most 2 units of 2^-24, against the format's half step of 2^-4.
@@ -87,8 +88,10 @@ __device__ __forceinline__ void store_seg(T* seg, int n, int lane, const Raw8<T>
     if (8 * lane + 8 <= n) {
 #pragma unroll
       for (int i = 0; i < static_cast<int>(sizeof(r) / 16); ++i)
-        if constexpr (STREAM) __stcs(reinterpret_cast<uint4*>(seg + 8 * lane) + i, reinterpret_cast<const uint4*>(&r)[i]);
-        else st_v4(reinterpret_cast<char*>(seg + 8 * lane) + 16 * i, reinterpret_cast<const uint4*>(&r)[i]);
+        if constexpr (STREAM)
+          __stcs(reinterpret_cast<uint4*>(seg + 8 * lane) + i, reinterpret_cast<const uint4*>(&r)[i]);
+        else
+          st_v4(reinterpret_cast<char*>(seg + 8 * lane) + 16 * i, reinterpret_cast<const uint4*>(&r)[i]);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)

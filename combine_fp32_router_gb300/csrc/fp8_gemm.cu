@@ -9,10 +9,10 @@
 // sums, which stay in registers:  acc = fma(sum, sa sb, acc), two values an instruction.  Every shape
 // adds the same products in the same order, so a row's results do not depend on the other rows.
 //
-// 8192 x 7168 x 7168 takes 306 us in bf16, 2.75 PFLOP/s; bound by bringing codes into the SMs, 32 KB a
-// block of K and SM, 83 GB/s: with all sums and scales and three quarters of the MMAs left out it takes
-// 266.  One row of 7168 x 4096 takes 11.1 us, 7.6 and 4.1 with a half and none of K: 4 KB a block from
-// HBM on 128 SMs, 4.3 TB/s.  Warps:
+// 8192 x 7168 x 7168 takes 308 us in bf16, 2.73 PFLOP/s (338 call after call, at the power limit);
+// bound by bringing codes into the SMs, 32 KB a block of K and SM, 83 GB/s: with all sums and scales
+// and three quarters of the MMAs left out it takes 266.  One row of 7168 x 4096 takes 11 us, 7.6 and
+// 4.1 with a half and none of K: 4 KB a block from HBM on 128 SMs, 4.3 TB/s.  Warps:
 //   0..7    sums: lanes 32 (w % 4) .. of TMEM, half w / 4 of the columns; then the output
 //   8       producer: codes by TMA (128-byte swizzle)
 //   9, 10   MMAs, groups of blocks of K in turn: what one spends on waiting, committing and looping
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_fp8_kernel(const __grid_cons
         const Tile t = decode<NT, PAIR>(p, sh, tile);
         const CUtensorMap* ma = &p.mapA[t.box];
         const uint32_t kb_tx = (8u << t.box) * 128u + C::kLocalN * 128u;
-                const int wrow = t.e * p.N + t.n0 + C::kLocalN * rank, arow = t.row0 + 128 * rank;
+        const int wrow = t.e * p.N + t.n0 + C::kLocalN * rank, arow = t.row0 + 128 * rank;
         for (int k0 = 0; k0 < p.kt; k0 += p.ks) {
           if (issued >= S) ok = warp_wait(empty(s), phase, 81);
           if (!ok) break;
@@ -806,7 +806,8 @@ cudaError_t run(Params& p, const uint8_t* a, const uint8_t* b, int K, int sms, c
     }
   if (p.vec) {  // rows start on 16 bytes
     auto enc = reinterpret_cast<Encode>(tensor_map_encoder());
-    const cuuint64_t size = p.f32 ? 4 : 2, dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.rows)};
+    const cuuint64_t size = p.f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.N), static_cast<cuuint64_t>(p.rows)};
     const cuuint64_t strides[1] = {p.N * size};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / size), 32}, ones[2] = {1, 1};
     if (!enc || enc(&p.mapOut, p.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p.out,

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(1024, V == 1 ? 2 : 1)
 // ---- many rows that start on 16 bytes.  Persistent CTAs; the next kAhead rows are on their way to
 // shared memory (cp.async, every thread its own values, so nothing is waited for but the thread's own
 // copies) while a row is normalised.  The weights stay in registers.  16384 x 7168 bf16 with
-// residual and both outputs: 180 us, 5.9 TB/s.
+// residual and both outputs: 168 us, 6.3 TB/s; without the residual 129 us, 4.6 TB/s, bound by issuing.
 constexpr int kAhead = 2;
 // A thread's places: kAhead rows of `tensors` tensors of V segments, 16-byte pieces a CTA apart.
 template <int DT, int V>
@@ -342,7 +342,8 @@ __device__ __forceinline__ Raw8<typename In<DT>::T> grad_out(const Raw8<typename
 
 // A CTA's sums of dy n to its row of `part`; with a row per warp through `sums` [warps][cols].
 template <int V, bool VEC>
-__device__ __forceinline__ void flush_dw(const NormGradArgs& a, const float (&dw)[V][8], float* sums, int w0, int lane) {
+__device__ __forceinline__ void flush_dw(const NormGradArgs& a, const float (&dw)[V][8], float* sums, int w0,
+                                         int lane) {
   if (!a.part) return;
   const bool alone = a.W == 1;
   const int warp = threadIdx.x >> 5;
@@ -434,8 +435,9 @@ __global__ void __launch_bounds__(1024)
 }
 
 // The same with the next rows on their way (as in rmsnorm_stream_kernel): dy, s and dsum are read from
-// shared memory where they are used.  8192 x 4096 bf16 with dsum: 56 us, 4.8 TB/s
-// (the weights' part 4 of them; with three rows ahead an SM holds two CTAs instead of four: 73 us).
+// shared memory where they are used.  8192 x 4096 bf16 with dsum: 51 us, 5.2 TB/s, the second kernel's
+// 4 among them; three rows ahead leave an SM two CTAs instead of four and took 73 us where two took 56.
+// Bound by issuing (71 % of all slots) and by each row's one synchronisation.
 template <int DT, int V>
 __global__ void __launch_bounds__(kStreamThreads, V == 4 ? 1 : 2)
     rmsnorm_backward_stream_kernel(const NormGradArgs a) {
@@ -539,10 +541,12 @@ moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE
 // How rows are cut: segments per warp, warps per row, threads of a CTA (a row, or kAloneWarps rows of
 // one warp each).
 //   kStream  16-bit rows that start on 16 bytes, more of them than SMs: two segments a warp, four beyond
-//            32 segments.  (16384 x 7168 bf16 with residual and both outputs 180 us, 215 as kFew; fp32,
-//            8192 x 4096: 120 us, 94 as kFew, since an SM then holds few rows.)
+//            32 segments.  (16384 x 7168 bf16 with residual and both outputs 168 us, 211 as kFew; the
+//            gradient of 8192 x 4096 51 us, 68 as kFew.  fp32, 8192 x 4096: 120 us, 88 as kFew, since
+//            an SM then holds few rows.)
 //   kFew     others that start on 16 bytes: a row over as many warps as it has segments, up to 32
-//   kAny     rows that do not: the same cut (16384 x 1925 fp32 80 us, 92 with four segments a warp)
+//   kAny     rows that do not: the same cut (16384 x 1925 fp32 58 us, 4.9 TB/s; bf16 60 us, 2.6 TB/s, bound
+//            by one value an instruction)
 enum Path { kStream, kFew, kAny };
 struct Shape {
   int v, W, threads;
@@ -571,7 +575,8 @@ int64_t units(int64_t rows, const Shape& s) { return s.W == 1 ? (rows + kAloneWa
 int64_t walkers(int64_t rows, const Shape& s, size_t smem, int sms) {
   int64_t per_sm = 1024 / s.threads;
   if (per_sm > 16) per_sm = 16;
-  if (smem > 0 && per_sm > static_cast<int64_t>(2 * kMostRing / smem)) per_sm = static_cast<int64_t>(2 * kMostRing / smem);
+  if (smem > 0 && per_sm > static_cast<int64_t>(2 * kMostRing / smem))
+    per_sm = static_cast<int64_t>(2 * kMostRing / smem);
   if (per_sm < 1) per_sm = 1;
   const int64_t n = units(rows, s);
   return n < per_sm * sms ? n : per_sm * sms;
