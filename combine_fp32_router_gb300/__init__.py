@@ -467,9 +467,11 @@ def _arg(t, dev, name, dtype, numel):
     device `dev`; None passes through."""
     if t is None:
         return None
+    dt = t.dtype
+    if dt is dtype and t.get_device() == dev and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError("%s must be a CUDA tensor on the device of the others" % name)
-    dt = t.dtype
     if dt is not dtype and not (type(dtype) is tuple and dt in dtype):
         raise ValueError("%s must hold %s: got %s" % (name, dtype, dt))
     if t.numel() != numel or not t.is_contiguous():
