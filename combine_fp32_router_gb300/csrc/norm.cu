@@ -510,24 +510,41 @@ __global__ void __launch_bounds__(kStreamThreads, V == 4 ? 1 : 2)
                                                                   Ring<DT, V>::kPieces * blockDim.x), w0, lane);
 }
 
-// dw[c] = sum over n partial rows: 32 columns a CTA, each of 32 warps every 32nd row, then the
-// warps' sums in order.
-__global__ void __launch_bounds__(1024) rmsnorm_dweight_kernel(const float* __restrict__ part, int n,
-                                                               int cols, float* __restrict__ dw) {
-  __shared__ float sums[32][33];
+// dw[c] = sum over n partial rows: 32 columns a cluster of C CTAs, whose warps take every C * kSumWarps-th
+// row; the sums of a CTA's warps and then of the CTAs are added in order.  Eight CTAs where all clusters
+// fit the SMs at once, four beyond: the gradient of 2048 x 2048 bf16 takes 13.1 and 14.3 us, of
+// 8192 x 7168 89.7 and 86.4 (15.2 and 86.5 with one CTA of 32 warps).
+constexpr int kSumWarps = 8;
+template <int C>
+__global__ void __cluster_dims__(1, C, 1) __launch_bounds__(32 * kSumWarps)
+    rmsnorm_dweight_kernel(const float* __restrict__ part, int n, int cols, float* __restrict__ dw) {
+  __shared__ float sums[kSumWarps][32];
+  __shared__ uint32_t all[C][32];  // rank 0's: every CTA's
+  cluster_sync_all();  // rank 0 runs: its shared memory can be written
   griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
   const int c = blockIdx.x * 32 + lane;
   float v = 0.0f;
   if (c < cols) {
-#pragma unroll 4
-    for (int r = warp; r < n; r += 32) v += part[static_cast<int64_t>(r) * cols + c];
+#pragma unroll 8
+    for (int r = rank * kSumWarps + warp; r < n; r += C * kSumWarps)
+      v += part[static_cast<int64_t>(r) * cols + c];
   }
   sums[warp][lane] = v;
   __syncthreads();
-  v = warp_sum(sums[lane][warp]);
-  const int o = blockIdx.x * 32 + warp;
-  if (lane == 0 && o < cols) dw[o] = v;
+  if (warp == 0) {
+#pragma unroll
+    for (int i = 1; i < kSumWarps; ++i) v += sums[i][lane];
+    st_shared_cluster_u32(mapa_shared(smem_u32(&all[rank][lane]), 0), __float_as_uint(v));
+  }
+  cluster_sync_all();
+  if (rank == 0 && warp == 0 && c < cols) {
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) v += __uint_as_float(all[i][lane]);
+    dw[c] = v;
+  }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -733,9 +750,12 @@ moe_status_t moe_rmsnorm_backward(const void* dy, const void* s, const void* wei
   cudaError_t st = dtype == MOE_DTYPE_BF16  ? launch_grad<MOE_DTYPE_BF16>(a, path, sh, sms, &ctas, stream)
                    : dtype == MOE_DTYPE_F16 ? launch_grad<MOE_DTYPE_F16>(a, path, sh, sms, &ctas, stream)
                                             : launch_grad<MOE_DTYPE_F32>(a, path, sh, sms, &ctas, stream);
-  if (st == cudaSuccess && dweight)
-    st = launch_pdl(rmsnorm_dweight_kernel, dim3((cols + 31) / 32), dim3(1024), 0, stream,
-                    static_cast<const float*>(ws), ctas, cols, dweight);
+  if (st == cudaSuccess && dweight) {
+    const int groups = (cols + 31) / 32, ctas_per_sm = 2048 / (32 * kSumWarps);
+    const bool eight = groups * 8 <= sms * ctas_per_sm;
+    st = launch_pdl(eight ? rmsnorm_dweight_kernel<8> : rmsnorm_dweight_kernel<4>, dim3(groups, eight ? 8 : 4),
+                    dim3(32 * kSumWarps), 0, stream, static_cast<const float*>(ws), ctas, cols, dweight);
+  }
   return cuda_status(st);
 }
 
