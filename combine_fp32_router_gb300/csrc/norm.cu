@@ -559,8 +559,8 @@ moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE
 // one warp each).
 //   kStream  16-bit rows that start on 16 bytes, more of them than SMs: two segments a warp, four beyond
 //            32 segments.  (16384 x 7168 bf16 with residual and both outputs 168 us, 211 as kFew; the
-//            gradient of 8192 x 4096 51 us, 68 as kFew.  fp32, 8192 x 4096: 120 us, 88 as kFew, since
-//            an SM then holds few rows.)
+//            gradient of 8192 x 4096 51 us, 68 as kFew.  fp32, 8192 x 4096: 120 us, 88 as kFew, the
+//            gradient 148 and 116, since an SM then holds few rows.)
 //   kFew     others that start on 16 bytes: a row over as many warps as it has segments, up to 32
 //   kAny     rows that do not: the same cut (16384 x 1925 fp32 58 us, 4.9 TB/s; bf16 60 us, 2.6 TB/s, bound
 //            by one value an instruction)
