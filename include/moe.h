@@ -419,10 +419,10 @@ moe_status_t moe_quantize_rows_fp8(const void* x, int dtype, int64_t rows, int c
 moe_status_t moe_dequantize_rows_fp8(const uint8_t* q, const float* scales, int64_t rows, int cols,
                                      int dtype, void* out, cudaStream_t stream);
 
-/* Expert weights W [E, K, N] bf16 in 128 x 128 blocks.  transpose = 1: Wq [E, N, Kp] and scales
- * [E, ceil(N / 128), ceil(K / 128)], for products over K (x W); 0: Wq [E, K, Np] and scales
- * [E, ceil(K / 128), ceil(N / 128)], for products over N (dy W^T, the gradient of x).  Both hold
- * the same values.  E <= 1024, K and N <= 2^20. */
+/* Expert weights W [E, K, N] bf16 (16-byte aligned) in 128 x 128 blocks.  transpose = 1: Wq
+ * [E, N, Kp] and scales [E, ceil(N / 128), ceil(K / 128)], for products over K (x W); 0: Wq [E, K, Np]
+ * and scales [E, ceil(K / 128), ceil(N / 128)], for products over N (dy W^T, the gradient of x).  Both
+ * hold the same values.  E <= 1024, K and N <= 2^20. */
 moe_status_t moe_quantize_blocks_fp8(const moe_bf16_t* W, int E, int K, int N, int transpose,
                                      uint8_t* Wq, float* scales, cudaStream_t stream);
 
