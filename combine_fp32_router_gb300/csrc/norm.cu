@@ -305,8 +305,10 @@ struct NormGradArgs {
   int cols, W, w_f32;
 };
 
-// The gradient's sums over eight values: t = dy s (exact for 16-bit types) goes into <t, w>, returned,
-// and with rstd into the columns' sums.
+// The gradient's sums over eight values: n = s rstd first, which is of the order of one whatever the row's
+// size is, so that no sum leaves fp32's range where the gradients do not (sums of dy s,
+// an instruction a pair less and 1 % faster, did for rows of 1e17 with dy of 1e20, or of 1e-16 with 1e-25).
+// <dy n, w> is returned, and dy n goes into the columns' sums.
 template <int DT>
 __device__ __forceinline__ float grad_sums(const Raw8<typename In<DT>::T>& s, const Raw8<typename In<DT>::T>& dy,
                                            const float (&w)[8], float rstd, float (&dw)[8]) {
@@ -314,18 +316,19 @@ __device__ __forceinline__ float grad_sums(const Raw8<typename In<DT>::T>& s, co
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const float2 a = get2<DT>(s, j), d = get2<DT>(dy, j);
-    float t = d.x, u = d.y;
-    mul2(t, u, a.x, a.y);
-    fma2(p, q, t, u, w[j], w[j + 1]);
-    fma2(dw[j], dw[j + 1], t, u, rstd, rstd);
+    float n = a.x, m = a.y;
+    mul2(n, m, rstd, rstd);
+    fma2(dw[j], dw[j + 1], d.x, d.y, n, m);
+    mul2(n, m, d.x, d.y);
+    fma2(p, q, n, m, w[j], w[j + 1]);
   }
   return p + q;
 }
-// What a row's values are subtracted with, from its total <t, w>: rstd^3 total / cols.
+// What a row's n are subtracted with, from its total <dy n, w>.
 __device__ __forceinline__ float grad_factor(float total, float rstd, int cols) {
-  return rstd * (rstd * (rstd * (total / static_cast<float>(cols))));
+  return rstd * (total / static_cast<float>(cols));
 }
-// dx = dsum + dy (rstd w) - s c
+// dx = dsum + dy (rstd w) - n c, n = s rstd
 template <int DT>
 __device__ __forceinline__ Raw8<typename In<DT>::T> grad_out(const Raw8<typename In<DT>::T>& s,
                                                              const Raw8<typename In<DT>::T>& dy, const float (&w)[8],
@@ -334,8 +337,10 @@ __device__ __forceinline__ Raw8<typename In<DT>::T> grad_out(const Raw8<typename
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
     const float2 a = get2<DT>(s, j), d = get2<DT>(dy, j);
-    set2<DT>(o, j, fmaf(-c, a.x, fmaf(d.x, rstd * w[j], dsum[j])),
-             fmaf(-c, a.y, fmaf(d.y, rstd * w[j + 1], dsum[j + 1])));
+    float n0 = a.x, n1 = a.y;
+    mul2(n0, n1, rstd, rstd);
+    set2<DT>(o, j, fmaf(-c, n0, fmaf(d.x, rstd * w[j], dsum[j])),
+             fmaf(-c, n1, fmaf(d.y, rstd * w[j + 1], dsum[j + 1])));
   }
   return o;
 }
@@ -435,7 +440,7 @@ __global__ void __launch_bounds__(1024)
 }
 
 // The same with the next rows on their way (as in rmsnorm_stream_kernel): dy, s and dsum are read from
-// shared memory where they are used.  8192 x 4096 bf16 with dsum: 51 us, 5.2 TB/s, the second kernel's
+// shared memory where they are used.  8192 x 4096 bf16 with dsum: 52 us, 5.2 TB/s, the second kernel's
 // 4 among them; three rows ahead leave an SM two CTAs instead of four and took 73 us where two took 56.
 // Bound by issuing (71 % of all slots) and by each row's one synchronisation.
 template <int DT, int V>
@@ -512,8 +517,8 @@ __global__ void __launch_bounds__(kStreamThreads, V == 4 ? 1 : 2)
 
 // dw[c] = sum over n partial rows: 32 columns a cluster of C CTAs, whose warps take every C * kSumWarps-th
 // row; the sums of a CTA's warps and then of the CTAs are added in order.  Eight CTAs where all clusters
-// fit the SMs at once, four beyond: the gradient of 2048 x 2048 bf16 takes 13.1 and 14.3 us, of
-// 8192 x 7168 89.7 and 86.4 (15.2 and 86.5 with one CTA of 32 warps).
+// fit the SMs at once, four beyond: the gradient of 2048 x 2048 bf16 takes 13.4 and 14.6 us, of
+// 8192 x 7168 91.6 and 88.3 (one CTA of 32 warps: 2 us more than eight of them at 2048 x 2048).
 constexpr int kSumWarps = 8;
 template <int C>
 __global__ void __cluster_dims__(1, C, 1) __launch_bounds__(32 * kSumWarps)
@@ -559,7 +564,7 @@ moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE
 // one warp each).
 //   kStream  16-bit rows that start on 16 bytes, more of them than SMs: two segments a warp, four beyond
 //            32 segments.  (16384 x 7168 bf16 with residual and both outputs 168 us, 211 as kFew; the
-//            gradient of 8192 x 4096 51 us, 68 as kFew.  fp32, 8192 x 4096: 120 us, 88 as kFew, the
+//            gradient of 8192 x 4096 52 us, 69 as kFew.  fp32, 8192 x 4096: 120 us, 88 as kFew, the
 //            gradient 148 and 116, since an SM then holds few rows.)
 //   kFew     others that start on 16 bytes: a row over as many warps as it has segments, up to 32
 //   kAny     rows that do not: the same cut (16384 x 1925 fp32 58 us, 4.9 TB/s; bf16 60 us, 2.6 TB/s, bound

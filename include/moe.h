@@ -476,9 +476,9 @@ moe_status_t moe_rmsnorm(const void* x, int64_t x_stride, const void* residual, 
  *   arrives at sum_out [rows, cols]; all contiguous.  dx may be dy, s or dsum itself.
  * ws: moe_rmsnorm_workspace_bytes(rows, cols) bytes of device memory, 256-byte aligned (0 for
  * unsupported sizes), ordered between calls as for moe_forward; unused without dweight.  rows = 0
- * writes dweight alone (zeros).  Bitwise reproducible on one kind of device.  dy * s is formed in
- * fp32: where it is beyond fp32's range (no 16-bit values of |s| < 1e18 and |dy| < 1e20 are), so are
- * the row's gradients.
+ * writes dweight alone (zeros).  Bitwise reproducible on one kind of device.  n is formed first, so the
+ * size of a row's values does not matter as long as rstd holds it; where a row's sum of |g n| is
+ * beyond fp32, its gradients are infinite or NaN.
  */
 size_t moe_rmsnorm_workspace_bytes(int64_t rows, int cols);
 moe_status_t moe_rmsnorm_backward(const void* dy, const void* s, const void* weight,
