@@ -574,16 +574,31 @@ struct Shape {
   int v, W, threads;
 };
 constexpr int kAloneWarps = 8;
-Shape shape_of(Path path, int cols) {
+constexpr Shape shape_of(Path path, int cols) {
   const int segs = (cols + kSeg - 1) / kSeg;
   const int most = path != kStream ? (segs > 32 ? 2 : 1) : segs > 32 ? 4 : 2;
-  Shape s;
-  s.v = 1;
+  Shape s{1, 0, 0};
   while (s.v < segs && s.v < most) s.v *= 2;
   s.W = (segs + s.v - 1) / s.v;
   s.threads = 32 * (s.W == 1 ? kAloneWarps : s.W);
   return s;
 }
+// Shared memory of the gradient's rows of one warp each: a CTA's sums by column, at most 16 KB beside a
+// stream's ring.  The other kernels' is not asked for beforehand, so it has to stay below 48 KB.
+constexpr size_t sums_bytes(const Shape& s, int cols) {
+  return s.W == 1 ? static_cast<size_t>(kAloneWarps) * cols * 4 : 0;
+}
+constexpr size_t most_sums(Path path) {
+  size_t most = 0;
+  for (int cols = kSeg; cols <= kMaxSegs * kSeg; cols += kSeg) {  // a cut's widest rows
+    const size_t n = sums_bytes(shape_of(path, cols), cols);
+    if (n > most) most = n;
+  }
+  return most;
+}
+constexpr size_t kMostSums = 16384;
+static_assert(most_sums(kStream) <= kMostSums, "");
+static_assert(most_sums(kFew) <= 40960 && most_sums(kAny) <= 40960, "launched without being allowed more");
 constexpr size_t kMostRing = 110000;  // two CTAs share an SM's memory
 size_t ring_bytes(const Shape& s, int tensors) {
   return static_cast<size_t>(kAhead) * tensors * s.v * 16 * s.threads;
@@ -620,7 +635,7 @@ cudaError_t allow_smem(K kern, std::atomic<unsigned long long>& done) {
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (bit == 0ull || !(done.load(std::memory_order_acquire) & bit)) {
     st = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(kMostRing) + 32768);  // and a CTA's sums
+                              static_cast<int>(kMostRing + kMostSums));
     if (st != cudaSuccess) return st;
     done.fetch_or(bit, std::memory_order_release);
   }
@@ -654,7 +669,7 @@ cudaError_t launch_norm(const NormArgs& a, Path path, const Shape& s, int sms, c
 // *ctas: rows of partial sums that the launch leaves in a.part
 template <int DT, int V>
 cudaError_t launch_grad(const NormGradArgs& a, Path path, const Shape& s, int sms, int* ctas, cudaStream_t st) {
-  const size_t sums = s.W == 1 ? static_cast<size_t>(kAloneWarps) * a.cols * 4 : 0;  // <= 32 KB
+  const size_t sums = sums_bytes(s, a.cols);
   const size_t smem = sums + (path == kStream ? ring_bytes(s, a.dsum ? 3 : 2) : 0);
   *ctas = static_cast<int>(walkers(a.rows, s, smem, sms));
   const dim3 grid(static_cast<unsigned>(*ctas)), block(s.threads);
