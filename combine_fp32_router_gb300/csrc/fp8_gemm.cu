@@ -9,9 +9,10 @@
 // sums, which stay in registers:  acc = fma(sum, sa sb, acc), two values an instruction.  Every shape
 // adds the same products in the same order, so a row's results do not depend on the other rows.
 //
-// 8192 x 7168 x 7168 takes 308 us in bf16, 2.73 PFLOP/s (338 call after call, at the power limit);
-// bound by bringing codes into the SMs, 32 KB a block of K and SM, 83 GB/s: with all sums and scales
-// and three quarters of the MMAs left out it takes 266.  One row of 7168 x 4096 takes 11 us, 7.6 and
+// 8192 x 7168 x 7168 takes 308 to 314 us in bf16, 2.7 PFLOP/s (335 call after call, at the power limit):
+// twelve rounds of tiles, 32 KB a block of K into each SM, 71 GB/s.  With all sums and scales and three
+// quarters of the MMAs left out it takes 266, 83 GB/s: most of it is bringing codes into the SMs, and 42
+// us are sums and the MMAs' hand-over that no load covers.  One row of 7168 x 4096 takes 11 us, 7.6 and
 // 4.1 with a half and none of K: 4 KB a block from HBM on 128 SMs, 4.3 TB/s.  Warps:
 //   0..7    sums: lanes 32 (w % 4) .. of TMEM, half w / 4 of the columns; then the output
 //   8       producer: codes by TMA (128-byte swizzle)
@@ -254,8 +255,8 @@ __device__ __forceinline__ void store_tile(const Params& p, int row, int col, co
 
 // The same for rows that start anywhere.  fp32: a row at a time.  bf16: eight lanes take a row, its
 // 16-byte pieces where its place in memory has them, and value by value the 16 bytes before the first
-// and behind the last of them.  8192 x 7161 x 2048: bf16 128 us, fp32 144, both 164 with 16 columns at a
-// time as in store16; bf16 a row at a time in words of two: 182 (7168 columns, by TMA: 101 and 121).
+// and behind the last of them.  8192 x 7161 x 2048: bf16 134 us, fp32 144, both 164 with 16 columns at a
+// time as in store16; bf16 a row at a time in words of two: 182 (7168 columns, by TMA: 102 and 121).
 template <int W>
 __device__ __forceinline__ void store_rows(const Params& p, int64_t row, int n, int col, const float* acc,
                                            uint32_t buf, int lane) {

@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(1024)
 // The same with the next rows on their way (as in rmsnorm_stream_kernel): dy, s and dsum are read from
 // shared memory where they are used.  8192 x 4096 bf16 with dsum: 52 us, 5.2 TB/s, the second kernel's
 // 4 among them; three rows ahead leave an SM two CTAs instead of four and took 73 us where two took 56.
-// Bound by issuing (71 % of all slots) and by each row's one synchronisation.
+// Bound by issuing (68 % of all slots) and by each row's one synchronisation.
 template <int DT, int V>
 __global__ void __launch_bounds__(kStreamThreads, V == 4 ? 1 : 2)
     rmsnorm_backward_stream_kernel(const NormGradArgs a) {

@@ -383,10 +383,12 @@ moe_status_t moe_forward_few_fp4(const moe_bf16_t* x, float* logits, const float
 
 /* ---------------------------------------------------------------------------------------
  * Around 8-bit experts: rows and weights with a scale per 128 values, their product, the norm
- * before the layer, and tokens sorted by expert and back, each with the gradient that training
- * needs.  moe_rmsnorm gives 8-bit rows, moe_sort_tokens lays them out by expert, moe_gemm_fp8
- * multiplies them by the experts' weights, moe_quantize_rows_fp8 (swiglu) makes the second
- * product's rows of the first one's, and moe_unsort_tokens brings the experts' rows back.
+ * before the layer, and tokens sorted by expert and back.  moe_rmsnorm gives 8-bit rows,
+ * moe_sort_tokens lays them out by expert, moe_gemm_fp8 multiplies them by the experts' weights,
+ * moe_quantize_rows_fp8 (swiglu) makes the second product's rows of the first one's, and
+ * moe_unsort_tokens brings the experts' rows back.  Gradients: of the norm, of a product's rows
+ * (the product with the weights in their other order) and of both ways of sorting.  SwiGLU's gradient
+ * and the experts' weights' are not here: neither has a call on sorted rows.
  *
  * Format of a matrix of R rows and C columns: Kp = C rounded up to a multiple of 128.
  *   codes  [R, Kp] E4M3 bytes (largest value 448); quantisers write zero codes past C.
@@ -498,8 +500,8 @@ moe_status_t moe_rmsnorm_backward(const void* dy, const void* s, const void* wei
  *            without a pair are left as they were.  n_rows >= moe_sort_rows_bound(T, k, E).
  *   counts [E], perm [n_rows] (the pair of a row, -1 for none), pos [T, k] (the row of a pair, -1)
  * k <= 16, E <= 1024, T k + 128 (E + 1) < 2^31, row_bytes and n_scales <= 2^20.  T = 0 writes
- * counts and perm.  ws: moe_sort_workspace_bytes(T, E, k) bytes (0 for unsupported sizes), 256-byte
- * aligned, ordered between calls as for moe_forward; its error word, which the call clears first,
+ * counts and perm.  ws: moe_sort_workspace_bytes(T, E, k) bytes (E before k, as in the other
+ * workspaces' sizes, where moe_sort_rows_bound has k before E; 0 for unsupported sizes), 256-byte aligned, ordered between calls as for moe_forward; its error word, which the call clears first,
  * is read with moe_get_error.  Bitwise reproducible.
  */
 int64_t moe_sort_rows_bound(int64_t T, int k, int E);
@@ -519,7 +521,9 @@ moe_status_t moe_sort_tokens_backward(const void* drows, int dtype, int64_t n_ro
  * -1 adds nothing (a token without any row gets zeros); others outside [0, n_rows) count as -1 and
  * record MOE_ERR_DEVICE_BOUNDS in the 16-byte error word err_word (device memory, e.g. the start of
  * a workspace of moe_sort_tokens; not cleared; read with moe_get_error).  d <= 65536, k <= 16.
- * T = 0 writes nothing.  Each token's results are bitwise independent of the others.
+ * T = 0 writes nothing.  Each token's results are bitwise independent of the others.  (moe_combine is the
+ * expert-parallel layer's own last step, bf16 alone, where every pair has a row: a position outside
+ * reads row 0 there.  Rows of moe_sort_tokens, where pairs may have none, come back with this one.)
  */
 moe_status_t moe_unsort_tokens(const void* rows, int dtype, int64_t n_rows, const float* gate,
                                const int32_t* pos, int64_t T, int k, int d, void* out,
@@ -644,8 +648,8 @@ moe_status_t moe_probe_dram_read(const void* buf, size_t bytes, int ctas, int mo
                                  uint32_t* out, cudaStream_t stream);
 
 /* Synchronises `stream`, reads the device error word of `ws` and returns it (MOE_OK when
- * no device-side problem was recorded since the last moe_route_dispatch / moe_forward on
- * this ws, which clear it).  Returns MOE_ERR_CUDA if the stream reports an error. */
+ * no device-side problem was recorded since the last moe_route_dispatch / moe_forward /
+ * moe_sort_tokens on this ws, which clear it).  Returns MOE_ERR_CUDA if the stream reports an error. */
 moe_status_t moe_get_error(const void* ws, cudaStream_t stream);
 
 /* Upper bound, in nanoseconds, of every device-side wait of kernels launched after this
